@@ -59,8 +59,10 @@ typedef enum {
   PGG_DEV_GROUP_SUM = 2,            /* sum(group_list) != M; detail = the sum (clamped to >= 0) */
   PGG_DEV_INDEX_RANGE = 3,          /* expanded_row_idx[t] outside [0, M); detail = t */
   PGG_DEV_INDEX_DUP = 4,            /* expanded_row_idx is not a permutation; detail = a repeated value */
-  PGG_DEV_EXPERT_RANGE = 5          /* pgg_moe_routing: an expert id outside [0, experts);
+  PGG_DEV_EXPERT_RANGE = 5,         /* pgg_moe_routing: an expert id outside [0, experts);
                                        detail = the smallest such position */
+  PGG_DEV_ADAPTER_RANGE = 6         /* pgg_lora_fwd: an adapter id >= adapters; detail = the
+                                       smallest such token */
 } pgg_device_error;
 
 /*
@@ -159,7 +161,8 @@ pgg_status pgg_moe_dx_noalloc(const pgg_moe_dx_desc* desc, const void* grad_y, c
 
 /*
  * Read the device error word of the last pgg_moe_dx (or pgg_moe_fwd,
- * pgg_moe_dw, pgg_moe_routing, pgg_moe_unpermute[_grad]) that used `workspace`.
+ * pgg_moe_dw, pgg_moe_routing, pgg_moe_unpermute[_grad], pgg_moe_glu[_grad],
+ * pgg_lora_fwd) that used `workspace`.
  * Synchronises `stream`.  Reads the workspace's first 64 bytes (the error
  * word's region), which every workspace of those calls holds.  *code
  * receives a pgg_device_error; *detail its detail value (may be NULL).  When several violations exist, the one with
@@ -435,6 +438,161 @@ pgg_status pgg_moe_unpermute_grad(const pgg_moe_unpermute_desc* desc, const void
                                   const void* grad, const int64_t* expanded_row_idx,
                                   const void* probs, void* perm_grad, void* probs_grad,
                                   void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The router's gate: from a token's logits the topk experts it goes to, their
+ * weights, and the log-sum-exp of the row (for the gradient and for a penalty
+ * on it).  fp32 arithmetic whatever the logits' type.
+ *
+ *   logits      [tokens, experts]  dtype                            input
+ *   bias        [experts]          float32, or NULL                 input
+ *   expert_ids  [tokens, topk]     int64, distinct within a token   output
+ *   probs       [tokens, topk]     float32                          output
+ *   lse         [tokens]           float32, may be NULL             output
+ *
+ * expert_ids holds the experts of the topk largest logit + bias, larger first
+ * and equal ones by lower index (the bias balances the choice and enters
+ * nothing else).  probs[t, j] = scale * exp(logits[t, e_j] - lse[t]) with
+ * renorm == 0; with renorm == 1 scale * the softmax over the chosen logits
+ * alone.
+ * A logit of -inf excludes an expert: it is chosen only after all others, with
+ * weight 0; in a row of -inf the choice is experts 0..topk-1, all weights are
+ * 0 and lse is -inf.  NaN counts as larger than any number, and a NaN or +inf
+ * logit makes lse and every weight it enters NaN.
+ * Limits: topk <= experts <= 8192 and topk <= PGG_GATE_MAX_TOPK.  No
+ * workspace; asynchronous; one kernel.  No output may alias an input.
+ */
+#define PGG_GATE_MAX_TOPK 64
+typedef struct {
+  int64_t tokens, experts, topk;
+  float scale;
+  int32_t renorm;          /* 0 or 1 */
+  int32_t dtype;           /* pgg_dtype of logits and grad_logits */
+  int32_t reserved;        /* must be 0 */
+} pgg_moe_gate_desc;
+
+pgg_status pgg_moe_gate(const pgg_moe_gate_desc* desc, const void* logits, const float* bias,
+                        int64_t* expert_ids, float* probs, float* lse, hipStream_t stream);
+
+/*
+ * Gradient of the gate with respect to the logits (the choice is constant):
+ * from grad_probs [tokens, topk] float32 and, unless NULL, grad_lse [tokens]
+ * float32, with d_j = scale * grad_probs_j and p = exp(logits - lse),
+ *
+ *   renorm 0: grad_logits_e = p_e * (sum_{j: e_j = e} d_j - sum_j d_j p_{e_j}) + grad_lse p_e
+ *   renorm 1: u = softmax of the chosen logits:
+ *             grad_logits_{e_j} = u_j * (d_j - sum_m d_m u_m), plus grad_lse p_e for every e
+ *
+ * logits, lse and expert_ids are pgg_moe_gate's; every element of grad_logits
+ * [tokens, experts] (dtype) is written.  A row of -inf gets zeros.  An id
+ * outside [0, experts) selects nothing.  No workspace; one kernel.
+ */
+pgg_status pgg_moe_gate_grad(const pgg_moe_gate_desc* desc, const void* logits, const float* lse,
+                             const int64_t* expert_ids, const float* grad_probs, const float* grad_lse,
+                             void* grad_logits, hipStream_t stream);
+
+/*
+ * Gated product of the experts (the first half of a gated feed-forward layer):
+ *
+ *   (gate | up)[i, :] = x[p(i) / topK, :] * W[g(i)]      2F columns: gate, then up
+ *   h[i, f]           = act(gate[i, f]) * up[i, f]
+ *
+ * for the expanded rows i, with p(i) and g(i) as for pgg_moe_fwd, whose
+ * descriptor fields and constraints these are; weight_cols = 2F is even.
+ *
+ *   x [batch, K] dtype, weight [G, K, 2F] dtype, expanded_row_idx [M] int64,
+ *   group_list [G] int64                                            inputs
+ *   h        [M, F]   dtype                                         output
+ *   gate_up  [M, 2F]  dtype, may be NULL: the products, for pgg_moe_glu_grad
+ *
+ * fp32 accumulation; h comes from the unrounded products and is rounded once.
+ * Errors, alignment and workspace rules are pgg_moe_fwd's.
+ */
+typedef enum { PGG_ACT_SILU = 0, PGG_ACT_GELU_TANH = 1 } pgg_act;
+
+typedef struct {
+  int64_t x_rows, x_cols;
+  int64_t weight_groups, weight_rows, weight_cols;
+  int64_t idx_len;
+  int64_t group_list_len;
+  int64_t batch, topk;
+  int32_t row_idx_type;
+  int32_t x_dtype;        /* pgg_dtype of x, h and gate_up */
+  int32_t weight_dtype;   /* must equal x_dtype */
+  int32_t act;            /* pgg_act */
+} pgg_moe_glu_desc;
+
+pgg_status pgg_moe_glu_workspace_size(const pgg_moe_glu_desc* desc, size_t* bytes);
+pgg_status pgg_moe_glu(const pgg_moe_glu_desc* desc, const void* x, const void* weight,
+                       const int64_t* expanded_row_idx, const int64_t* group_list, void* h, void* gate_up,
+                       void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradient through the gated product, fused behind the gradient of the
+ * expert's second matrix (h * W2[g], W2 [G, F, D]):
+ *
+ *   dh[i, f] = sum_d grad_y[i, d] * W2[g(i), f, d]
+ *   grad_gate_up[i, f]     = dh * up * act'(gate)
+ *   grad_gate_up[i, F + f] = dh * act(gate)
+ *   h[i, f]                = act(gate) * up     (recomputed, for the gradient of W2)
+ *
+ *   grad_y [M, D], weight = W2 [G, F, D], gate_up [M, 2F] (pgg_moe_glu's), all
+ *   dtype, group_list [G] int64                                     inputs
+ *   grad_gate_up [M, 2F] dtype                                      output
+ *   h            [M, F]  dtype, may be NULL                         output
+ *
+ * Rows are in expanded (expert-grouped) order.  The gradients that remain are
+ * pgg_moe_dx and pgg_moe_dw with grad_gate_up, and pgg_moe_dw with h and
+ * grad_y.  fp32 accumulation, one rounding.  Workspace: O(M + G) integers;
+ * group_list is checked on the device (PGG_DEV_GROUP_NEGATIVE / _SUM; the
+ * outputs are then unspecified).
+ */
+typedef struct {
+  int64_t grad_y_rows, grad_y_cols;
+  int64_t weight_groups, weight_rows, weight_cols;
+  int64_t group_list_len;
+  int32_t grad_y_dtype;   /* pgg_dtype of grad_y, gate_up and the outputs */
+  int32_t weight_dtype;   /* must equal grad_y_dtype */
+  int32_t act;            /* pgg_act */
+  int32_t reserved;       /* must be 0 */
+} pgg_moe_glu_grad_desc;
+
+pgg_status pgg_moe_glu_grad_workspace_size(const pgg_moe_glu_grad_desc* desc, size_t* bytes);
+pgg_status pgg_moe_glu_grad(const pgg_moe_glu_grad_desc* desc, const void* grad_y, const void* weight,
+                            const void* gate_up, const int64_t* group_list, void* grad_gate_up, void* h,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * A shared projection with low-rank adapters of many requests beside it:
+ *
+ *   y[t, :] = x[t, :] * W + scales[p] * (x[t, :] * A_p^T) * B_p,   p = adapter_ids[t]
+ *
+ *   x [tokens, K], weight = W [K, N], a [adapters, rank, K], b [adapters,
+ *   rank, N], all dtype; adapter_ids [tokens] int64; scales [adapters] float32
+ *   y [tokens, N] dtype                                             output
+ *
+ * Tokens come in any order; a negative id means no adapter.  An id >= adapters
+ * sets the workspace error word (PGG_DEV_ADAPTER_RANGE) and leaves y
+ * unspecified.  Adapters of smaller rank are padded with zero rows.  A token's
+ * row depends on its own x and adapter only, whatever values other adapters
+ * hold.  fp32 accumulation; the inner product x * A_p^T stays in fp32; one
+ * rounding.  Limit: rank <= PGG_LORA_MAX_RANK.  The workspace holds tokens x
+ * rank floats and, with few tokens, fp32 partial results (at most 64 x tokens
+ * x N floats, and at most about 512 tiles' worth).  Its rules are
+ * pgg_moe_fwd's.
+ */
+#define PGG_LORA_MAX_RANK 1024
+typedef struct {
+  int64_t tokens, in_features, out_features;   /* tokens, K, N */
+  int64_t adapters, rank;
+  int32_t dtype;           /* pgg_dtype of x, weight, a, b and y */
+  int32_t reserved;        /* must be 0 */
+} pgg_lora_desc;
+
+pgg_status pgg_lora_workspace_size(const pgg_lora_desc* desc, size_t* bytes);
+pgg_status pgg_lora_fwd(const pgg_lora_desc* desc, const void* x, const void* weight, const void* a, const void* b,
+                        const int64_t* adapter_ids, const float* scales, void* y, void* workspace,
+                        size_t workspace_bytes, hipStream_t stream);
 
 const char* pgg_status_string(pgg_status status);
 const char* pgg_device_error_string(int32_t code);

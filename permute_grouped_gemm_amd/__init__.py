@@ -27,6 +27,18 @@ expert), float32 [G, K, N], and
 
 is MoeInitRouting on the device (§1.1 step 1): the routing tables (and the
 permuted x) from the router's choices.
+
+    expert_ids, probs, lse = moe_gate(logits, topk)
+    h, gate_up = moe_glu(x, weight, expanded_row_idx, group_list, topk, save_gate_up=True)
+
+are the router in front of it (top-k softmax gate) and the experts' gated
+product, act(x·Wgate) * (x·Wup), with moe_gate_grad and moe_glu_grad as their
+gradients, and
+
+    y = lora_fwd(x, weight, a, b, adapter_ids, scales)
+
+is a projection that all tokens share with a low-rank adapter per token
+beside it.
 """
 from __future__ import annotations
 
@@ -41,7 +53,8 @@ __all__ = [
     "moe_dx", "moe_dx_noalloc", "workspace_size", "plan", "read_device_error", "debug_tables", "debug_tiles",
     "moe_fwd", "fwd_workspace_size", "fwd_plan", "fwd_kernel_time",
     "moe_dw", "dw_workspace_size", "dw_kernel_time", "moe_routing", "moe_unpermute",
-    "moe_unpermute_grad",
+    "moe_unpermute_grad", "moe_gate", "moe_gate_grad", "moe_glu", "glu_workspace_size", "moe_glu_grad",
+    "glu_grad_workspace_size", "lora_fwd", "lora_workspace_size",
     "KernelTimer", "PggError", "lib", "LIB_PATH", "HEADER_PATH",
 ]
 
@@ -50,8 +63,10 @@ LIB_PATH = os.path.join(PKG, "libpgg.so")
 HEADER_PATH = os.path.join(os.path.dirname(PKG), "include", "pgg.h")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE_TOO_SMALL, ERR_HIP, ERR_MISALIGNED = range(6)
-DEV_OK, DEV_GROUP_NEGATIVE, DEV_GROUP_SUM, DEV_INDEX_RANGE, DEV_INDEX_DUP, DEV_EXPERT_RANGE = range(6)
+(DEV_OK, DEV_GROUP_NEGATIVE, DEV_GROUP_SUM, DEV_INDEX_RANGE, DEV_INDEX_DUP, DEV_EXPERT_RANGE,
+ DEV_ADAPTER_RANGE) = range(7)
 DTYPE_CODE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+ACT_CODE = {"silu": 0, "gelu_tanh": 1}
 
 
 class Desc(ctypes.Structure):
@@ -88,6 +103,43 @@ class UnpermuteDesc(ctypes.Structure):
         ("batch", ctypes.c_int64), ("topk", ctypes.c_int64), ("hidden", ctypes.c_int64),
         ("row_idx_type", ctypes.c_int32), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
         ("pad", ctypes.c_int32),
+    ]
+
+
+class GateDesc(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int64), ("experts", ctypes.c_int64), ("topk", ctypes.c_int64),
+        ("scale", ctypes.c_float), ("renorm", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class GluDesc(ctypes.Structure):
+    _fields_ = [
+        ("x_rows", ctypes.c_int64), ("x_cols", ctypes.c_int64),
+        ("weight_groups", ctypes.c_int64), ("weight_rows", ctypes.c_int64),
+        ("weight_cols", ctypes.c_int64), ("idx_len", ctypes.c_int64),
+        ("group_list_len", ctypes.c_int64), ("batch", ctypes.c_int64), ("topk", ctypes.c_int64),
+        ("row_idx_type", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
+        ("weight_dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+    ]
+
+
+class GluGradDesc(ctypes.Structure):
+    _fields_ = [
+        ("grad_y_rows", ctypes.c_int64), ("grad_y_cols", ctypes.c_int64),
+        ("weight_groups", ctypes.c_int64), ("weight_rows", ctypes.c_int64),
+        ("weight_cols", ctypes.c_int64), ("group_list_len", ctypes.c_int64),
+        ("grad_y_dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32),
+        ("act", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
+
+
+class LoraDesc(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int64), ("in_features", ctypes.c_int64), ("out_features", ctypes.c_int64),
+        ("adapters", ctypes.c_int64), ("rank", ctypes.c_int64), ("dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
     ]
 
 
@@ -157,6 +209,18 @@ def lib():
         L.pgg_moe_unpermute_workspace_size.argtypes = [PU, ctypes.POINTER(sz)]
         L.pgg_moe_unpermute.argtypes = [PU, vp, vp, vp, vp, vp, sz, vp]
         L.pgg_moe_unpermute_grad.argtypes = [PU, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        PG = ctypes.POINTER(GateDesc)
+        L.pgg_moe_gate.argtypes = [PG, vp, vp, vp, vp, vp, vp]
+        L.pgg_moe_gate_grad.argtypes = [PG, vp, vp, vp, vp, vp, vp, vp]
+        PL = ctypes.POINTER(GluDesc)
+        L.pgg_moe_glu_workspace_size.argtypes = [PL, ctypes.POINTER(sz)]
+        L.pgg_moe_glu.argtypes = [PL, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        PLG = ctypes.POINTER(GluGradDesc)
+        L.pgg_moe_glu_grad_workspace_size.argtypes = [PLG, ctypes.POINTER(sz)]
+        L.pgg_moe_glu_grad.argtypes = [PLG, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        PA = ctypes.POINTER(LoraDesc)
+        L.pgg_lora_workspace_size.argtypes = [PA, ctypes.POINTER(sz)]
+        L.pgg_lora_fwd.argtypes = [PA, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.pgg_timing_begin.argtypes = [i32]
         L.pgg_timing_end.argtypes = [ctypes.POINTER(KernelTime), i32, ctypes.POINTER(i32)]
         L.pgg_status_string.argtypes = [ctypes.c_int]
@@ -170,7 +234,9 @@ def lib():
                   "pgg_moe_fwd_plan", "pgg_moe_fwd_kernel_time", "pgg_moe_dw_workspace_size",
                   "pgg_moe_dw", "pgg_moe_dw_kernel_time", "pgg_moe_routing_workspace_size",
                   "pgg_moe_routing", "pgg_moe_unpermute_workspace_size", "pgg_moe_unpermute",
-                  "pgg_moe_unpermute_grad",
+                  "pgg_moe_unpermute_grad", "pgg_moe_gate", "pgg_moe_gate_grad",
+                  "pgg_moe_glu_workspace_size", "pgg_moe_glu", "pgg_moe_glu_grad_workspace_size",
+                  "pgg_moe_glu_grad", "pgg_lora_workspace_size", "pgg_lora_fwd",
                   "pgg_timing_begin", "pgg_timing_end"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
@@ -701,6 +767,242 @@ def moe_unpermute_grad(grad: torch.Tensor, expanded_row_idx: torch.Tensor, batch
                                       ptr(probs_grad), ws.data_ptr(), _ws_bytes(ws), _stream_handle(stream))
     _check(st, "pgg_moe_unpermute_grad")
     return perm_grad, probs_grad
+
+
+# ---------------------------------------------------------------- gate, gated products, adapters
+
+def _expect(t, name, shape, dtype, dev):
+    """t: a contiguous GPU tensor of this shape and dtype on dev."""
+    if t.dtype != dtype or t.device != dev or not t.is_cuda or t.shape != shape or not t.is_contiguous():
+        raise PggError(ERR_INVALID_ARG, f"{name} must be a contiguous {dtype} {list(shape)} tensor on {dev}")
+
+
+def _value_type(t, name, dim):
+    """dtype code of t: a contiguous float32 / float16 / bfloat16 GPU tensor of `dim` dimensions."""
+    code = DTYPE_CODE.get(t.dtype)
+    if code is None or t.dim() != dim or not t.is_cuda or not t.is_contiguous():
+        raise PggError(ERR_INVALID_ARG, f"{name} must be a contiguous {dim}-dimensional float32, float16 or "
+                                        "bfloat16 GPU tensor")
+    return code
+
+
+def _on_stream(stream, dev):
+    """Handle of ``stream``, or of the current stream of ``dev``."""
+    return int((torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream)
+
+
+def _fresh(shape, dtype, dev, stream):
+    """A new tensor that a kernel on ``stream`` uses: its memory is not handed
+    out again before that stream has passed the point where it was freed."""
+    t = torch.empty(shape, dtype=dtype, device=dev)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _out(t, name, shape, dtype, dev, stream):
+    if t is None:
+        return _fresh(shape, dtype, dev, stream)
+    _expect(t, name, shape, dtype, dev)
+    return t
+
+
+def _scratch(workspace, size, dev, stream):
+    if workspace is None:
+        return _fresh(size(), torch.uint8, dev, stream)
+    if not workspace.is_cuda:
+        raise PggError(ERR_INVALID_ARG, "workspace must be a GPU tensor")
+    _check_workspace(workspace, dev)
+    return workspace
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _act_code(act):
+    if act not in ACT_CODE:
+        raise PggError(ERR_INVALID_ARG, f"act must be one of {sorted(ACT_CODE)}")
+    return ACT_CODE[act]
+
+
+def _size_of(query, d, where):
+    n = ctypes.c_size_t()
+    _check(query(ctypes.byref(d), ctypes.byref(n)), where)
+    return n.value
+
+
+def moe_gate(logits: torch.Tensor, topk: int, *, bias: Optional[torch.Tensor] = None, renorm: bool = False,
+             scale: float = 1.0, stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """The router's gate: (expert_ids [T, topk] int64, probs [T, topk] float32,
+    lse [T] float32) from logits [T, E] (asynchronous).
+
+    The experts are those of the topk largest ``logits + bias``, larger first,
+    equal ones by lower index; ``bias`` [E] float32 enters the choice only.
+    probs = scale * softmax(logits) at the chosen experts, or with ``renorm``
+    scale * the softmax over the chosen logits.  A logit of -inf excludes an
+    expert: it comes after all others and gets weight 0; a row of -inf gets
+    experts 0..topk-1, weights 0 and lse -inf.  Limits: E <= 8192, topk <= 64."""
+    code = _value_type(logits, "logits", 2)
+    T, E = logits.shape
+    dev = logits.device
+    if bias is not None:
+        _expect(bias, "bias", (E,), torch.float32, dev)
+    k = int(topk)
+    d = GateDesc(T, E, k, float(scale), int(bool(renorm)), code, 0)
+    if T <= 0 or not 0 < k <= E:
+        raise PggError(ERR_INVALID_ARG, "moe_gate needs tokens and 0 < topk <= experts")
+    ids = _fresh((T, k), torch.int64, dev, stream)
+    probs = _fresh((T, k), torch.float32, dev, stream)
+    lse = _fresh((T,), torch.float32, dev, stream)
+    _check(lib().pgg_moe_gate(ctypes.byref(d), logits.data_ptr(), _ptr(bias), ids.data_ptr(), probs.data_ptr(),
+                              lse.data_ptr(), _on_stream(stream, dev)), "pgg_moe_gate")
+    return ids, probs, lse
+
+
+def moe_gate_grad(logits: torch.Tensor, lse: torch.Tensor, expert_ids: torch.Tensor, grad_probs: torch.Tensor, *,
+                  grad_lse: Optional[torch.Tensor] = None, renorm: bool = False, scale: float = 1.0,
+                  out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of moe_gate: grad_logits [T, E] in logits' dtype from grad_probs
+    [T, topk] float32 and optionally grad_lse [T] float32.  ``lse`` and
+    ``expert_ids`` are moe_gate's, ``renorm`` and ``scale`` its arguments."""
+    code = _value_type(logits, "logits", 2)
+    T, E = logits.shape
+    dev = logits.device
+    if expert_ids.dim() != 2:
+        raise PggError(ERR_INVALID_ARG, "expert_ids must be an int64 [tokens, topk] tensor")
+    k = expert_ids.shape[1]
+    _expect(expert_ids, "expert_ids", (T, k), torch.int64, dev)
+    _expect(grad_probs, "grad_probs", (T, k), torch.float32, dev)
+    _expect(lse, "lse", (T,), torch.float32, dev)
+    if grad_lse is not None:
+        _expect(grad_lse, "grad_lse", (T,), torch.float32, dev)
+    d = GateDesc(T, E, k, float(scale), int(bool(renorm)), code, 0)
+    out = _out(out, "out", (T, E), logits.dtype, dev, stream)
+    _check(lib().pgg_moe_gate_grad(ctypes.byref(d), logits.data_ptr(), lse.data_ptr(), expert_ids.data_ptr(),
+                                   grad_probs.data_ptr(), _ptr(grad_lse), out.data_ptr(),
+                                   _on_stream(stream, dev)), "pgg_moe_gate_grad")
+    return out
+
+
+def _glu_desc(x, weight, eri, group_list, topk, row_idx_type, act) -> GluDesc:
+    code = _value_type(x, "x", 2)
+    _value_type(weight, "weight", 3)
+    dev = x.device
+    if weight.device != dev:
+        raise PggError(ERR_INVALID_ARG, "inputs must be contiguous tensors on one GPU")
+    batch, (G, K, C) = x.shape[0], weight.shape
+    _expect(eri, "expanded_row_idx", (batch * int(topk),), torch.int64, dev)
+    _expect(group_list, "group_list", (G,), torch.int64, dev)
+    return GluDesc(batch, x.shape[1], G, K, C, eri.shape[0], G, batch, int(topk), int(row_idx_type), code,
+                   DTYPE_CODE[weight.dtype], _act_code(act))
+
+
+def glu_workspace_size(x, weight, expanded_row_idx, group_list, topk, row_idx_type=0) -> int:
+    d = _glu_desc(x, weight, expanded_row_idx, group_list, topk, row_idx_type, "silu")
+    return _size_of(lib().pgg_moe_glu_workspace_size, d, "glu_workspace_size")
+
+
+def moe_glu(x: torch.Tensor, weight: torch.Tensor, expanded_row_idx: torch.Tensor, group_list: torch.Tensor,
+            topk: int, row_idx_type: int = 0, *, act: str = "silu", save_gate_up: bool = False,
+            out: Optional[torch.Tensor] = None, gate_up: Optional[torch.Tensor] = None,
+            workspace: Optional[torch.Tensor] = None, stream=None):
+    """The experts' gated product: h [M, F] = act(gate) * up in x's dtype, with
+    (gate | up) = the expanded rows of x times weight [G, K, 2F] (gate columns
+    first), in expanded row order (asynchronous).  With ``save_gate_up`` (or a
+    ``gate_up`` [M, 2F] to fill) returns (h, gate_up), as moe_glu_grad needs it.
+
+    x [batch, K] and weight share one of float32 / float16 / bfloat16;
+    expanded_row_idx [batch*topk] and group_list [G] are int64, as for moe_fwd.
+    ``act``: "silu" or "gelu_tanh"."""
+    d = _glu_desc(x, weight, expanded_row_idx, group_list, topk, row_idx_type, act)
+    dev, M, C = x.device, d.batch * d.topk, d.weight_cols
+    ws = _scratch(workspace, lambda: _size_of(lib().pgg_moe_glu_workspace_size, d, "glu_workspace_size"), dev, stream)
+    out = _out(out, "out", (M, C // 2), x.dtype, dev, stream)
+    if save_gate_up or gate_up is not None:
+        gate_up = _out(gate_up, "gate_up", (M, C), x.dtype, dev, stream)
+    _check(lib().pgg_moe_glu(ctypes.byref(d), x.data_ptr(), weight.data_ptr(), expanded_row_idx.data_ptr(),
+                             group_list.data_ptr(), out.data_ptr(), _ptr(gate_up), ws.data_ptr(), _ws_bytes(ws),
+                             _on_stream(stream, dev)), "pgg_moe_glu")
+    return out if gate_up is None else (out, gate_up)
+
+
+def _glu_grad_desc(grad_y, weight, gate_up, group_list, act) -> GluGradDesc:
+    code = _value_type(grad_y, "grad_y", 2)
+    _value_type(weight, "weight", 3)
+    dev, M, (G, F, D) = grad_y.device, grad_y.shape[0], weight.shape
+    if weight.device != dev:
+        raise PggError(ERR_INVALID_ARG, "inputs must be contiguous tensors on one GPU")
+    _expect(gate_up, "gate_up", (M, 2 * F), grad_y.dtype, dev)
+    _expect(group_list, "group_list", (G,), torch.int64, dev)
+    return GluGradDesc(M, grad_y.shape[1], G, F, D, G, code, DTYPE_CODE[weight.dtype], _act_code(act), 0)
+
+
+def glu_grad_workspace_size(grad_y, weight, gate_up, group_list) -> int:
+    d = _glu_grad_desc(grad_y, weight, gate_up, group_list, "silu")
+    return _size_of(lib().pgg_moe_glu_grad_workspace_size, d, "glu_grad_workspace_size")
+
+
+def moe_glu_grad(grad_y: torch.Tensor, weight: torch.Tensor, gate_up: torch.Tensor, group_list: torch.Tensor, *,
+                 act: str = "silu", want_h: bool = True, out: Optional[torch.Tensor] = None,
+                 h: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradient through the gated product, fused behind the gradient of the
+    experts' second matrix: (grad_gate_up [M, 2F], h [M, F] or None) from grad_y
+    [M, D] (the gradient of h · weight[g]), weight [G, F, D] and moe_glu's
+    gate_up [M, 2F], all in expanded row order and one dtype.  h is recomputed
+    for the second matrix's gradient; the others are moe_dx and moe_dw with
+    grad_gate_up."""
+    d = _glu_grad_desc(grad_y, weight, gate_up, group_list, act)
+    dev, M, F = grad_y.device, d.grad_y_rows, d.weight_rows
+    ws = _scratch(workspace, lambda: _size_of(lib().pgg_moe_glu_grad_workspace_size, d, "glu_grad_workspace_size"),
+                  dev, stream)
+    out = _out(out, "out", (M, 2 * F), grad_y.dtype, dev, stream)
+    if want_h or h is not None:
+        h = _out(h, "h", (M, F), grad_y.dtype, dev, stream)
+    _check(lib().pgg_moe_glu_grad(ctypes.byref(d), grad_y.data_ptr(), weight.data_ptr(), gate_up.data_ptr(),
+                                  group_list.data_ptr(), out.data_ptr(), _ptr(h), ws.data_ptr(), _ws_bytes(ws),
+                                  _on_stream(stream, dev)), "pgg_moe_glu_grad")
+    return out, h
+
+
+def _lora_desc(x, weight, a, b, adapter_ids, scales) -> LoraDesc:
+    code = _value_type(x, "x", 2)
+    dev, T, K = x.device, x.shape[0], x.shape[1]
+    if weight.dim() != 2 or a.dim() != 3:
+        raise PggError(ERR_INVALID_ARG, "weight must be [K, N], a [adapters, rank, K] and b [adapters, rank, N]")
+    N, (P, R, _) = weight.shape[1], a.shape
+    _expect(weight, "weight", (K, N), x.dtype, dev)
+    _expect(a, "a", (P, R, K), x.dtype, dev)
+    _expect(b, "b", (P, R, N), x.dtype, dev)
+    _expect(adapter_ids, "adapter_ids", (T,), torch.int64, dev)
+    _expect(scales, "scales", (P,), torch.float32, dev)
+    return LoraDesc(T, K, N, P, R, code, 0)
+
+
+def lora_workspace_size(x, weight, a, b, adapter_ids, scales) -> int:
+    return _size_of(lib().pgg_lora_workspace_size, _lora_desc(x, weight, a, b, adapter_ids, scales),
+                    "lora_workspace_size")
+
+
+def lora_fwd(x: torch.Tensor, weight: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapter_ids: torch.Tensor,
+             scales: torch.Tensor, *, out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+             stream=None) -> torch.Tensor:
+    """A shared projection with a low-rank adapter per token: y [T, N] in x's
+    dtype, y[t] = x[t]·weight + scales[p] * (x[t]·a[p]ᵀ)·b[p] with p =
+    adapter_ids[t] (asynchronous).
+
+    x [T, K], weight [K, N], a [P, R, K] and b [P, R, N] share one of float32 /
+    float16 / bfloat16; adapter_ids [T] int64, negative for a token without an
+    adapter; scales [P] float32.  Tokens come in any order; runs of one id (the
+    tokens of a request) are fastest."""
+    d = _lora_desc(x, weight, a, b, adapter_ids, scales)
+    dev = x.device
+    ws = _scratch(workspace, lambda: _size_of(lib().pgg_lora_workspace_size, d, "lora_workspace_size"), dev, stream)
+    out = _out(out, "out", (d.tokens, d.out_features), x.dtype, dev, stream)
+    _check(lib().pgg_lora_fwd(ctypes.byref(d), x.data_ptr(), weight.data_ptr(), a.data_ptr(), b.data_ptr(),
+                              adapter_ids.data_ptr(), scales.data_ptr(), out.data_ptr(), ws.data_ptr(),
+                              _ws_bytes(ws), _on_stream(stream, dev)), "pgg_lora_fwd")
+    return out
 
 
 class KernelTimer:

@@ -1,5 +1,6 @@
 // C ABI of the fused MoE d_x backward, of the layer's forward, of its weight
-// gradient, of on-device routing and of unpermute and its gradient (declared
+// gradient, of on-device routing, of unpermute and its gradient, of the
+// router's gate, of the gated products and of the low-rank adapters (declared
 // in include/pgg.h).
 //
 // The execute call validates the descriptor on the host, lays out the
@@ -532,6 +533,129 @@ pgg_status pgg_moe_unpermute_grad(const pgg_moe_unpermute_desc* desc, const void
   return e == hipSuccess ? PGG_OK : PGG_ERR_HIP;
 }
 
+pgg_status pgg_moe_gate(const pgg_moe_gate_desc* desc, const void* logits, const float* bias,
+                        int64_t* expert_ids, float* probs, float* lse, hipStream_t stream) {
+  const pgg_status st = check_gate_desc(desc);
+  if (st != PGG_OK) return st;
+  if (!logits || !expert_ids || !probs) return PGG_ERR_INVALID_ARG;
+  if (!is_aligned(logits, elem_size(desc->dtype)) || !is_aligned(bias, 4) || !is_aligned(expert_ids, 8) ||
+      !is_aligned(probs, 4) || !is_aligned(lse, 4))
+    return PGG_ERR_MISALIGNED;
+  TimedLaunch t("gate", stream);
+  return launch_gate(*desc, logits, bias, expert_ids, probs, lse, stream) == hipSuccess ? PGG_OK : PGG_ERR_HIP;
+}
+
+pgg_status pgg_moe_gate_grad(const pgg_moe_gate_desc* desc, const void* logits, const float* lse,
+                             const int64_t* expert_ids, const float* grad_probs, const float* grad_lse,
+                             void* grad_logits, hipStream_t stream) {
+  const pgg_status st = check_gate_desc(desc);
+  if (st != PGG_OK) return st;
+  if (!logits || !lse || !expert_ids || !grad_probs || !grad_logits) return PGG_ERR_INVALID_ARG;
+  const size_t es = elem_size(desc->dtype);
+  if (!is_aligned(logits, es) || !is_aligned(grad_logits, es) || !is_aligned(lse, 4) || !is_aligned(expert_ids, 8) ||
+      !is_aligned(grad_probs, 4) || !is_aligned(grad_lse, 4))
+    return PGG_ERR_MISALIGNED;
+  TimedLaunch t("gate_grad", stream);
+  return launch_gate_grad(*desc, logits, lse, expert_ids, grad_probs, grad_lse, grad_logits, stream) == hipSuccess
+             ? PGG_OK : PGG_ERR_HIP;
+}
+
+pgg_status pgg_moe_glu_workspace_size(const pgg_moe_glu_desc* desc, size_t* bytes) {
+  if (!bytes) return PGG_ERR_INVALID_ARG;
+  Plan p;
+  const pgg_status st = make_glu_plan(desc, &p);
+  if (st != PGG_OK) return st;
+  *bytes = p.total;
+  return PGG_OK;
+}
+
+pgg_status pgg_moe_glu(const pgg_moe_glu_desc* desc, const void* x, const void* weight,
+                       const int64_t* expanded_row_idx, const int64_t* group_list, void* h, void* gate_up,
+                       void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  Plan p;
+  const pgg_status st = make_glu_plan(desc, &p);
+  if (st != PGG_OK) return st;
+  if (!x || !weight || !expanded_row_idx || !group_list || !h || !workspace) return PGG_ERR_INVALID_ARG;
+  if (workspace_bytes < p.total) return PGG_ERR_WORKSPACE_TOO_SMALL;
+  const size_t es = elem_size(p.dtype);
+  if (!is_aligned(workspace, kWorkspaceAlign) || !is_aligned(expanded_row_idx, 8) || !is_aligned(group_list, 8) ||
+      !is_aligned(x, es) || !is_aligned(weight, es) || !is_aligned(h, es) || !is_aligned(gate_up, es))
+    return PGG_ERR_MISALIGNED;
+  // rows of x, and the gate and the up half of every weight row
+  const bool aligned = is_aligned(x, 16) && is_aligned(weight, 16) && (size_t(p.N) * es) % 16 == 0 &&
+                       (size_t(p.K / 2) * es) % 16 == 0;
+  const WsView w = ws_view(p, workspace);
+  hipError_t e = enqueue_prep(p, expanded_row_idx, group_list, w, stream);
+  if (e == hipSuccess) {
+    TimedLaunch t("glu", stream);
+    e = launch_glu(p, desc->act, x, weight, h, gate_up, aligned, w, stream);
+  }
+  return e == hipSuccess ? PGG_OK : PGG_ERR_HIP;
+}
+
+pgg_status pgg_moe_glu_grad_workspace_size(const pgg_moe_glu_grad_desc* desc, size_t* bytes) {
+  if (!bytes) return PGG_ERR_INVALID_ARG;
+  Plan p;
+  const pgg_status st = make_glu_grad_plan(desc, &p);
+  if (st != PGG_OK) return st;
+  *bytes = p.total;
+  return PGG_OK;
+}
+
+pgg_status pgg_moe_glu_grad(const pgg_moe_glu_grad_desc* desc, const void* grad_y, const void* weight,
+                            const void* gate_up, const int64_t* group_list, void* grad_gate_up, void* h,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  Plan p;
+  const pgg_status st = make_glu_grad_plan(desc, &p);
+  if (st != PGG_OK) return st;
+  if (!grad_y || !weight || !gate_up || !group_list || !grad_gate_up || !workspace) return PGG_ERR_INVALID_ARG;
+  if (workspace_bytes < p.total) return PGG_ERR_WORKSPACE_TOO_SMALL;
+  const size_t es = elem_size(p.dtype);
+  if (!is_aligned(workspace, kWorkspaceAlign) || !is_aligned(group_list, 8) || !is_aligned(grad_y, es) ||
+      !is_aligned(weight, es) || !is_aligned(gate_up, es) || !is_aligned(grad_gate_up, es) || !is_aligned(h, es))
+    return PGG_ERR_MISALIGNED;
+  const bool aligned = is_aligned(grad_y, 16) && is_aligned(weight, 16) && (size_t(p.N) * es) % 16 == 0;
+  const WsView w = ws_view(p, workspace);
+  hipError_t e;
+  {
+    TimedLaunch t("prep_groups", stream);
+    e = launch_prep_groups(p, group_list, w, stream);
+  }
+  if (e == hipSuccess) {
+    TimedLaunch t("glu_grad", stream);
+    e = launch_glu_grad(p, desc->act, grad_y, weight, gate_up, grad_gate_up, h, aligned, w, stream);
+  }
+  return e == hipSuccess ? PGG_OK : PGG_ERR_HIP;
+}
+
+pgg_status pgg_lora_workspace_size(const pgg_lora_desc* desc, size_t* bytes) {
+  if (!bytes) return PGG_ERR_INVALID_ARG;
+  LoraPlan p;
+  const pgg_status st = make_lora_plan(desc, &p);
+  if (st != PGG_OK) return st;
+  *bytes = p.total;
+  return PGG_OK;
+}
+
+pgg_status pgg_lora_fwd(const pgg_lora_desc* desc, const void* x, const void* weight, const void* a, const void* b,
+                        const int64_t* adapter_ids, const float* scales, void* y, void* workspace,
+                        size_t workspace_bytes, hipStream_t stream) {
+  LoraPlan p;
+  const pgg_status st = make_lora_plan(desc, &p);
+  if (st != PGG_OK) return st;
+  if (!x || !weight || !a || !b || !adapter_ids || !scales || !y || !workspace) return PGG_ERR_INVALID_ARG;
+  if (workspace_bytes < p.total) return PGG_ERR_WORKSPACE_TOO_SMALL;
+  const size_t es = elem_size(p.dtype);
+  if (!is_aligned(workspace, kWorkspaceAlign) || !is_aligned(adapter_ids, 8) || !is_aligned(scales, 4) ||
+      !is_aligned(x, es) || !is_aligned(weight, es) || !is_aligned(a, es) || !is_aligned(b, es) || !is_aligned(y, es))
+    return PGG_ERR_MISALIGNED;
+  const bool aligned = is_aligned(x, 16) && is_aligned(weight, 16) && (size_t(p.K) * es) % 16 == 0 &&
+                       (size_t(p.N) * es) % 16 == 0;
+  TimedLaunch t("lora", stream);
+  return launch_lora(p, x, weight, a, b, adapter_ids, scales, y, workspace, aligned, stream) == hipSuccess
+             ? PGG_OK : PGG_ERR_HIP;
+}
+
 pgg_status pgg_moe_dx_read_device_error(const void* workspace, hipStream_t stream, int32_t* code,
                                         int64_t* detail) {
   if (!workspace || !code) return PGG_ERR_INVALID_ARG;
@@ -668,6 +792,7 @@ const char* pgg_device_error_string(int32_t code) {
     case PGG_DEV_INDEX_RANGE: return "expanded_row_idx value outside [0, M)";
     case PGG_DEV_INDEX_DUP: return "expanded_row_idx is not a permutation";
     case PGG_DEV_EXPERT_RANGE: return "expert id outside [0, experts)";
+    case PGG_DEV_ADAPTER_RANGE: return "adapter id not below the number of adapters";
   }
   return "unknown device error";
 }

@@ -1,0 +1,193 @@
+// Gated product of the experts, the first half of a gated feed-forward layer:
+//
+//   (gate | up)[i, :] = x[p(i) / topK, :] * W[g(i)]      W[g] is [K, 2F]: gate columns, then up columns
+//   h[i, f]           = act(gate[i, f]) * up[i, f]
+//
+// for the expanded rows i of the routing index (rows of one expert are
+// neighbours, experts hold any number of them).  Neither the permuted copy of
+// x nor, unless the caller wants it for the backward pass, the [M, 2F] product
+// is stored: a tile of the product holds gate columns in its even blocks of 32
+// and the matching up columns in its odd ones, so a wave has both of a pair in
+// registers and the activation is part of the store.  h is rounded once, from
+// the fp32 accumulators.
+//
+// Many rows per expert are bound by the matrix instructions, few by reading
+// the used experts' weights once.  The tiles and the pipelines are those of
+// pgg_nn.h; with few rows per expert the reduction is split over workgroups so
+// that enough of them stream weights, the fp32 partial products of the splits
+// go to the workspace, and a second kernel adds them in split order and applies
+// the activation.
+#include <algorithm>
+
+#include "pgg_act.h"
+#include "pgg_nn.h"
+
+namespace pgg {
+
+namespace {
+
+struct GluArgs {
+  const void* A;            // x [batch, R]
+  const void* W;            // weight [G, R, C]
+  const WsHeader* hdr;
+  const MTile* tiles;
+  const int32_t* ori;       // expanded row -> original position
+  void* h;                  // [M, F]
+  void* gate_up;            // [M, C] or NULL
+  float* part;              // split partials [ksplit, M, C], or NULL
+  int64_t R, C, F, M, kspan;
+  uint32_t topk;
+  int32_t bm;               // rows of a table entry
+  int32_t n_slots, n_col_tiles;
+};
+
+template <int ACT>
+struct GluOp {
+  using Args = GluArgs;
+
+  template <int BM>
+  static __device__ __forceinline__ bool tile(const Args& a, int slot, MTile& t) {
+    if (a.hdr->err != kNoError) return false;
+    const int sub = a.bm / BM;   // tiles to a table entry
+    const int entry = slot / sub;
+    if (entry >= a.hdr->n_tiles) return false;
+    t = a.tiles[entry];
+    const int skip = (slot - entry * sub) * BM;
+    t.row0 += skip;
+    t.rows = min(t.rows - skip, BM);
+    return t.rows > 0;
+  }
+
+  static __device__ __forceinline__ int64_t src(const Args& a, const MTile& t, int r) {
+    return static_cast<uint32_t>(a.ori[t.row0 + r]) / a.topk;
+  }
+
+  static __device__ __forceinline__ int64_t weight(const Args& a, const MTile& t) {
+    return static_cast<int64_t>(t.g) * a.R * a.C;
+  }
+
+  // column f of the pair that column n of the tile belongs to
+  template <int BN>
+  static __device__ __forceinline__ int64_t pair(int ct, int n) {
+    return static_cast<int64_t>(ct) * (BN / 2) + (n >> 6) * 32 + (n & 31);
+  }
+
+  template <int BN>
+  static __device__ __forceinline__ ColumnRun column(const Args& a, int ct, int n) {
+    const int64_t f = pair<BN>(ct, n);
+    return {f + ((n >> 5) & 1) * a.F, a.F - f};
+  }
+
+  template <class T, int BN, int FM, int FN>
+  static __device__ __forceinline__ void store(const Args& a, const MTile& t, int ct, int m0, int n0, int lane,
+                                               const f32x16_t (&acc)[FM][FN]) {
+    using E = typename T::elem;
+    const int lr = lane & 31, lh = lane >> 5;
+    const int64_t split = static_cast<int64_t>(blockIdx.y) * a.M;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; j += 2) {
+        const int64_t f = pair<BN>(ct, n0 + j * 32 + lr);
+        if (f >= a.F) continue;
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const int m = m0 + i * 32 + acc_row(v, lh);
+          if (m >= t.rows) continue;
+          const int64_t row = t.row0 + m;
+          const float gate = acc[i][j][v], up = acc[i][j + 1][v];
+          if (a.part) {
+            a.part[(split + row) * a.C + f] = gate;
+            a.part[(split + row) * a.C + a.F + f] = up;
+            continue;
+          }
+          static_cast<E*>(a.h)[row * a.F + f] = from_float<T>(activate<ACT>(gate) * up);
+          if (a.gate_up) {
+            static_cast<E*>(a.gate_up)[row * a.C + f] = from_float<T>(gate);
+            static_cast<E*>(a.gate_up)[row * a.C + a.F + f] = from_float<T>(up);
+          }
+        }
+      }
+  }
+};
+
+// Adds the splits' partial products in split order and stores h (and the products).
+template <class T, int ACT>
+__global__ __launch_bounds__(256) void glu_finish_kernel(GluArgs a, int32_t ksplit) {
+  using E = typename T::elem;
+  if (a.hdr->err != kNoError) return;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  const int64_t n = a.M * a.F, plane = a.M * a.C;
+  for (int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < n; e += step) {
+    const int64_t row = e / a.F, f = e - row * a.F;
+    const float* p = a.part + row * a.C + f;
+    float gate = p[0], up = p[a.F];
+    for (int32_t s = 1; s < ksplit; ++s) {
+      gate += p[s * plane];
+      up += p[s * plane + a.F];
+    }
+    static_cast<E*>(a.h)[e] = from_float<T>(activate<ACT>(gate) * up);
+    if (a.gate_up) {
+      static_cast<E*>(a.gate_up)[row * a.C + f] = from_float<T>(gate);
+      static_cast<E*>(a.gate_up)[row * a.C + a.F + f] = from_float<T>(up);
+    }
+  }
+}
+
+template <class T, int BM, int BN, int WM, int WN, int EU, int ACT>
+hipError_t launch_reg(const Plan& p, GluArgs a, hipStream_t s) {
+  a.n_slots = p.max_tiles * (p.bm / BM);
+  a.n_col_tiles = static_cast<int32_t>((a.F + BN / 2 - 1) / (BN / 2));
+  return launch_nn_reg<T, GluOp<ACT>, BM, BN, WM, WN, EU>(a, p.ksplit, s);
+}
+
+template <class T, int ACT>
+hipError_t launch_16(const Plan& p, GluArgs a, bool aligned, hipStream_t s) {
+  if (p.regime == kStream) return launch_reg<T, 32, 256, 1, 4, 2, ACT>(p, a, s);
+  if (!aligned) return launch_reg<T, 128, 128, 2, 2, 2, ACT>(p, a, s);
+  a.n_slots = p.max_tiles;
+  a.n_col_tiles = static_cast<int32_t>((a.F + 127) / 128);
+  return launch_nn_dma<T, GluOp<ACT>>(a, s);
+}
+
+template <class T, int ACT>
+hipError_t finish(const GluArgs& a, int32_t ksplit, hipStream_t s) {
+  const int64_t blocks = std::min<int64_t>((a.M * a.F + 255) / 256, 2048);
+  hipLaunchKernelGGL((glu_finish_kernel<T, ACT>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a, ksplit);
+  return hipGetLastError();
+}
+
+template <int ACT>
+hipError_t launch_act(const Plan& p, const GluArgs& a, bool aligned, hipStream_t s) {
+  hipError_t e;
+  if (p.dtype == PGG_F32) return launch_reg<TF32, 128, 128, 2, 2, 2, ACT>(p, a, s);
+  e = p.dtype == PGG_BF16 ? launch_16<TBf16, ACT>(p, a, aligned, s) : launch_16<TF16, ACT>(p, a, aligned, s);
+  if (e != hipSuccess || p.ksplit == 1) return e;
+  return p.dtype == PGG_BF16 ? finish<TBf16, ACT>(a, p.ksplit, s) : finish<TF16, ACT>(a, p.ksplit, s);
+}
+
+}  // namespace
+
+hipError_t launch_glu(const Plan& p, int32_t act, const void* x, const void* weight, void* h, void* gate_up,
+                      bool aligned, const WsView& w, hipStream_t s) {
+  GluArgs a;
+  a.A = x;
+  a.W = weight;
+  a.hdr = w.hdr;
+  a.tiles = w.tiles;
+  a.ori = w.ori;
+  a.h = h;
+  a.gate_up = gate_up;
+  a.part = p.ksplit > 1 ? w.ring : nullptr;
+  a.R = p.N;          // the plan keeps the reduction in N and the columns in K
+  a.C = p.K;
+  a.F = p.K / 2;
+  a.M = p.M;
+  a.kspan = p.kspan;
+  a.topk = static_cast<uint32_t>(p.topk);
+  a.bm = p.bm;
+  return act == PGG_ACT_SILU ? launch_act<PGG_ACT_SILU>(p, a, aligned, s)
+                             : launch_act<PGG_ACT_GELU_TANH>(p, a, aligned, s);
+}
+
+}  // namespace pgg

@@ -1,0 +1,233 @@
+// Gradient through the experts' gated product, from the gradient of the
+// products that follow it:
+//
+//   dh[i, f]       = sum_d grad_y[i, d] * W[g(i), f, d]       W[g]: the expert's second matrix, [F, D]
+//   grad_gate[i, f] = dh * up[i, f] * act'(gate[i, f])
+//   grad_up[i, f]   = dh * act(gate[i, f])
+//   h[i, f]         = act(gate[i, f]) * up[i, f]              (recomputed, for the gradient of W)
+//
+// dh stays in the fp32 accumulators: a tile reads the saved products (gate |
+// up)[M, 2F] at its place and stores the three results.
+//
+// Both operands hold the reduction d contiguously, the layout that MFMA
+// operands take, so tiles are staged in LDS as rows of 16-byte chunks, chunk c
+// of row r at c ^ ((r >> 1) & 7).
+#include "pgg_act.h"
+#include "pgg_nn.h"
+
+namespace pgg {
+
+namespace {
+
+struct GluGradArgs {
+  const void* A;            // grad_y [M, D]
+  const void* B;            // weight [G, F, D]
+  const void* gate_up;      // [M, 2F]
+  const WsHeader* hdr;
+  const MTile* tiles;
+  void* grad;               // [M, 2F]
+  void* h;                  // [M, F] or NULL
+  int64_t D, F;
+  int32_t bm;               // rows of a table entry
+  int32_t n_slots, n_col_tiles;
+};
+
+template <class T, int ACT, int FM, int FN>
+__device__ __forceinline__ void store_grad(const GluGradArgs& a, const MTile& t, int64_t col0, int m0, int n0,
+                                           int lane, const f32x16_t (&acc)[FM][FN]) {
+  using E = typename T::elem;
+  const int lr = lane & 31, lh = lane >> 5;
+  const int64_t C = 2 * a.F;
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const int64_t f = col0 + n0 + j * 32 + lr;
+      if (f >= a.F) continue;
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int m = m0 + i * 32 + acc_row(v, lh);
+        if (m >= t.rows) continue;
+        const int64_t row = t.row0 + m;
+        const E* gu = static_cast<const E*>(a.gate_up) + row * C + f;
+        const float up = to_float<T>(gu[a.F]), dh = acc[i][j][v];
+        float value, slope;
+        activate_grad<ACT>(to_float<T>(gu[0]), value, slope);
+        E* g = static_cast<E*>(a.grad) + row * C + f;
+        g[0] = from_float<T>(dh * up * slope);
+        g[a.F] = from_float<T>(dh * value);
+        if (a.h) static_cast<E*>(a.h)[row * a.F + f] = from_float<T>(value * up);
+      }
+    }
+}
+
+// Through registers: every type and alignment.  Rows and columns past the
+// tile's repeat valid ones and are not stored; elements past the reduction are
+// zero in both operands.
+template <class T, int BM, int BN, int WM, int WN, int EU, int ACT>
+__global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(EU, EU)))
+void glu_grad_reg_kernel(GluGradArgs a) {
+  using E = typename T::elem;
+  constexpr int NT = WM * WN * 64;
+  constexpr int EPC = T::kPerChunk;
+  constexpr int kChunks = 8;
+  constexpr int BK = kChunks * EPC;
+  constexpr int WTM = BM / WM, WTN = BN / WN;
+  constexpr int FM = WTM / 32, FN = WTN / 32;
+  constexpr int A_CHUNKS = BM * kChunks, B_CHUNKS = BN * kChunks;
+  constexpr int A_PER_T = A_CHUNKS / NT, B_PER_T = B_CHUNKS / NT;
+  static_assert(WTM % 32 == 0 && WTN % 32 == 0, "whole 32x32 blocks per wave");
+  static_assert(A_CHUNKS % NT == 0 && B_CHUNKS % NT == 0, "a stage splits evenly");
+  __shared__ u32x4_t lds[2][A_CHUNKS + B_CHUNKS];
+
+  if (a.hdr->err != kNoError) return;
+  int slot, ct;
+  if (!raster<8, 4>(blockIdx.x, a.n_slots, a.n_col_tiles, slot, ct)) return;
+  const int sub = a.bm / BM;
+  const int entry = slot / sub;
+  if (entry >= a.hdr->n_tiles) return;
+  MTile tile = a.tiles[entry];
+  tile.row0 += (slot - entry * sub) * BM;
+  tile.rows = min(tile.rows - (slot - entry * sub) * BM, BM);
+  if (tile.rows <= 0) return;
+  const int64_t col0 = static_cast<int64_t>(ct) * BN;
+  const int64_t D = a.D;
+
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = tid >> 6;
+  const int wm = wave % WM, wn = wave / WM;
+  const int lr = lane & 31, lh = lane >> 5;
+
+  const E* arow[A_PER_T];
+  const E* brow[B_PER_T];
+#pragma unroll
+  for (int s = 0; s < A_PER_T; ++s) {
+    const int q = tid + s * NT;
+    arow[s] = static_cast<const E*>(a.A) + (tile.row0 + static_cast<int64_t>(min(q / kChunks, tile.rows - 1))) * D +
+              (q % kChunks) * EPC;
+  }
+#pragma unroll
+  for (int s = 0; s < B_PER_T; ++s) {
+    const int q = tid + s * NT;
+    const int64_t f = min<int64_t>(col0 + q / kChunks, a.F - 1);
+    brow[s] = static_cast<const E*>(a.B) + (tile.g * a.F + f) * D + (q % kChunks) * EPC;
+  }
+
+  u32x4_t ra[A_PER_T], rb[B_PER_T];
+  auto load_stage = [&](int kt) {
+    const int64_t k0 = static_cast<int64_t>(kt) * BK;
+    if (k0 + BK <= D) {
+#pragma unroll
+      for (int s = 0; s < A_PER_T; ++s) ra[s] = load16(arow[s] + k0);
+#pragma unroll
+      for (int s = 0; s < B_PER_T; ++s) rb[s] = load16(brow[s] + k0);
+    } else {
+#pragma unroll
+      for (int s = 0; s < A_PER_T; ++s)
+        ra[s] = load16_part<T>(arow[s] + k0, D - k0 - (tid + s * NT) % kChunks * EPC);
+#pragma unroll
+      for (int s = 0; s < B_PER_T; ++s)
+        rb[s] = load16_part<T>(brow[s] + k0, D - k0 - (tid + s * NT) % kChunks * EPC);
+    }
+  };
+  auto store_stage = [&](int buf) {
+#pragma unroll
+    for (int s = 0; s < A_PER_T; ++s) {
+      const int q = tid + s * NT;
+      lds[buf][q / kChunks * kChunks + a_slot(q / kChunks, q % kChunks)] = ra[s];
+    }
+#pragma unroll
+    for (int s = 0; s < B_PER_T; ++s) {
+      const int q = tid + s * NT;
+      lds[buf][A_CHUNKS + q / kChunks * kChunks + a_slot(q / kChunks, q % kChunks)] = rb[s];
+    }
+  };
+
+  f32x16_t acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+
+  auto compute = [&](int buf) {
+    const u32x4_t* As = lds[buf];
+    const u32x4_t* Bs = lds[buf] + A_CHUNKS;
+    u32x4_t fa[2][FM], fb[2][FN];
+    auto load_frags = [&](int q, u32x4_t (&xa)[FM], u32x4_t (&xb)[FN]) {
+      const int sl = a_slot(lr, 2 * q + lh);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) xa[i] = As[(wm * WTM + i * 32 + lr) * kChunks + sl];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) xb[j] = Bs[(wn * WTN + j * 32 + lr) * kChunks + sl];
+    };
+    load_frags(0, fa[0], fb[0]);
+#pragma unroll
+    for (int q = 0; q < kChunks / 2; ++q) {
+      if (q + 1 < kChunks / 2) load_frags(q + 1, fa[(q + 1) & 1], fb[(q + 1) & 1]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) mma<T>(acc[i][j], fa[q & 1][i], fb[q & 1][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  const int nk = static_cast<int>((D + BK - 1) / BK);
+  load_stage(0);
+  store_stage(0);
+  __syncthreads();
+  for (int kt = 0; kt < nk; ++kt) {
+    if (kt + 1 < nk) load_stage(kt + 1);
+    compute(kt & 1);
+    if (kt + 1 < nk) store_stage((kt & 1) ^ 1);
+    __syncthreads();
+  }
+  store_grad<T, ACT, FM, FN>(a, tile, col0, wm * WTM, wn * WTN, lane, acc);
+}
+
+template <class T, int BM, int BN, int WM, int WN, int EU, int ACT>
+hipError_t launch_reg(const Plan& p, GluGradArgs a, hipStream_t s) {
+  a.n_slots = p.max_tiles * (p.bm / BM);
+  a.n_col_tiles = static_cast<int32_t>((a.F + BN - 1) / BN);
+  unsigned tiles = static_cast<unsigned>(a.n_slots) * static_cast<unsigned>(a.n_col_tiles);
+  tiles = (tiles + 8 * 32 - 1) / (8 * 32) * (8 * 32);
+  hipLaunchKernelGGL((glu_grad_reg_kernel<T, BM, BN, WM, WN, EU, ACT>), dim3(tiles), dim3(WM * WN * 64), 0, s, a);
+  return hipGetLastError();
+}
+
+template <class T, int ACT>
+hipError_t launch_typed(const Plan& p, const GluGradArgs& a, hipStream_t s) {
+  if (p.bm == 64) return launch_reg<T, 64, 128, 2, 2, 2, ACT>(p, a, s);
+  return launch_reg<T, 128, 128, 2, 2, 2, ACT>(p, a, s);
+}
+
+template <int ACT>
+hipError_t launch_act(const Plan& p, const GluGradArgs& a, hipStream_t s) {
+  if (p.dtype == PGG_F32) return launch_typed<TF32, ACT>(p, a, s);
+  return p.dtype == PGG_BF16 ? launch_typed<TBf16, ACT>(p, a, s) : launch_typed<TF16, ACT>(p, a, s);
+}
+
+}  // namespace
+
+hipError_t launch_glu_grad(const Plan& p, int32_t act, const void* grad_y, const void* weight, const void* gate_up,
+                           void* grad, void* h, bool aligned, const WsView& w, hipStream_t s) {
+  GluGradArgs a;
+  a.A = grad_y;
+  a.B = weight;
+  a.gate_up = gate_up;
+  a.hdr = w.hdr;
+  a.tiles = w.tiles;
+  a.grad = grad;
+  a.h = h;
+  a.D = p.N;          // the plan keeps the reduction in N and the columns in K
+  a.F = p.K;
+  a.bm = p.bm;
+  (void)aligned;
+  return act == PGG_ACT_SILU ? launch_act<PGG_ACT_SILU>(p, a, s) : launch_act<PGG_ACT_GELU_TANH>(p, a, s);
+}
+
+}  // namespace pgg

@@ -1,0 +1,393 @@
+// A shared projection with low-rank adapters of many requests beside it:
+//
+//   y[t, :] = x[t, :] * W + scale[p] * (x[t, :] * A_p^T) * B_p      p = adapter_ids[t]
+//
+// W [K, N] is the same for every token; A_p and B_p hold one row per rank,
+// A [P, R, K] and B [P, R, N]; a token with a negative id has no adapter.
+// Tokens may come in any order; requests of many tokens are runs of one id.
+//
+// The inner product z = scale * x * A_p^T is computed first, in fp32, into the
+// workspace ([T, R], a few values per token).  Then the shared product runs on
+// the tiles of pgg_nn.h, and the tokens' z * B_p are added to its fp32
+// accumulators before the one rounding of the store, so y is written once and
+// the projection is never read back.
+//
+// Which adapter a row has is data.  A wave that multiplies 32 rows goes through
+// the adapters found among them: it multiplies all 32 rows with one adapter and
+// keeps the rows that have it.  Selecting results, not operands, means that
+// infinities or NaN in one request's adapter stay in that request's rows.
+// Runs of one id make that one pass, 32 different ids 32 passes.
+//
+// z is fp32 and the matrix instructions take 16 bits, so z is split into two
+// bf16 parts (16 significand bits, relative error 2^-17, far below the
+// rounding of a 16-bit y; bf16 has the range of fp32, so nothing overflows),
+// and an fp16 B_p into two bf16 parts exactly.  fp32 inputs use fp32 matrix
+// instructions.
+//
+// With few tokens the projection is bound by reading W once and the launches:
+// the reduction is split over workgroups, the first launch also computes z,
+// token by token, in spare workgroups, and a second one adds the splits in
+// split order and the tokens' z * B_p.
+#include <algorithm>
+
+#include "pgg_nn.h"
+#include "pgg_prep.h"
+
+namespace pgg {
+
+namespace {
+
+struct LoraArgs {
+  const void* A;            // x [T, R]
+  const void* W;            // weight [R, C]
+  const void* a;            // [P, rank, R]
+  const void* b;            // [P, rank, C]
+  const int64_t* ids;       // [T]
+  const float* scales;      // [P]
+  float* z;                 // [T, rank]
+  void* y;                  // [T, C]
+  float* part;              // split partials [ksplit, T, C], or NULL
+  WsHeader* hdr;
+  int64_t R, C, T, kspan;
+  int64_t P;
+  int32_t rank;
+  int32_t n_slots, n_col_tiles;
+};
+
+// The token's adapter, or -1 where it has none (also for an id past the
+// adapters, which the header reports).
+__device__ __forceinline__ int32_t adapter_of(const LoraArgs& a, int64_t t) {
+  const int64_t p = a.ids[t];
+  return p >= 0 && p < a.P ? static_cast<int32_t>(p) : -1;
+}
+
+// One workgroup: the header, with the smallest token whose id is past the adapters.
+__device__ void check_ids(const LoraArgs& a) {
+  __shared__ unsigned long long bad;
+  if (threadIdx.x == 0) bad = ~0ull;
+  __syncthreads();
+  for (int64_t t = threadIdx.x; t < a.T; t += blockDim.x)
+    if (a.ids[t] >= a.P) {
+      atomicMin(&bad, static_cast<unsigned long long>(t));
+      break;
+    }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    reset_header(a.hdr);
+    if (bad != ~0ull) set_error(a.hdr, PGG_DEV_ADAPTER_RANGE, static_cast<long long>(bad));
+  }
+}
+
+// ---------------------------------------------------------------- z, many tokens
+
+// 32 tokens x 32 ranks per workgroup (blockIdx.y: which 32 ranks), the
+// reduction split over its four waves and added in wave order.  The last
+// workgroup along x checks the ids.
+template <class T>
+__global__ __launch_bounds__(256) void lora_shrink_kernel(LoraArgs a) {
+  using E = typename T::elem;
+  constexpr int EPC = T::kPerChunk, kStep = 2 * EPC, kUnroll = 4;
+  __shared__ float red[4][32][33];
+  if (blockIdx.x == gridDim.x - 1) {
+    if (blockIdx.y == 0) check_ids(a);
+    return;
+  }
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lr = lane & 31, lh = lane >> 5;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * 32;
+  const int rows = static_cast<int>(min<int64_t>(32, a.T - t0));
+  const int r0 = blockIdx.y * 32;
+  const int64_t R = a.R;
+  const int32_t id = lr < rows ? adapter_of(a, t0 + lr) : -1;
+  // this wave's part of the reduction, in whole steps
+  const int64_t steps = (R + kStep - 1) / kStep;
+  const int64_t per = (steps + 3) / 4;
+  const int64_t s0 = min<int64_t>(steps, wave * per), s1 = min<int64_t>(steps, s0 + per);
+  const E* x = static_cast<const E*>(a.A) + (t0 + min(lr, rows - 1)) * R;
+  uint32_t pending = static_cast<uint32_t>(__ballot(id >= 0));
+  while (pending) {
+    const int32_t p = __shfl(id, __builtin_ctz(pending));
+    const uint32_t mine = static_cast<uint32_t>(__ballot(id == p));
+    pending &= ~mine;
+    const E* ar = static_cast<const E*>(a.a) + (static_cast<int64_t>(p) * a.rank + min(r0 + lr, a.rank - 1)) * R;
+    f32x16_t acc;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
+    int64_t s = s0;
+    for (; s + kUnroll <= s1 && (s + kUnroll) * kStep <= R; s += kUnroll) {
+      u32x4_t fx[kUnroll], fw[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int64_t k = (s + u) * kStep + lh * EPC;
+        fx[u] = load16(x + k);
+        fw[u] = load16(ar + k);
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) mma<T>(acc, fx[u], fw[u]);
+    }
+    for (; s < s1; ++s) {
+      const int64_t k = s * kStep + lh * EPC;
+      mma<T>(acc, load16_part<T>(x + k, R - k), load16_part<T>(ar + k, R - k));
+    }
+#pragma unroll
+    for (int v = 0; v < 16; ++v) red[wave][acc_row(v, lh)][lr] = acc[v];
+    __syncthreads();
+    const float scale = a.scales[p];
+    for (int e = threadIdx.x; e < 32 * 32; e += 256) {
+      const int m = e >> 5, r = e & 31;
+      if (((mine >> m) & 1) && r0 + r < a.rank)
+        a.z[(t0 + m) * a.rank + r0 + r] = scale * (((red[0][m][r] + red[1][m][r]) + red[2][m][r]) + red[3][m][r]);
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------- z, few tokens
+
+// One workgroup per token: wave w takes ranks w, w + 4, ...; lanes run along
+// the reduction and their sums are added over a fixed tree.
+template <class T>
+__device__ __forceinline__ void shrink_token(const LoraArgs& a, int64_t t) {
+  using E = typename T::elem;
+  constexpr int EPC = T::kPerChunk;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int32_t p = adapter_of(a, t);
+  if (p < 0) return;
+  const E* x = static_cast<const E*>(a.A) + t * a.R;
+  const float scale = a.scales[p];
+  for (int r = wave; r < a.rank; r += 4) {
+    const E* ar = static_cast<const E*>(a.a) + (static_cast<int64_t>(p) * a.rank + r) * a.R;
+    float sum = 0.0f;
+    for (int64_t k = lane * EPC; k < a.R; k += 64 * EPC) {
+      const u32x4_t vx = load16_part<T>(x + k, a.R - k), vw = load16_part<T>(ar + k, a.R - k);
+      E ex[EPC], ew[EPC];
+      __builtin_memcpy(ex, &vx, 16);
+      __builtin_memcpy(ew, &vw, 16);
+#pragma unroll
+      for (int e = 0; e < EPC; ++e) sum = fmaf(to_float<T>(ex[e]), to_float<T>(ew[e]), sum);
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+    if (lane == 0) a.z[t * a.rank + r] = scale * sum;
+  }
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void lora_shrink_few_kernel(LoraArgs a) {
+  if (static_cast<int64_t>(blockIdx.x) == a.T) check_ids(a);
+  else shrink_token<T>(a, blockIdx.x);
+}
+
+// ---------------------------------------------------------------- the shared product
+
+// 8 fp32 values as two bf16 parts.
+__device__ __forceinline__ void split_bf16(const float (&v)[8], u32x4_t& hi, u32x4_t& lo) {
+  uint16_t h[8], l[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    h[e] = from_float<TBf16>(v[e]);
+    const float rest = v[e] - to_float<TBf16>(h[e]);
+    l[e] = rest == rest ? from_float<TBf16>(rest) : 0;   // an infinite value has no rest
+  }
+  __builtin_memcpy(&hi, h, 16);
+  __builtin_memcpy(&lo, l, 16);
+}
+
+struct LoraOp {
+  using Args = LoraArgs;
+
+  template <int BM>
+  static __device__ __forceinline__ bool tile(const Args& a, int slot, MTile& t) {
+    const int64_t row0 = static_cast<int64_t>(slot) * BM;
+    t.g = 0;
+    t.row0 = static_cast<int32_t>(row0);
+    t.rows = static_cast<int32_t>(min<int64_t>(BM, a.T - row0));
+    t.pad = 0;
+    return t.rows > 0;
+  }
+
+  static __device__ __forceinline__ int64_t src(const Args&, const MTile& t, int r) { return int64_t(t.row0) + r; }
+  static __device__ __forceinline__ int64_t weight(const Args&, const MTile&) { return 0; }
+
+  template <int BN>
+  static __device__ __forceinline__ ColumnRun column(const Args& a, int ct, int n) {
+    const int64_t c = static_cast<int64_t>(ct) * BN + n;
+    return {c, a.C - c};
+  }
+
+  // rows t (this lane: zrow) times columns c of adapter p, all ranks
+  template <class T>
+  static __device__ __forceinline__ f32x16_t expand(const Args& a, const float* zrow, int32_t p, int64_t c, int lh) {
+    using E = typename T::elem;
+    const E* b = static_cast<const E*>(a.b) + static_cast<int64_t>(p) * a.rank * a.C + c;
+    const bool ok = c < a.C;
+    f32x16_t d;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) d[v] = 0.0f;
+    if constexpr (T::kPerChunk == 8) {
+      for (int r = 0; r < a.rank; r += 16) {
+        float zv[8], bv[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int k = r + 8 * lh + e;
+          zv[e] = k < a.rank ? zrow[k] : 0.0f;
+          bv[e] = ok && k < a.rank ? to_float<T>(b[static_cast<int64_t>(k) * a.C]) : 0.0f;
+        }
+        u32x4_t zh, zl, bh, bl;
+        split_bf16(zv, zh, zl);
+        split_bf16(bv, bh, bl);
+        mma<TBf16>(d, zh, bh);
+        mma<TBf16>(d, zl, bh);
+        if constexpr (__is_same(T, TF16)) mma<TBf16>(d, zh, bl);
+      }
+    } else {
+      for (int r = 0; r < a.rank; r += 8) {
+        u32x4_t fz, fb;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int k = r + 4 * lh + e;
+          fz[e] = __builtin_bit_cast(uint32_t, k < a.rank ? zrow[k] : 0.0f);
+          fb[e] = __builtin_bit_cast(uint32_t, ok && k < a.rank ? b[static_cast<int64_t>(k) * a.C] : 0.0f);
+        }
+        mma<T>(d, fz, fb);
+      }
+    }
+    return d;
+  }
+
+  template <class T, int BN, int FM, int FN>
+  static __device__ __forceinline__ void store(const Args& a, const MTile& t, int ct, int m0, int n0, int lane,
+                                               f32x16_t (&acc)[FM][FN]) {
+    using E = typename T::elem;
+    const int lr = lane & 31, lh = lane >> 5;
+    const int64_t c0 = static_cast<int64_t>(ct) * BN + n0 + lr;
+    if (a.part) {
+      float* out = a.part + (static_cast<int64_t>(blockIdx.y) * a.T + t.row0) * a.C;
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const int m = m0 + i * 32 + acc_row(v, lh);
+            if (m < t.rows && c0 + j * 32 < a.C) out[m * a.C + c0 + j * 32] = acc[i][j][v];
+          }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int m = m0 + i * 32 + lr;
+      const int32_t id = m < t.rows ? adapter_of(a, int64_t(t.row0) + m) : -1;
+      const float* zrow = a.z + (int64_t(t.row0) + min(m, t.rows - 1)) * a.rank;
+      uint32_t pending = static_cast<uint32_t>(__ballot(id >= 0));
+      while (pending) {
+        const int32_t p = __shfl(id, __builtin_ctz(pending));
+        const uint32_t mine = static_cast<uint32_t>(__ballot(id == p));
+        pending &= ~mine;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          const f32x16_t d = expand<T>(a, zrow, p, c0 + j * 32, lh);
+#pragma unroll
+          for (int v = 0; v < 16; ++v)
+            if ((mine >> acc_row(v, lh)) & 1) acc[i][j][v] += d[v];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const int m = m0 + i * 32 + acc_row(v, lh);
+          const int64_t c = c0 + j * 32;
+          if (m < t.rows && c < a.C)
+            static_cast<E*>(a.y)[(int64_t(t.row0) + m) * a.C + c] = from_float<T>(acc[i][j][v]);
+        }
+  }
+};
+
+// Adds the splits' partial products in split order and the token's z * B_p.
+template <class T>
+__global__ __launch_bounds__(256) void lora_finish_kernel(LoraArgs a, int32_t ksplit) {
+  using E = typename T::elem;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  const int64_t n = a.T * a.C;
+  for (int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < n; e += step) {
+    const int64_t t = e / a.C, c = e - t * a.C;
+    float sum = a.part[e];
+    for (int32_t s = 1; s < ksplit; ++s) sum += a.part[s * n + e];
+    const int32_t p = adapter_of(a, t);
+    if (p >= 0) {
+      const E* b = static_cast<const E*>(a.b) + static_cast<int64_t>(p) * a.rank * a.C + c;
+      float d = 0.0f;
+      for (int32_t r = 0; r < a.rank; ++r) d = fmaf(a.z[t * a.rank + r], to_float<T>(b[r * a.C]), d);
+      sum += d;
+    }
+    static_cast<E*>(a.y)[e] = from_float<T>(sum);
+  }
+}
+
+template <class T, int BM, int BN, int WM, int WN>
+hipError_t launch_tiles(LoraArgs a, const LoraPlan& p, hipStream_t s) {
+  a.n_slots = static_cast<int32_t>((a.T + BM - 1) / BM);
+  a.n_col_tiles = static_cast<int32_t>((a.C + BN - 1) / BN);
+  return launch_nn_reg<T, LoraOp, BM, BN, WM, WN, 2>(a, p.ksplit, s);
+}
+
+template <class T>
+hipError_t launch_typed(const LoraPlan& p, LoraArgs a, bool aligned, hipStream_t s) {
+  if (a.T <= kLoraFewTokens) {
+    hipLaunchKernelGGL((lora_shrink_few_kernel<T>), dim3(static_cast<unsigned>(a.T + 1)), dim3(256), 0, s, a);
+  } else {
+    const dim3 grid(static_cast<unsigned>((a.T + 31) / 32 + 1), static_cast<unsigned>((a.rank + 31) / 32));
+    hipLaunchKernelGGL((lora_shrink_kernel<T>), grid, dim3(256), 0, s, a);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if constexpr (T::kPerChunk == 8) {
+    if (p.tile == kLoraRows32) {
+      e = launch_tiles<T, 32, 256, 1, 4>(a, p, s);
+    } else if (p.tile == kLoraRows256 && aligned) {
+      a.n_slots = static_cast<int32_t>((a.T + 255) / 256);
+      a.n_col_tiles = static_cast<int32_t>((a.C + 255) / 256);
+      e = launch_nn_dma<T, LoraOp>(a, s);
+    } else {
+      e = launch_tiles<T, 128, 128, 2, 2>(a, p, s);
+    }
+  } else {
+    e = p.tile == kLoraRows32 ? launch_tiles<T, 32, 128, 1, 4>(a, p, s) : launch_tiles<T, 128, 128, 2, 2>(a, p, s);
+  }
+  if (e != hipSuccess || p.ksplit == 1) return e;
+  const int64_t blocks = std::min<int64_t>((a.T * a.C + 255) / 256, 4096);
+  hipLaunchKernelGGL((lora_finish_kernel<T>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a, p.ksplit);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_lora(const LoraPlan& p, const void* x, const void* weight, const void* a, const void* b,
+                       const int64_t* ids, const float* scales, void* y, void* ws, bool aligned, hipStream_t s) {
+  char* base = static_cast<char*>(ws);
+  LoraArgs g;
+  g.A = x;
+  g.W = weight;
+  g.a = a;
+  g.b = b;
+  g.ids = ids;
+  g.scales = scales;
+  g.z = reinterpret_cast<float*>(base + p.off_z);
+  g.y = y;
+  g.part = p.ksplit > 1 ? reinterpret_cast<float*>(base + p.off_part) : nullptr;
+  g.hdr = reinterpret_cast<WsHeader*>(base + p.off_header);
+  g.R = p.K;
+  g.C = p.N;
+  g.T = p.T;
+  g.kspan = p.kspan;
+  g.P = p.P;
+  g.rank = p.rank;
+  if (p.dtype == PGG_F32) return launch_typed<TF32>(p, g, aligned, s);
+  return p.dtype == PGG_BF16 ? launch_typed<TBf16>(p, g, aligned, s) : launch_typed<TF16>(p, g, aligned, s);
+}
+
+}  // namespace pgg

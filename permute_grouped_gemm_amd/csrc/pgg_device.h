@@ -16,6 +16,26 @@ struct TF16 { using elem = uint16_t; static constexpr int kPerChunk = 8; };
 struct TF32 { using elem = float; static constexpr int kPerChunk = 4; };
 
 
+// One stored element widened to fp32 (exact), and fp32 rounded once to the
+// element type (to nearest even).
+template <class T> __device__ __forceinline__ float to_float(typename T::elem e);
+template <> __device__ __forceinline__ float to_float<TF32>(float e) { return e; }
+template <> __device__ __forceinline__ float to_float<TF16>(uint16_t e) {
+  return static_cast<float>(__builtin_bit_cast(_Float16, e));
+}
+template <> __device__ __forceinline__ float to_float<TBf16>(uint16_t e) {
+  return __builtin_bit_cast(float, static_cast<uint32_t>(e) << 16);
+}
+
+template <class T> __device__ __forceinline__ typename T::elem from_float(float v);
+template <> __device__ __forceinline__ float from_float<TF32>(float v) { return v; }
+template <> __device__ __forceinline__ uint16_t from_float<TF16>(float v) {
+  return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+}
+template <> __device__ __forceinline__ uint16_t from_float<TBf16>(float v) {
+  return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+}
+
 // Load one 16-byte chunk of a row (elements [n, n + kPerChunk)), zero outside
 // the row or past N.  NT: aligned chunks are loaded with the non-temporal
 // hint (data read once, such as a weight stream).

@@ -179,6 +179,37 @@ hipError_t launch_routing(const RoutePlan& p, const int64_t* ids, const void* x,
                           int64_t* eri_gather, int64_t* eri_scatter, void* expanded_x, void* ws,
                           bool vec, hipStream_t s);
 
+// The router's gate and its gradient (one launch each, no workspace).
+pgg_status check_gate_desc(const pgg_moe_gate_desc* desc);
+hipError_t launch_gate(const pgg_moe_gate_desc& d, const void* logits, const float* bias, int64_t* ids,
+                       float* probs, float* lse, hipStream_t s);
+hipError_t launch_gate_grad(const pgg_moe_gate_desc& d, const void* logits, const float* lse, const int64_t* ids,
+                            const float* grad_probs, const float* grad_lse, void* grad_logits, hipStream_t s);
+
+// Gated product of the experts: the forward's plan (N = reduction, K = 2F
+// columns) and tables; the gradient's plan has N = reduction D, K = F columns
+// and only the group tables.
+pgg_status make_glu_plan(const pgg_moe_glu_desc* desc, Plan* plan);
+hipError_t launch_glu(const Plan& p, int32_t act, const void* x, const void* weight, void* h, void* gate_up,
+                      bool aligned, const WsView& w, hipStream_t s);
+pgg_status make_glu_grad_plan(const pgg_moe_glu_grad_desc* desc, Plan* plan);
+hipError_t launch_glu_grad(const Plan& p, int32_t act, const void* grad_y, const void* weight, const void* gate_up,
+                           void* grad, void* h, bool aligned, const WsView& w, hipStream_t s);
+
+// Shared projection with low-rank adapters.
+enum LoraTile : int32_t { kLoraRows32 = 0, kLoraRows128 = 1, kLoraRows256 = 2 };
+constexpr int64_t kLoraFewTokens = 64;
+struct LoraPlan {
+  int64_t T, K, N, P;
+  int32_t rank, dtype, tile;
+  int32_t ksplit;       // reduction splits (1: none)
+  int64_t kspan;        // reduction elements per split
+  size_t off_header, off_z, off_part, total;
+};
+pgg_status make_lora_plan(const pgg_lora_desc* desc, LoraPlan* plan);
+hipError_t launch_lora(const LoraPlan& p, const void* x, const void* weight, const void* a, const void* b,
+                       const int64_t* ids, const float* scales, void* y, void* ws, bool aligned, hipStream_t s);
+
 // Forward grouped matmul with the permute gathered into the A operand:
 // y[i, :] = x[ori[i] / topK, :] · W[g(i)] for every m-tile of the plan.
 hipError_t launch_forward(const Plan& p, const void* x, const void* weight, float* y, bool aligned,

@@ -485,4 +485,126 @@ pgg_status make_dw_plan(const pgg_moe_fwd_desc* d, Plan* p) {
   return PGG_OK;
 }
 
+pgg_status check_gate_desc(const pgg_moe_gate_desc* d) {
+  if (!d || d->reserved != 0) return PGG_ERR_INVALID_ARG;
+  if (d->tokens <= 0 || d->experts <= 0 || d->topk <= 0 || d->topk > d->experts) return PGG_ERR_INVALID_ARG;
+  if (d->renorm != 0 && d->renorm != 1) return PGG_ERR_INVALID_ARG;
+  if (d->dtype < PGG_F32 || d->dtype > PGG_BF16) return PGG_ERR_INVALID_ARG;
+  // the picks of a row live in registers, and a launch of up to 64 lanes per
+  // row holds fewer than 2^32 lanes
+  if (d->experts > 8192 || d->topk > PGG_GATE_MAX_TOPK || d->tokens >= (int64_t(1) << 26))
+    return PGG_ERR_UNSUPPORTED;
+  return PGG_OK;
+}
+
+pgg_status make_glu_plan(const pgg_moe_glu_desc* d, Plan* p) {
+  if (!d || !p) return PGG_ERR_INVALID_ARG;
+  if (d->act != PGG_ACT_SILU && d->act != PGG_ACT_GELU_TANH) return PGG_ERR_INVALID_ARG;
+  if (d->weight_cols % 2 != 0) return PGG_ERR_INVALID_ARG;
+  pgg_moe_fwd_desc f = {};
+  f.x_rows = d->x_rows;
+  f.x_cols = d->x_cols;
+  f.weight_groups = d->weight_groups;
+  f.weight_rows = d->weight_rows;
+  f.weight_cols = d->weight_cols;
+  f.idx_len = d->idx_len;
+  f.group_list_len = d->group_list_len;
+  f.batch = d->batch;
+  f.topk = d->topk;
+  f.row_idx_type = d->row_idx_type;
+  f.x_dtype = d->x_dtype;
+  f.weight_dtype = d->weight_dtype;
+  const pgg_status st = make_fwd_plan(&f, p);
+  if (st != PGG_OK) return st;
+  // tiles of 128 rows and 128 columns where rows are not 16-byte aligned are four
+  // times as many as the plan's; a launch holds fewer than 2^32 lanes
+  if (int64_t(p->max_tiles) * p->n_col_tiles >= (int64_t(1) << 21)) return PGG_ERR_UNSUPPORTED;
+  return PGG_OK;
+}
+
+pgg_status make_glu_grad_plan(const pgg_moe_glu_grad_desc* d, Plan* p) {
+  if (!d || !p || d->reserved != 0) return PGG_ERR_INVALID_ARG;
+  if (d->act != PGG_ACT_SILU && d->act != PGG_ACT_GELU_TANH) return PGG_ERR_INVALID_ARG;
+  if (d->grad_y_dtype != d->weight_dtype) return PGG_ERR_INVALID_ARG;
+  if (d->grad_y_dtype < PGG_F32 || d->grad_y_dtype > PGG_BF16) return PGG_ERR_INVALID_ARG;
+  const int64_t M = d->grad_y_rows, D = d->grad_y_cols, G = d->weight_groups, F = d->weight_rows;
+  if (M <= 0 || D <= 0 || G <= 0 || F <= 0) return PGG_ERR_INVALID_ARG;
+  if (D != d->weight_cols || d->group_list_len != G) return PGG_ERR_INVALID_ARG;
+  if (M >= (int64_t(1) << 31) - 1 || G >= (int64_t(1) << 30) || D >= (int64_t(1) << 31) ||
+      F >= (int64_t(1) << 30))
+    return PGG_ERR_UNSUPPORTED;
+  Plan q{};
+  q.M = M; q.N = D; q.G = G; q.K = F; q.batch = M; q.topk = 1;
+  q.panel_cols = F;
+  q.dtype = d->grad_y_dtype;
+  q.regime = q.dtype == PGG_F32 ? kF32 : kLarge;
+  q.bm = M <= 64 * G ? 64 : 128;
+  q.bn = 128;
+  const int64_t max_tiles = (M + q.bm - 1) / q.bm + G;
+  const int64_t col_tiles = (F + q.bn - 1) / q.bn;
+  if (max_tiles * col_tiles >= (int64_t(1) << 23)) return PGG_ERR_UNSUPPORTED;   // fewer than 2^32 lanes
+  q.max_tiles = static_cast<int32_t>(max_tiles);
+  q.tc = q.max_tiles;
+  q.max_chunks = 1;
+  q.n_panels = 1;
+  q.n_col_tiles = static_cast<int32_t>(col_tiles);
+  q.ksplit = 1;
+  size_t off = 0;
+  q.off_header = off;   off = align_up(off + sizeof(WsHeader), kRegionAlign);
+  q.off_offsets = off;  off = align_up(off + sizeof(int64_t) * size_t(G + 1), kRegionAlign);
+  q.off_tiles = off;    off = align_up(off + sizeof(MTile) * size_t(q.max_tiles), kRegionAlign);
+  q.off_chunks = off;   off = align_up(off + sizeof(int32_t) * 2, kRegionAlign);
+  q.off_inv = q.off_ori = q.off_ring = off;
+  q.table_bytes = q.total = off;
+  *p = q;
+  return PGG_OK;
+}
+
+pgg_status make_lora_plan(const pgg_lora_desc* d, LoraPlan* p) {
+  if (!d || !p || d->reserved != 0) return PGG_ERR_INVALID_ARG;
+  if (d->tokens <= 0 || d->in_features <= 0 || d->out_features <= 0 || d->adapters <= 0 || d->rank <= 0)
+    return PGG_ERR_INVALID_ARG;
+  if (d->dtype < PGG_F32 || d->dtype > PGG_BF16) return PGG_ERR_INVALID_ARG;
+  if (d->tokens >= (int64_t(1) << 31) - 1 || d->in_features >= (int64_t(1) << 31) ||
+      d->out_features >= (int64_t(1) << 31) || d->adapters >= (int64_t(1) << 31) || d->rank > PGG_LORA_MAX_RANK)
+    return PGG_ERR_UNSUPPORTED;
+  LoraPlan q{};
+  q.T = d->tokens;
+  q.K = d->in_features;
+  q.N = d->out_features;
+  q.P = d->adapters;
+  q.rank = static_cast<int32_t>(d->rank);
+  q.dtype = d->dtype;
+  const bool f32 = q.dtype == PGG_F32;
+  auto tiles = [&](int64_t bm, int64_t bn) { return ((q.T + bm - 1) / bm) * ((q.N + bn - 1) / bn); };
+  int64_t count;
+  if (q.T <= kLoraFewTokens) {
+    q.tile = kLoraRows32;
+    count = tiles(32, f32 ? 128 : 256);
+  } else if (!f32 && tiles(256, 256) >= 160) {
+    q.tile = kLoraRows256;
+    count = tiles(256, 256);
+  } else {
+    q.tile = kLoraRows128;
+    count = tiles(128, 128);
+  }
+  if (tiles(32, 128) >= (int64_t(1) << 23)) return PGG_ERR_UNSUPPORTED;   // launches of fewer than 2^32 lanes
+  // Splits of the reduction until about 512 workgroups stream (two per compute
+  // unit), each of at least 256 elements.
+  constexpr int64_t kStage = 64, kMinSpan = 256, kTarget = 512;
+  int64_t split = q.tile == kLoraRows256 ? 1 : std::min<int64_t>(kTarget / count, q.K / kMinSpan);
+  split = std::max<int64_t>(1, std::min<int64_t>(split, 64));
+  q.kspan = ((q.K + split - 1) / split + kStage - 1) / kStage * kStage;
+  q.ksplit = static_cast<int32_t>((q.K + q.kspan - 1) / q.kspan);
+  size_t off = 0;
+  q.off_header = off; off = align_up(off + sizeof(WsHeader), kRegionAlign);
+  q.off_z = off;      off = align_up(off + sizeof(float) * size_t(q.T) * size_t(q.rank), kRegionAlign);
+  q.off_part = off;
+  if (q.ksplit > 1)
+    off = align_up(off + sizeof(float) * size_t(q.ksplit) * size_t(q.T) * size_t(q.N), kRegionAlign);
+  q.total = off;
+  *p = q;
+  return PGG_OK;
+}
+
 }  // namespace pgg
