@@ -20,7 +20,7 @@
 #include <algorithm>
 
 #include "pgg_act.h"
-#include "pgg_nn.h"
+#include "pgg_pipe.h"
 
 namespace pgg {
 
@@ -66,20 +66,23 @@ struct GluOp {
     return static_cast<int64_t>(t.g) * a.R * a.C;
   }
 
-  // column f of the pair that column n of the tile belongs to
-  template <int BN>
-  static __device__ __forceinline__ int64_t pair(int ct, int n) {
-    return static_cast<int64_t>(ct) * (BN / 2) + (n >> 6) * 32 + (n & 31);
-  }
+  static constexpr bool kPaired = true;
+  static __device__ __forceinline__ int64_t src_base(const Args&, const MTile&) { return 0; }
+  static __device__ __forceinline__ int64_t first_column(int ct, int bn) { return static_cast<int64_t>(ct) * (bn / 2); }
 
   template <int BN>
   static __device__ __forceinline__ ColumnRun column(const Args& a, int ct, int n) {
-    const int64_t f = pair<BN>(ct, n);
+    const int64_t f = first_column(ct, BN) + (n >> 6) * 32 + (n & 31);
     return {f + ((n >> 5) & 1) * a.F, a.F - f};
   }
 
-  template <class T, int BN, int FM, int FN>
-  static __device__ __forceinline__ void store(const Args& a, const MTile& t, int ct, int m0, int n0, int lane,
+  // run j (0: gate, 1: up), column n; past the end: a valid one, not stored
+  static __device__ __forceinline__ int64_t half_column(const Args& a, int ct, int j, int n) {
+    return j * a.F + min<int64_t>(first_column(ct, 256) + n, a.F - 8);
+  }
+
+  template <class T, int FM, int FN>
+  static __device__ __forceinline__ void store(const Args& a, const MTile& t, int64_t c, int step, int m0, int lane,
                                                const f32x16_t (&acc)[FM][FN]) {
     using E = typename T::elem;
     const int lr = lane & 31, lh = lane >> 5;
@@ -88,24 +91,29 @@ struct GluOp {
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < FN; j += 2) {
-        const int64_t f = pair<BN>(ct, n0 + j * 32 + lr);
-        if (f >= a.F) continue;
+        const int64_t f = c + j / 2 * step;
+        const int m = m0 + i * 32 + lr;
+        const int64_t left = m < t.rows ? a.F - f : 0;
+        const int64_t row = t.row0 + m;
+        float gate[16], up[16], h[16];
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
-          const int m = m0 + i * 32 + acc_row(v, lh);
-          if (m >= t.rows) continue;
-          const int64_t row = t.row0 + m;
-          const float gate = acc[i][j][v], up = acc[i][j + 1][v];
-          if (a.part) {
-            a.part[(split + row) * a.C + f] = gate;
-            a.part[(split + row) * a.C + a.F + f] = up;
-            continue;
-          }
-          static_cast<E*>(a.h)[row * a.F + f] = from_float<T>(activate<ACT>(gate) * up);
-          if (a.gate_up) {
-            static_cast<E*>(a.gate_up)[row * a.C + f] = from_float<T>(gate);
-            static_cast<E*>(a.gate_up)[row * a.C + a.F + f] = from_float<T>(up);
-          }
+          gate[v] = acc[i][j][v];
+          up[v] = acc[i][j + 1][v];
+        }
+        if (a.part) {
+          float* p = a.part + (split + row) * a.C + f;
+          store_block<TF32>(p, left, gate, lh);
+          store_block<TF32>(p + a.F, left, up, lh);
+          continue;
+        }
+#pragma unroll
+        for (int v = 0; v < 16; ++v) h[v] = activate<ACT>(gate[v]) * up[v];
+        store_block<T>(static_cast<E*>(a.h) + row * a.F + f, left, h, lh);
+        if (a.gate_up) {
+          E* p = static_cast<E*>(a.gate_up) + row * a.C + f;
+          store_block<T>(p, left, gate, lh);
+          store_block<T>(p + a.F, left, up, lh);
         }
       }
   }
@@ -144,10 +152,12 @@ hipError_t launch_reg(const Plan& p, GluArgs a, hipStream_t s) {
 template <class T, int ACT>
 hipError_t launch_16(const Plan& p, GluArgs a, bool aligned, hipStream_t s) {
   if (p.regime == kStream) return launch_reg<T, 32, 256, 1, 4, 2, ACT>(p, a, s);
-  if (!aligned) return launch_reg<T, 128, 128, 2, 2, 2, ACT>(p, a, s);
+  // the pipeline's 32-bit byte offsets: into all of x, and into 64 rows of W
+  if (!aligned || p.batch * a.R >= (int64_t(1) << 31) || a.C >= (int64_t(1) << 25))
+    return launch_reg<T, 128, 128, 2, 2, 2, ACT>(p, a, s);
   a.n_slots = p.max_tiles;
   a.n_col_tiles = static_cast<int32_t>((a.F + 127) / 128);
-  return launch_nn_dma<T, GluOp<ACT>>(a, s);
+  return launch_pipe<T, GluOp<ACT>, false>(a, s);
 }
 
 template <class T, int ACT>

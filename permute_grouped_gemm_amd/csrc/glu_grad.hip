@@ -13,58 +13,84 @@
 // operands take, so tiles are staged in LDS as rows of 16-byte chunks, chunk c
 // of row r at c ^ ((r >> 1) & 7).
 #include "pgg_act.h"
-#include "pgg_nn.h"
+#include "pgg_pipe.h"
 
 namespace pgg {
 
 namespace {
 
 struct GluGradArgs {
-  const void* A;            // grad_y [M, D]
-  const void* B;            // weight [G, F, D]
-  const void* gate_up;      // [M, 2F]
+  const void* A;            // grad_y [M, R]
+  const void* W;            // weight [G, F, R]
+  const void* gate_up;      // [M, C]
   const WsHeader* hdr;
   const MTile* tiles;
-  void* grad;               // [M, 2F]
+  void* grad;               // [M, C]
   void* h;                  // [M, F] or NULL
-  int64_t D, F;
+  int64_t R, C, F;
   int32_t bm;               // rows of a table entry
   int32_t n_slots, n_col_tiles;
 };
 
-template <class T, int ACT, int FM, int FN>
-__device__ __forceinline__ void store_grad(const GluGradArgs& a, const MTile& t, int64_t col0, int m0, int n0,
-                                           int lane, const f32x16_t (&acc)[FM][FN]) {
-  using E = typename T::elem;
-  const int lr = lane & 31, lh = lane >> 5;
-  const int64_t C = 2 * a.F;
+template <int ACT>
+struct GluGradOp {
+  using Args = GluGradArgs;
+  static constexpr bool kPaired = false;
+
+  template <int BM>
+  static __device__ __forceinline__ bool tile(const Args& a, int slot, MTile& t) {
+    if (a.hdr->err != kNoError) return false;
+    const int sub = a.bm / BM;   // tiles to a table entry
+    const int entry = slot / sub;
+    if (entry >= a.hdr->n_tiles) return false;
+    t = a.tiles[entry];
+    const int skip = (slot - entry * sub) * BM;
+    t.row0 += skip;
+    t.rows = min(t.rows - skip, BM);
+    return t.rows > 0;
+  }
+
+  static __device__ __forceinline__ int64_t src_base(const Args&, const MTile& t) { return t.row0; }
+  static __device__ __forceinline__ int64_t src(const Args&, const MTile& t, int r) { return int64_t(t.row0) + r; }
+  static __device__ __forceinline__ int64_t weight(const Args& a, const MTile& t) { return t.g * a.F * a.R; }
+  static __device__ __forceinline__ int64_t first_column(int ct, int bn) { return static_cast<int64_t>(ct) * bn; }
+
+  template <class T, int FM, int FN>
+  static __device__ __forceinline__ void store(const Args& a, const MTile& t, int64_t c, int step, int m0, int lane,
+                                               const f32x16_t (&acc)[FM][FN]) {
+    using E = typename T::elem;
+    const int lr = lane & 31, lh = lane >> 5;
 #pragma unroll
-  for (int i = 0; i < FM; ++i)
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int64_t f = col0 + n0 + j * 32 + lr;
-      if (f >= a.F) continue;
+      for (int j = 0; j < FN; ++j) {
+        const int64_t f = c + j * step;
+        const int m = m0 + i * 32 + lr;
+        const int64_t left = m < t.rows ? a.F - f : 0;
+        const int64_t row = t.row0 + m, at = row * a.C + f;
+        float gate[16], up[16], h[16];
+        load_block<T>(static_cast<const E*>(a.gate_up) + at, left, gate, lh);
+        load_block<T>(static_cast<const E*>(a.gate_up) + at + a.F, left, up, lh);
 #pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int m = m0 + i * 32 + acc_row(v, lh);
-        if (m >= t.rows) continue;
-        const int64_t row = t.row0 + m;
-        const E* gu = static_cast<const E*>(a.gate_up) + row * C + f;
-        const float up = to_float<T>(gu[a.F]), dh = acc[i][j][v];
-        float value, slope;
-        activate_grad<ACT>(to_float<T>(gu[0]), value, slope);
-        E* g = static_cast<E*>(a.grad) + row * C + f;
-        g[0] = from_float<T>(dh * up * slope);
-        g[a.F] = from_float<T>(dh * value);
-        if (a.h) static_cast<E*>(a.h)[row * a.F + f] = from_float<T>(value * up);
+        for (int v = 0; v < 16; ++v) {
+          const float dh = acc[i][j][v];
+          float value, slope;
+          activate_grad<ACT>(gate[v], value, slope);
+          gate[v] = dh * up[v] * slope;
+          h[v] = value * up[v];
+          up[v] = dh * value;
+        }
+        store_block<T>(static_cast<E*>(a.grad) + at, left, gate, lh);
+        store_block<T>(static_cast<E*>(a.grad) + at + a.F, left, up, lh);
+        if (a.h) store_block<T>(static_cast<E*>(a.h) + row * a.F + f, left, h, lh);
       }
-    }
-}
+  }
+};
 
 // Through registers: every type and alignment.  Rows and columns past the
 // tile's repeat valid ones and are not stored; elements past the reduction are
 // zero in both operands.
-template <class T, int BM, int BN, int WM, int WN, int EU, int ACT>
+template <class T, class Op, int BM, int BN, int WM, int WN, int EU>
 __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(EU, EU)))
 void glu_grad_reg_kernel(GluGradArgs a) {
   using E = typename T::elem;
@@ -80,18 +106,12 @@ void glu_grad_reg_kernel(GluGradArgs a) {
   static_assert(A_CHUNKS % NT == 0 && B_CHUNKS % NT == 0, "a stage splits evenly");
   __shared__ u32x4_t lds[2][A_CHUNKS + B_CHUNKS];
 
-  if (a.hdr->err != kNoError) return;
   int slot, ct;
   if (!raster<8, 4>(blockIdx.x, a.n_slots, a.n_col_tiles, slot, ct)) return;
-  const int sub = a.bm / BM;
-  const int entry = slot / sub;
-  if (entry >= a.hdr->n_tiles) return;
-  MTile tile = a.tiles[entry];
-  tile.row0 += (slot - entry * sub) * BM;
-  tile.rows = min(tile.rows - (slot - entry * sub) * BM, BM);
-  if (tile.rows <= 0) return;
-  const int64_t col0 = static_cast<int64_t>(ct) * BN;
-  const int64_t D = a.D;
+  MTile tile;
+  if (!Op::template tile<BM>(a, slot, tile)) return;
+  const int64_t col0 = Op::first_column(ct, BN);
+  const int64_t D = a.R;
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -104,14 +124,13 @@ void glu_grad_reg_kernel(GluGradArgs a) {
 #pragma unroll
   for (int s = 0; s < A_PER_T; ++s) {
     const int q = tid + s * NT;
-    arow[s] = static_cast<const E*>(a.A) + (tile.row0 + static_cast<int64_t>(min(q / kChunks, tile.rows - 1))) * D +
-              (q % kChunks) * EPC;
+    arow[s] = static_cast<const E*>(a.A) + Op::src(a, tile, min(q / kChunks, tile.rows - 1)) * D + (q % kChunks) * EPC;
   }
 #pragma unroll
   for (int s = 0; s < B_PER_T; ++s) {
     const int q = tid + s * NT;
     const int64_t f = min<int64_t>(col0 + q / kChunks, a.F - 1);
-    brow[s] = static_cast<const E*>(a.B) + (tile.g * a.F + f) * D + (q % kChunks) * EPC;
+    brow[s] = static_cast<const E*>(a.W) + Op::weight(a, tile) + f * D + (q % kChunks) * EPC;
   }
 
   u32x4_t ra[A_PER_T], rb[B_PER_T];
@@ -171,7 +190,7 @@ void glu_grad_reg_kernel(GluGradArgs a) {
 #pragma unroll
       for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < FN; ++j) mma<T>(acc[i][j], fa[q & 1][i], fb[q & 1][j]);
+        for (int j = 0; j < FN; ++j) mma<T>(acc[i][j], fb[q & 1][j], fa[q & 1][i]);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -186,29 +205,38 @@ void glu_grad_reg_kernel(GluGradArgs a) {
     if (kt + 1 < nk) store_stage((kt & 1) ^ 1);
     __syncthreads();
   }
-  store_grad<T, ACT, FM, FN>(a, tile, col0, wm * WTM, wn * WTN, lane, acc);
+  Op::template store<T, FM, FN>(a, tile, col0 + wn * WTN, 32, wm * WTM, lane, acc);
 }
 
-template <class T, int BM, int BN, int WM, int WN, int EU, int ACT>
+template <class T, int BM, int ACT>
 hipError_t launch_reg(const Plan& p, GluGradArgs a, hipStream_t s) {
+  constexpr int BN = 128;
   a.n_slots = p.max_tiles * (p.bm / BM);
   a.n_col_tiles = static_cast<int32_t>((a.F + BN - 1) / BN);
   unsigned tiles = static_cast<unsigned>(a.n_slots) * static_cast<unsigned>(a.n_col_tiles);
   tiles = (tiles + 8 * 32 - 1) / (8 * 32) * (8 * 32);
-  hipLaunchKernelGGL((glu_grad_reg_kernel<T, BM, BN, WM, WN, EU, ACT>), dim3(tiles), dim3(WM * WN * 64), 0, s, a);
+  hipLaunchKernelGGL((glu_grad_reg_kernel<T, GluGradOp<ACT>, BM, BN, 2, 2, 2>), dim3(tiles), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
 template <class T, int ACT>
-hipError_t launch_typed(const Plan& p, const GluGradArgs& a, hipStream_t s) {
-  if (p.bm == 64) return launch_reg<T, 64, 128, 2, 2, 2, ACT>(p, a, s);
-  return launch_reg<T, 128, 128, 2, 2, 2, ACT>(p, a, s);
+hipError_t launch_typed(const Plan& p, GluGradArgs a, bool aligned, hipStream_t s) {
+  if (p.bm == 64) return launch_reg<T, 64, ACT>(p, a, s);
+  if constexpr (T::kPerChunk == 8) {
+    // the pipeline's 32-bit byte offsets: into 256 rows of either operand
+    if (aligned && p.bm == 256 && a.R < (int64_t(1) << 23)) {
+      a.n_slots = p.max_tiles;
+      a.n_col_tiles = static_cast<int32_t>((a.F + 255) / 256);
+      return launch_pipe<T, GluGradOp<ACT>, true>(a, s);
+    }
+  }
+  return launch_reg<T, 128, ACT>(p, a, s);
 }
 
 template <int ACT>
-hipError_t launch_act(const Plan& p, const GluGradArgs& a, hipStream_t s) {
-  if (p.dtype == PGG_F32) return launch_typed<TF32, ACT>(p, a, s);
-  return p.dtype == PGG_BF16 ? launch_typed<TBf16, ACT>(p, a, s) : launch_typed<TF16, ACT>(p, a, s);
+hipError_t launch_act(const Plan& p, const GluGradArgs& a, bool aligned, hipStream_t s) {
+  if (p.dtype == PGG_F32) return launch_typed<TF32, ACT>(p, a, aligned, s);
+  return p.dtype == PGG_BF16 ? launch_typed<TBf16, ACT>(p, a, aligned, s) : launch_typed<TF16, ACT>(p, a, aligned, s);
 }
 
 }  // namespace
@@ -217,17 +245,18 @@ hipError_t launch_glu_grad(const Plan& p, int32_t act, const void* grad_y, const
                            void* grad, void* h, bool aligned, const WsView& w, hipStream_t s) {
   GluGradArgs a;
   a.A = grad_y;
-  a.B = weight;
+  a.W = weight;
   a.gate_up = gate_up;
   a.hdr = w.hdr;
   a.tiles = w.tiles;
   a.grad = grad;
   a.h = h;
-  a.D = p.N;          // the plan keeps the reduction in N and the columns in K
+  a.R = p.N;          // the plan keeps the reduction in N and the columns in K
   a.F = p.K;
+  a.C = 2 * p.K;
   a.bm = p.bm;
-  (void)aligned;
-  return act == PGG_ACT_SILU ? launch_act<PGG_ACT_SILU>(p, a, s) : launch_act<PGG_ACT_GELU_TANH>(p, a, s);
+  return act == PGG_ACT_SILU ? launch_act<PGG_ACT_SILU>(p, a, aligned, s)
+                             : launch_act<PGG_ACT_GELU_TANH>(p, a, aligned, s);
 }
 
 }  // namespace pgg

@@ -30,7 +30,7 @@
 // split order and the tokens' z * B_p.
 #include <algorithm>
 
-#include "pgg_nn.h"
+#include "pgg_pipe.h"
 #include "pgg_prep.h"
 
 namespace pgg {
@@ -77,6 +77,9 @@ __device__ void check_ids(const LoraArgs& a) {
     if (bad != ~0ull) set_error(a.hdr, PGG_DEV_ADAPTER_RANGE, static_cast<long long>(bad));
   }
 }
+
+// Row of accumulator v in a 32 x 32 block (its column is the lane's place in its half).
+__device__ __forceinline__ int acc_row(int v, int lh) { return 8 * (v >> 2) + 4 * lh + (v & 3); }
 
 // ---------------------------------------------------------------- z, many tokens
 
@@ -209,13 +212,22 @@ struct LoraOp {
   static __device__ __forceinline__ int64_t src(const Args&, const MTile& t, int r) { return int64_t(t.row0) + r; }
   static __device__ __forceinline__ int64_t weight(const Args&, const MTile&) { return 0; }
 
+  static constexpr bool kPaired = false;
+  static __device__ __forceinline__ int64_t src_base(const Args&, const MTile& t) { return t.row0; }
+  static __device__ __forceinline__ int64_t first_column(int ct, int bn) { return static_cast<int64_t>(ct) * bn; }
+
+  // past the end: a valid column, not stored
+  static __device__ __forceinline__ int64_t half_column(const Args& a, int ct, int j, int n) {
+    return min<int64_t>(first_column(ct, 256) + j * 128 + n, a.C - 8);
+  }
+
   template <int BN>
   static __device__ __forceinline__ ColumnRun column(const Args& a, int ct, int n) {
     const int64_t c = static_cast<int64_t>(ct) * BN + n;
     return {c, a.C - c};
   }
 
-  // rows t (this lane: zrow) times columns c of adapter p, all ranks
+  // 32 rows of z (this lane's: zrow) times 32 columns of adapter p (this lane's: c), all ranks
   template <class T>
   static __device__ __forceinline__ f32x16_t expand(const Args& a, const float* zrow, int32_t p, int64_t c, int lh) {
     using E = typename T::elem;
@@ -236,9 +248,9 @@ struct LoraOp {
         u32x4_t zh, zl, bh, bl;
         split_bf16(zv, zh, zl);
         split_bf16(bv, bh, bl);
-        mma<TBf16>(d, zh, bh);
-        mma<TBf16>(d, zl, bh);
-        if constexpr (__is_same(T, TF16)) mma<TBf16>(d, zh, bl);
+        mma<TBf16>(d, bh, zh);
+        mma<TBf16>(d, bh, zl);
+        if constexpr (__is_same(T, TF16)) mma<TBf16>(d, bl, zh);
       }
     } else {
       for (int r = 0; r < a.rank; r += 8) {
@@ -249,61 +261,50 @@ struct LoraOp {
           fz[e] = __builtin_bit_cast(uint32_t, k < a.rank ? zrow[k] : 0.0f);
           fb[e] = __builtin_bit_cast(uint32_t, ok && k < a.rank ? b[static_cast<int64_t>(k) * a.C] : 0.0f);
         }
-        mma<T>(d, fz, fb);
+        mma<T>(d, fb, fz);
       }
     }
     return d;
   }
 
-  template <class T, int BN, int FM, int FN>
-  static __device__ __forceinline__ void store(const Args& a, const MTile& t, int ct, int m0, int n0, int lane,
+  template <class T, int FM, int FN>
+  static __device__ __forceinline__ void store(const Args& a, const MTile& t, int64_t c0, int step, int m0, int lane,
                                                f32x16_t (&acc)[FM][FN]) {
     using E = typename T::elem;
     const int lr = lane & 31, lh = lane >> 5;
-    const int64_t c0 = static_cast<int64_t>(ct) * BN + n0 + lr;
-    if (a.part) {
-      float* out = a.part + (static_cast<int64_t>(blockIdx.y) * a.T + t.row0) * a.C;
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-          for (int v = 0; v < 16; ++v) {
-            const int m = m0 + i * 32 + acc_row(v, lh);
-            if (m < t.rows && c0 + j * 32 < a.C) out[m * a.C + c0 + j * 32] = acc[i][j][v];
-          }
-      return;
-    }
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       const int m = m0 + i * 32 + lr;
-      const int32_t id = m < t.rows ? adapter_of(a, int64_t(t.row0) + m) : -1;
-      const float* zrow = a.z + (int64_t(t.row0) + min(m, t.rows - 1)) * a.rank;
-      uint32_t pending = static_cast<uint32_t>(__ballot(id >= 0));
-      while (pending) {
-        const int32_t p = __shfl(id, __builtin_ctz(pending));
-        const uint32_t mine = static_cast<uint32_t>(__ballot(id == p));
-        pending &= ~mine;
+      const int64_t token = int64_t(t.row0) + m;
+      if (!a.part) {
+        const int32_t id = m < t.rows ? adapter_of(a, token) : -1;
+        const float* zrow = a.z + (int64_t(t.row0) + min(m, t.rows - 1)) * a.rank;
+        uint32_t pending = static_cast<uint32_t>(__ballot(id >= 0));
+        while (pending) {
+          const int32_t p = __shfl(id, __builtin_ctz(pending));
+          pending &= ~static_cast<uint32_t>(__ballot(id == p));
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          const f32x16_t d = expand<T>(a, zrow, p, c0 + j * 32, lh);
+          for (int j = 0; j < FN; ++j) {
+            const f32x16_t d = expand<T>(a, zrow, p, c0 + j * step + lr, lh);
 #pragma unroll
-          for (int v = 0; v < 16; ++v)
-            if ((mine >> acc_row(v, lh)) & 1) acc[i][j][v] += d[v];
+            for (int v = 0; v < 16; ++v)
+              if (id == p) acc[i][j][v] += d[v];
+            __builtin_amdgcn_sched_barrier(0);   // one block at a time: registers
+          }
         }
       }
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int64_t c = c0 + j * step, left = m < t.rows ? a.C - c : 0;
+        float y[16];
+#pragma unroll
+        for (int v = 0; v < 16; ++v) y[v] = acc[i][j][v];
+        if (a.part)
+          store_block<TF32>(a.part + (static_cast<int64_t>(blockIdx.y) * a.T + token) * a.C + c, left, y, lh);
+        else
+          store_block<T>(static_cast<E*>(a.y) + token * a.C + c, left, y, lh);
+      }
     }
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; ++j)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          const int m = m0 + i * 32 + acc_row(v, lh);
-          const int64_t c = c0 + j * 32;
-          if (m < t.rows && c < a.C)
-            static_cast<E*>(a.y)[(int64_t(t.row0) + m) * a.C + c] = from_float<T>(acc[i][j][v]);
-        }
   }
 };
 
@@ -348,10 +349,11 @@ hipError_t launch_typed(const LoraPlan& p, LoraArgs a, bool aligned, hipStream_t
   if constexpr (T::kPerChunk == 8) {
     if (p.tile == kLoraRows32) {
       e = launch_tiles<T, 32, 256, 1, 4>(a, p, s);
-    } else if (p.tile == kLoraRows256 && aligned) {
+    } else if (p.tile == kLoraRows256 && aligned && a.R < (int64_t(1) << 23) && a.C < (int64_t(1) << 25)) {
+      // (32-bit byte offsets into 256 rows of x and 64 rows of W)
       a.n_slots = static_cast<int32_t>((a.T + 255) / 256);
       a.n_col_tiles = static_cast<int32_t>((a.C + 255) / 256);
-      e = launch_nn_dma<T, LoraOp>(a, s);
+      e = launch_pipe<T, LoraOp, false>(a, s);
     } else {
       e = launch_tiles<T, 128, 128, 2, 2>(a, p, s);
     }

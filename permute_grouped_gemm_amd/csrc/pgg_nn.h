@@ -13,11 +13,21 @@
 //   Op::weight(args, t)      first element of the tile's W
 //   Op::column<BN>(args, ct, n)  column of W at column n (a multiple of 4) of
 //                            the tile, and how many of W's columns follow in that run
-//   Op::store<...>(...)      takes the accumulators
+//   Op::first_column(ct, bn) output column of the tile's first one
+//   Op::kPaired              blocks of 32 columns belong together two by two and
+//                            make 32 output columns
+//   Op::store<T, FM, FN>(args, t, c, step, m0, lane, acc)
+//                            takes the accumulators: output column c of the
+//                            wave's first block, the step from one block (or
+//                            pair) to the next, the wave's first tile row m0
 //
-// Two kernels: nn_dma_kernel (16-bit types, 16-byte aligned rows, 256 x 256
-// tiles loaded straight into LDS) and nn_reg_kernel (every type and alignment,
-// loads through registers, any tile).
+// The matrix instructions get the columns as their first operand, so that a
+// lane ends with 16 columns of one row of a 32 x 32 block: lane (lr, lh) has
+// row lr, and accumulator v is column 8 (v / 4) + 4 lh + v % 4.  Rows are then
+// stored in pieces of 16 bytes (store_block).
+//
+// nn_reg_kernel takes every type and alignment (loads through registers, any
+// tile); pgg_pipe.h has the kernel for many rows of aligned 16-bit data.
 //
 // Operand layouts in LDS.  An A row is contiguous along k, which is what an
 // MFMA operand wants (a lane takes 16 bytes of one row): rows of 8 chunks of
@@ -101,6 +111,91 @@ __device__ __forceinline__ u32x4_t read_w(const char* base, int q, int n, int la
     for (int t = 0; t < 4; ++t)
       v[t] = *reinterpret_cast<const uint32_t*>(base + w_offset<T, ROW>(k + t, (n + (lane & 31)) * 4));
     return v;
+  }
+}
+
+// A row of a 32 x 32 block between accumulators and memory.  fp32: the four
+// columns of accumulators 4 p .. 4 p + 3 are piece p.  16 bits: the halves of
+// the wave exchange every other group of four, so that a lane of the lower half
+// has 8 successive columns from 16 p on and one of the upper half from 16 p + 8.
+template <class T>
+__device__ __forceinline__ int piece_column(int p, int lh) {
+  return T::kPerChunk == 8 ? 16 * p + 8 * lh : 8 * p + 4 * lh;
+}
+
+// What the upper half of the wave holds in x for what the lower one holds in y.
+__device__ __forceinline__ void exchange_halves(uint32_t& x, uint32_t& y) {
+  const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+  x = r[0];
+  y = r[1];
+}
+
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  return static_cast<uint32_t>(from_float<T>(lo)) | (static_cast<uint32_t>(from_float<T>(hi)) << 16);
+}
+
+// Stores this lane's part of a block row that starts at p, of which `left`
+// columns exist (0 or less: none, for a row past the tile).  Every lane of the
+// wave takes part.
+template <class T>
+__device__ __forceinline__ void store_block(typename T::elem* p, int64_t left, const float (&val)[16], int lh) {
+  using E = typename T::elem;
+  constexpr int W = T::kPerChunk;
+#pragma unroll
+  for (int q = 0; q < 32 / (2 * W); ++q) {
+    u32x4_t v;
+    if constexpr (W == 8) {
+      uint32_t x[2], y[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        x[e] = pack2<T>(val[8 * q + 2 * e], val[8 * q + 2 * e + 1]);
+        y[e] = pack2<T>(val[8 * q + 4 + 2 * e], val[8 * q + 5 + 2 * e]);
+        exchange_halves(x[e], y[e]);
+      }
+      v = u32x4_t{x[0], x[1], y[0], y[1]};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __builtin_bit_cast(uint32_t, val[4 * q + e]);
+    }
+    const int c = piece_column<T>(q, lh);
+    if (left >= c + W) {
+      __builtin_memcpy(p + c, &v, 16);
+    } else if (left > c) {
+      E e[W];
+      __builtin_memcpy(e, &v, 16);
+#pragma unroll
+      for (int t = 0; t < W; ++t)
+        if (c + t < left) p[c + t] = e[t];
+    }
+  }
+}
+
+// The reverse: accumulator order from memory; what does not exist is 0.
+template <class T>
+__device__ __forceinline__ void load_block(const typename T::elem* p, int64_t left, float (&val)[16], int lh) {
+  using E = typename T::elem;
+  constexpr int W = T::kPerChunk;
+#pragma unroll
+  for (int q = 0; q < 32 / (2 * W); ++q) {
+    const int c = piece_column<T>(q, lh);
+    u32x4_t v = load16_part<T>(p + c, left - c);
+    if constexpr (W == 8) {
+      uint32_t d[4] = {v[0], v[1], v[2], v[3]};
+      exchange_halves(d[0], d[2]);
+      exchange_halves(d[1], d[3]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        val[8 * q + 2 * e] = to_float<T>(static_cast<E>(d[e] & 0xFFFFu));
+        val[8 * q + 2 * e + 1] = to_float<T>(static_cast<E>(d[e] >> 16));
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t u = v[e];
+        val[4 * q + e] = __builtin_bit_cast(float, u);
+      }
+    }
   }
 }
 
@@ -224,7 +319,7 @@ void nn_reg_kernel(typename Op::Args a) {
 #pragma unroll
       for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < FN; ++j) mma<T>(acc[i][j], fa[q & 1][i], fb[q & 1][j]);
+        for (int j = 0; j < FN; ++j) mma<T>(acc[i][j], fb[q & 1][j], fa[q & 1][i]);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -239,7 +334,8 @@ void nn_reg_kernel(typename Op::Args a) {
     if (kt + 1 < nk) store_stage((kt & 1) ^ 1);
     __syncthreads();
   }
-  Op::template store<T, BN, FM, FN>(a, tile, ct, wm * WTM, wn * WTN, lane, acc);
+  Op::template store<T, FM, FN>(a, tile, Op::first_column(ct, BN) + wn * (Op::kPaired ? WTN / 2 : WTN), 32,
+                                wm * WTM, lane, acc);
 }
 
 template <class T, class Op, int BM, int BN, int WM, int WN, int EU>
@@ -250,155 +346,6 @@ hipError_t launch_nn_reg(const typename Op::Args& a, int ksplit, hipStream_t s) 
                      dim3(WM * WN * 64), 0, s, a);
   return hipGetLastError();
 }
-
-// ---------------------------------------------------------------------------
-// Straight into LDS (16-bit types, every row 16-byte aligned): 256 x 256
-// tiles, 8 waves (two per SIMD) of 128 x 64 accumulators, two LDS stages of 64
-// k (128 bytes of every A row, 512 bytes of 64 W rows; 128 KiB in all), loads
-// that write no register and explicit waits on their counter.  The refill of
-// a stage is issued by the first wave of each SIMD right after the stage
-// barrier and by the second after its last MFMAs, so one of the two always
-// feeds the matrix unit.  Lanes with nothing to load read 16 zero bytes.
-// ---------------------------------------------------------------------------
-template <class T, class Op>
-__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
-void nn_dma_kernel(typename Op::Args a) {
-  using E = typename T::elem;
-  constexpr int BM = 256, BN = 256, NT = 512, kWaves = 8, WM = 2;
-  constexpr int WTM = 128, WTN = 64, FM = 4, FN = 2;
-  constexpr int kChunks = 8, BK = 64, kPairs = kChunks / 2, kStages = 2;
-  constexpr int ROW = BN * 2, kRowChunks = ROW / 16;
-  constexpr int kSlotsA = BM * kChunks, kStageSlots = kSlotsA + BK * kRowChunks;
-  constexpr int kLoadsA = kSlotsA / NT, kLoadsB = BK * kRowChunks / NT;
-  __shared__ u32x4_t lds[kStages * kStageSlots];
-
-  int slot, ct;
-  if (!raster<8, 4>(blockIdx.x, a.n_slots, a.n_col_tiles, slot, ct)) return;
-  MTile tile;
-  if (!Op::template tile<BM>(a, slot, tile)) return;
-  const int rows = tile.rows;
-  const int64_t R = a.R, C = a.C;
-
-  const int tid = threadIdx.x;
-  const int lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave % WM, wn = wave / WM;
-  const int lr = lane & 31, lh = lane >> 5;
-
-  // A: load j of this lane fills row r0 + 64 j, slot lane % 8, which holds
-  // chunk dma_c (the same for every j).
-  const int r0 = wave * 8 + (lane >> 3);
-  const int dma_c = a_slot(r0, lane & 7);
-  const E* pa[kLoadsA];
-#pragma unroll
-  for (int j = 0; j < kLoadsA; ++j)
-    pa[j] = static_cast<const E*>(a.A) + Op::src(a, tile, min(r0 + 64 * j, rows - 1)) * R + dma_c * 8;
-  // W: load j fills stage row kb_j (two rows to a wave instruction), chunk
-  // lane % 32, which holds logical chunk lc_j.
-  const E* W = static_cast<const E*>(a.W) + Op::weight(a, tile);
-  int64_t boff[kLoadsB];
-  uint32_t vb = 0;
-#pragma unroll
-  for (int j = 0; j < kLoadsB; ++j) {
-    const int kb = (j * kWaves + wave) * 2 + lane / kRowChunks;
-    const int pc = lane % kRowChunks;
-    const int lc = (((pc >> 2) ^ (kb & 3)) << 2) | (pc & 3);
-    const ColumnRun run = Op::template column<BN>(a, ct, lc * 8);
-    boff[j] = kb * C + run.first;
-    vb |= (run.left > 0 ? 1u : 0u) << j;
-  }
-  const void* zero = &kZero16;
-  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(lds));
-
-  auto issue = [&](int kt) {
-    const uint32_t base = lds0 + static_cast<uint32_t>((kt % kStages) * kStageSlots * 16);
-    const int64_t k0 = static_cast<int64_t>(kt) * BK;
-    const bool in_k = k0 + dma_c * 8 < R;
-#pragma unroll
-    for (int j = 0; j < kLoadsA; ++j)
-      dma16(in_k ? static_cast<const void*>(pa[j] + k0) : zero,
-            base + static_cast<uint32_t>((j * kWaves + wave) * 64 * 16));
-    const E* wk = W + k0 * C;
-#pragma unroll
-    for (int j = 0; j < kLoadsB; ++j) {
-      const int kb = (j * kWaves + wave) * 2 + lane / kRowChunks;
-      dma16(k0 + kb < R && ((vb >> j) & 1) ? static_cast<const void*>(wk + boff[j]) : zero,
-            base + static_cast<uint32_t>((kSlotsA + (j * kWaves + wave) * 64) * 16));
-    }
-  };
-  auto load_frags = [&](int kt, int q, u32x4_t (&fa)[FM], u32x4_t (&fb)[FN]) {
-    const u32x4_t* st = lds + (kt % kStages) * kStageSlots;
-    const int sl = a_slot(lr, 2 * q + lh);
-#pragma unroll
-    for (int i = 0; i < FM; ++i) fa[i] = st[(wm * WTM + i * 32 + lr) * kChunks + sl];
-#pragma unroll
-    for (int j = 0; j < FN; ++j)
-      fb[j] = read_w<T, ROW>(reinterpret_cast<const char*>(st + kSlotsA), q, wn * WTN + j * 32, lane);
-  };
-  f32x16_t acc[FM][FN];
-#pragma unroll
-  for (int i = 0; i < FM; ++i)
-#pragma unroll
-    for (int j = 0; j < FN; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-  auto mfmas = [&](const u32x4_t (&fa)[FM], const u32x4_t (&fb)[FN]) {
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; ++j) mma<T>(acc[i][j], fa[i], fb[j]);
-    __builtin_amdgcn_sched_barrier(0);
-  };
-
-  const int nk = static_cast<int>((R + BK - 1) / BK);
-#pragma unroll
-  for (int s = 0; s < kStages; ++s)
-    if (s < nk) issue(s);
-  u32x4_t fa0[FM], fb0[FN], fa1[FM], fb1[FN];
-  if (nk > 1) wait_then_barrier<kLoadsA + kLoadsB>(); else wait_then_barrier<0>();
-  load_frags(0, 0, fa0, fb0);
-  int kt = 0;
-  for (; kt + kStages < nk; ++kt) {
-#pragma unroll
-    for (int q = 0; q < kPairs; ++q) {
-      if (q + 1 < kPairs) {
-        if (q & 1) load_frags(kt, q + 1, fa0, fb0); else load_frags(kt, q + 1, fa1, fb1);
-      } else {
-        wait_then_barrier<0>();
-        if (wave < kWaves / 2) issue(kt + kStages);
-        load_frags(kt + 1, 0, fa0, fb0);
-      }
-      if (q & 1) mfmas(fa1, fb1); else mfmas(fa0, fb0);
-      if (q + 1 == kPairs && wave >= kWaves / 2) issue(kt + kStages);
-    }
-  }
-  for (; kt < nk; ++kt) {
-#pragma unroll
-    for (int q = 0; q < kPairs; ++q) {
-      if (q + 1 < kPairs) {
-        if (q & 1) load_frags(kt, q + 1, fa0, fb0); else load_frags(kt, q + 1, fa1, fb1);
-      } else if (kt + 1 < nk) {
-        wait_then_barrier<0>();
-        load_frags(kt + 1, 0, fa0, fb0);
-      }
-      if (q & 1) mfmas(fa1, fb1); else mfmas(fa0, fb0);
-    }
-  }
-  Op::template store<T, BN, FM, FN>(a, tile, ct, wm * WTM, wn * WTN, lane, acc);
-}
-
-template <class T, class Op>
-hipError_t launch_nn_dma(const typename Op::Args& a, hipStream_t s) {
-  unsigned tiles = static_cast<unsigned>(a.n_slots) * static_cast<unsigned>(a.n_col_tiles);
-  tiles = (tiles + 8 * 32 - 1) / (8 * 32) * (8 * 32);
-  hipLaunchKernelGGL((nn_dma_kernel<T, Op>), dim3(tiles), dim3(512), 0, s, a);
-  return hipGetLastError();
-}
-
-// Row of accumulator v in its 32x32 block, for lane half lh (its column is the
-// lane's place in the half).
-__device__ __forceinline__ int acc_row(int v, int lh) { return 8 * (v >> 2) + 4 * lh + (v & 3); }
 
 }  // namespace
 

@@ -1,0 +1,251 @@
+// 256 x 256 tiles of a 16-bit product with fp32 accumulation, for many rows:
+//
+//   acc[r, c] = sum_k A[src(r), k] * B[k, c]
+//
+// with every row 16-byte aligned.  B comes in one of two layouts: NT = false,
+// a matrix W [R, C] that holds the output columns contiguously (read from LDS
+// with the transposing ds_read_b64_tr_b16, as in pgg_nn.h), or NT = true, rows
+// of R contiguous reduction elements, one per output column (read like A).
+//
+// 8 waves (2 along rows x 4 along columns, two per SIMD), 128 x 64
+// accumulators each: four blocks of 32 rows and two of 32 columns, of which
+// block j sits at tile column 128 j + 32 wn, so that the columns of all waves'
+// first blocks are one run of 128 and those of the second blocks another.  (A
+// gated product puts gate columns in one run and up columns in the other.)
+//
+// A stage is 64 reduction elements: 64 KiB of LDS in four quarters A0 A1 B0 B1
+// of 16 KiB, A0 holding the first two row blocks of every wave, B0 the first
+// column block.  It is multiplied in four phases of 8 matrix instructions per
+// wave, A0 B0, A0 B1, A1 B1, A1 B0, and each phase has two halves: fetch
+// (fragments from LDS to registers, two direct-to-LDS loads of a later stage)
+// and multiply.  The first wave of every SIMD runs one half ahead of the
+// second, with a workgroup barrier between halves, so that on each SIMD one
+// wave always multiplies while the other fetches, and the loads are spread
+// evenly over time.  The 8 matrix instructions of a half take 256 cycles, the
+// fetch of four waves at most 12 reads each, 192 cycles of LDS.
+//
+// A quarter is refilled, for the stage after next, as soon as both waves of
+// every SIMD have read it: A0 and B0 from the second phase on, B1 in the
+// fourth, A1 in the first phase of the following stage.  A load so has six or
+// seven phases, 1.5 stages, until its data is needed.  In every phase the loads
+// that the next phase's fetch needs are the oldest 2 of 12 outstanding ones:
+// one wait for "at most 10" covers them, and no phase drains the queue.
+#pragma once
+
+#include "pgg_nn.h"
+
+namespace pgg {
+
+namespace {
+
+// Direct global -> LDS load of 16 bytes per lane from base + off (bytes).
+__device__ __forceinline__ void dma16_off(const void* base, uint32_t off, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :: "s"(m0), "v"(off), "s"(base) : "memory", "m0");
+}
+
+// This wave's LDS operations done, and at most VM vector memory operations
+// outstanding (VM < 0: any number); then the workgroup's barrier.
+template <int VM>
+__device__ __forceinline__ void fetched_barrier() {
+  constexpr int n = VM < 0 ? 63 : VM;
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((n & 15) | (7 << 4) | ((n >> 4) << 14));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ void plain_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <bool B>
+struct Whole {
+  static constexpr bool value = B;
+};
+
+template <class T, class Op, bool NT>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void pipe_kernel(typename Op::Args a) {
+  using E = typename T::elem;
+  constexpr int kStageBytes = 65536, kQuarter = 16384;
+  constexpr int kA = 0, kB = 2 * kQuarter;    // byte offsets of the operands in a stage
+  __shared__ u32x4_t lds[2 * kStageBytes / 16];
+
+  int slot, ct;
+  if (!raster<8, 4>(blockIdx.x, a.n_slots, a.n_col_tiles, slot, ct)) return;
+  MTile tile;
+  if (!Op::template tile<256>(a, slot, tile)) return;
+  const int64_t R = a.R, C = a.C;
+
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave & 1, wn = wave >> 1;
+  const int lr = lane & 31, lh = lane >> 5;
+
+  // Load u of quarter A_h of this wave: 8 tile rows 128 u + 64 h + 8 wave + ...,
+  // 128 bytes each; LDS slot lane % 8 of a row holds chunk `chunk`.
+  const int l8 = lane >> 3;
+  const int chunk = a_slot(8 * wave + l8, lane & 7);
+  const int64_t row_base = Op::src_base(a, tile);
+  const char* pa = reinterpret_cast<const char*>(static_cast<const E*>(a.A) + row_base * R);
+  uint32_t oa[2][2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int r = min(128 * u + 64 * h + 8 * wave + l8, tile.rows - 1);
+      oa[h][u] = static_cast<uint32_t>((Op::src(a, tile, r) - row_base) * R * 2) + chunk * 16;
+    }
+  // Load u of quarter B_j.  NT: 8 columns' rows, as for A.  Otherwise 4 rows of
+  // k, 256 bytes each, whose 64-byte segments sit at s ^ (k & 3).
+  const E* W = static_cast<const E*>(a.W) + Op::weight(a, tile);
+  const int kq = lane >> 4;                                     // which of the 4 rows
+  const char* pb;
+  uint32_t ob[2][2];
+  if constexpr (NT) {
+    const int64_t c0 = Op::first_column(ct, 256);
+    pb = reinterpret_cast<const char*>(W + c0 * R);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int64_t c = min<int64_t>(c0 + 128 * j + 64 * u + 8 * wave + l8, a.F - 1);
+        ob[j][u] = static_cast<uint32_t>((c - c0) * R * 2) + chunk * 16;
+      }
+  } else {
+    pb = reinterpret_cast<const char*>(W);
+    const int n = ((((lane & 15) >> 2) ^ kq) << 5) | ((lane & 3) << 3);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int64_t c = Op::half_column(a, ct, j, n);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        ob[j][u] = static_cast<uint32_t>(((32 * u + 4 * wave + kq) * C + c) * 2);
+    }
+  }
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(lds));
+  const void* zero = &kZero16;
+
+  const int nk = static_cast<int>((R + 63) >> 6);
+  const int n_full = static_cast<int>(R >> 6);      // stages without a tail
+  // The two loads of a quarter for stage kt.  Whole: the stage lies inside the
+  // reduction.  Otherwise elements past it read zeros (also whole stages, as
+  // every phase issues its two loads).
+  auto load_a = [&](int kt, int h, auto whole) {
+    const uint32_t m0 = lds0 + (kt & 1) * kStageBytes + kA + h * kQuarter + wave * 1024;
+    const char* p = pa + static_cast<int64_t>(kt) * 128;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if constexpr (decltype(whole)::value) dma16_off(p, oa[h][u], m0 + u * 8192);
+      else dma16(kt * 64 + chunk * 8 < R ? static_cast<const void*>(p + oa[h][u]) : zero, m0 + u * 8192);
+    }
+  };
+  auto load_b = [&](int kt, int j, auto whole) {
+    const uint32_t m0 = lds0 + (kt & 1) * kStageBytes + kB + j * kQuarter + wave * 1024;
+    const char* p = pb + static_cast<int64_t>(kt) * (NT ? 128 : 128 * C);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t k = static_cast<int64_t>(kt) * 64 + (NT ? chunk * 8 : 32 * u + 4 * wave + kq);
+      if constexpr (decltype(whole)::value) dma16_off(p, ob[j][u], m0 + u * 8192);
+      else dma16(k < R ? static_cast<const void*>(p + ob[j][u]) : zero, m0 + u * 8192);
+    }
+  };
+  // fragments of a quarter: q-th 16 reduction elements
+  const char* base = reinterpret_cast<const char*>(lds);
+  auto read_rows = [&](const char* quarter, int row, int q) {
+    return *reinterpret_cast<const u32x4_t*>(quarter + (row + lr) * 128 + a_slot(lr, 2 * q + lh) * 16);
+  };
+  auto read_a = [&](int kt, int h, u32x4_t (&f)[2][4]) {
+    const char* st = base + (kt & 1) * kStageBytes + kA + h * kQuarter;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) f[i][q] = read_rows(st, wm * 64 + i * 32, q);
+  };
+  auto read_b = [&](int kt, int j, u32x4_t (&f)[4]) {
+    const char* st = base + (kt & 1) * kStageBytes + kB + j * kQuarter;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if constexpr (NT) f[q] = read_rows(st, wn * 32, q);
+      else f[q] = read_w<T, 256>(st, q, wn * 32, lane);
+    }
+  };
+
+  f32x16_t acc[4][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+  auto multiply = [&](int h, int j, const u32x4_t (&fa)[2][4], const u32x4_t (&fb)[4]) {
+    __builtin_amdgcn_s_setprio(1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) mma<T>(acc[2 * h + i][j], fb[q], fa[i][q]);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(0);
+  };
+
+  u32x4_t fa[2][4], fb0[4], fb1[4];
+  auto stage = [&](int kt, auto whole) {
+    read_a(kt, 0, fa);
+    read_b(kt, 0, fb0);
+    load_a(kt + 1, 1, whole);
+    fetched_barrier<10>();
+    multiply(0, 0, fa, fb0);
+    plain_barrier();
+
+    read_b(kt, 1, fb1);
+    load_a(kt + 2, 0, whole);
+    fetched_barrier<10>();
+    multiply(0, 1, fa, fb1);
+    plain_barrier();
+
+    read_a(kt, 1, fa);
+    load_b(kt + 2, 0, whole);
+    fetched_barrier<-1>();
+    multiply(1, 1, fa, fb1);
+    plain_barrier();
+
+    load_b(kt + 2, 1, whole);
+    fetched_barrier<10>();
+    multiply(1, 0, fa, fb0);
+    plain_barrier();
+  };
+  const Whole<true> yes;
+  const Whole<false> no;
+  load_a(0, 0, no);
+  load_b(0, 0, no);
+  load_b(0, 1, no);
+  load_a(0, 1, no);
+  load_a(1, 0, no);
+  load_b(1, 0, no);
+  load_b(1, 1, no);
+  fetched_barrier<10>();
+  if (wave >= 4) plain_barrier();   // the second wave of each SIMD: half a phase behind
+  int kt = 0;
+  for (; kt + 2 < n_full; ++kt) stage(kt, yes);
+  for (; kt < nk; ++kt) stage(kt, no);
+  if (wave < 4) plain_barrier();
+  fetched_barrier<0>();   // the zeros past the reduction have landed before LDS is released
+  Op::template store<T, 4, 2>(a, tile, Op::first_column(ct, 256) + wn * 32, 128, wm * 128, lane, acc);
+}
+
+template <class T, class Op, bool NT>
+hipError_t launch_pipe(const typename Op::Args& a, hipStream_t s) {
+  unsigned tiles = static_cast<unsigned>(a.n_slots) * static_cast<unsigned>(a.n_col_tiles);
+  tiles = (tiles + 8 * 32 - 1) / (8 * 32) * (8 * 32);   // whole raster rounds
+  hipLaunchKernelGGL((pipe_kernel<T, Op, NT>), dim3(tiles), dim3(512), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+}  // namespace pgg

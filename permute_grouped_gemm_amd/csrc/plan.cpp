@@ -538,11 +538,12 @@ pgg_status make_glu_grad_plan(const pgg_moe_glu_grad_desc* d, Plan* p) {
   q.panel_cols = F;
   q.dtype = d->grad_y_dtype;
   q.regime = q.dtype == PGG_F32 ? kF32 : kLarge;
-  q.bm = M <= 64 * G ? 64 : 128;
+  q.bm = M <= 64 * G ? 64 : q.dtype == PGG_F32 ? 128 : 256;
   q.bn = 128;
   const int64_t max_tiles = (M + q.bm - 1) / q.bm + G;
   const int64_t col_tiles = (F + q.bn - 1) / q.bn;
-  if (max_tiles * col_tiles >= (int64_t(1) << 23)) return PGG_ERR_UNSUPPORTED;   // fewer than 2^32 lanes
+  // launches of fewer than 2^32 lanes, also as tiles of 128 rows
+  if (max_tiles * col_tiles >= (int64_t(1) << 22)) return PGG_ERR_UNSUPPORTED;
   q.max_tiles = static_cast<int32_t>(max_tiles);
   q.tc = q.max_tiles;
   q.max_chunks = 1;

@@ -48,7 +48,7 @@ def _run(x, w, eri, gl, topk, row_idx_type, act, save=True):
 # that end inside K, F and the expert's rows
 GLU = [(1, 1, 1, 1, 1), (1, 2, 4, 64, 32), (5, 2, 3, 33, 7), (16, 8, 16, 2048, 128), (17, 3, 5, 1000, 72),
        (64, 2, 4, 256, 64), (100, 4, 6, 520, 200), (257, 2, 3, 129, 65), (400, 2, 2, 328, 136),
-       (300, 1, 1, 200, 264)]
+       (300, 1, 1, 200, 264), (200, 1, 1, 40, 24), (520, 1, 2, 64, 8), (260, 1, 1, 136, 520)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
@@ -116,7 +116,7 @@ def test_extreme_gates():
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("batch,topk,G,D,F", [(1, 1, 1, 1, 1), (1, 2, 4, 64, 32), (5, 2, 3, 33, 7), (40, 2, 5, 200, 136),
                                               (333, 2, 7, 203, 141), (300, 1, 1, 264, 200), (257, 2, 2, 520, 264),
-                                              (600, 2, 3, 192, 320)])
+                                              (600, 2, 3, 192, 320), (200, 1, 1, 40, 24), (520, 1, 2, 64, 8)])
 def test_glu_grad(batch, topk, G, D, F, dtype):
     _, gl = _routing(batch, topk, G, D + F, 0, 1.0, min(1, G - topk))
     gen = torch.Generator().manual_seed(D)
