@@ -585,7 +585,20 @@ pgg_status pgg_moe_glu(const pgg_moe_glu_desc* desc, const void* x, const void* 
   const bool aligned = is_aligned(x, 16) && is_aligned(weight, 16) && (size_t(p.N) * es) % 16 == 0 &&
                        (size_t(p.K / 2) * es) % 16 == 0;
   const WsView w = ws_view(p, workspace);
-  hipError_t e = enqueue_prep(p, expanded_row_idx, group_list, w, stream);
+  hipError_t e;
+  if (p.fused_prep) {
+    TimedLaunch t("prep_fused", stream);
+    e = launch_prep_fused(p, expanded_row_idx, group_list, w, stream);
+  } else {
+    {
+      TimedLaunch t("prep_tables", stream);
+      e = launch_prep_tables(p, expanded_row_idx, group_list, w, stream);
+    }
+    if (e == hipSuccess) {
+      TimedLaunch t("prep_check", stream);
+      e = launch_prep_check(p, expanded_row_idx, w, stream);
+    }
+  }
   if (e == hipSuccess) {
     TimedLaunch t("glu", stream);
     e = launch_glu(p, desc->act, x, weight, h, gate_up, aligned, w, stream);

@@ -81,41 +81,31 @@ struct GluOp {
     return j * a.F + min<int64_t>(first_column(ct, 256) + n, a.F - 8);
   }
 
-  template <class T, int FM, int FN>
-  static __device__ __forceinline__ void store(const Args& a, const MTile& t, int64_t c, int step, int m0, int lane,
-                                               const f32x16_t (&acc)[FM][FN]) {
+  static __device__ __forceinline__ int64_t columns(const Args& a) { return a.F; }
+
+  template <class T, int B, class Acc, class Column>
+  static __device__ __forceinline__ void adjust(const Args&, const MTile&, int, int, Acc&, Column) {}
+
+  template <class T>
+  static __device__ __forceinline__ void piece(const Args& a, const MTile& t, int m, int64_t f, int64_t left,
+                                               const float (&gate)[8], const float (&up)[8]) {
     using E = typename T::elem;
-    const int lr = lane & 31, lh = lane >> 5;
-    const int64_t split = static_cast<int64_t>(blockIdx.y) * a.M;
+    const int64_t row = t.row0 + m;
+    if (a.part) {
+      float* p = a.part + (static_cast<int64_t>(blockIdx.y) * a.M + row) * a.C + f;
+      store8<TF32>(p, left, gate);
+      store8<TF32>(p + a.F, left, up);
+      return;
+    }
+    float h[8];
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; j += 2) {
-        const int64_t f = c + j / 2 * step;
-        const int m = m0 + i * 32 + lr;
-        const int64_t left = m < t.rows ? a.F - f : 0;
-        const int64_t row = t.row0 + m;
-        float gate[16], up[16], h[16];
-#pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          gate[v] = acc[i][j][v];
-          up[v] = acc[i][j + 1][v];
-        }
-        if (a.part) {
-          float* p = a.part + (split + row) * a.C + f;
-          store_block<TF32>(p, left, gate, lh);
-          store_block<TF32>(p + a.F, left, up, lh);
-          continue;
-        }
-#pragma unroll
-        for (int v = 0; v < 16; ++v) h[v] = activate<ACT>(gate[v]) * up[v];
-        store_block<T>(static_cast<E*>(a.h) + row * a.F + f, left, h, lh);
-        if (a.gate_up) {
-          E* p = static_cast<E*>(a.gate_up) + row * a.C + f;
-          store_block<T>(p, left, gate, lh);
-          store_block<T>(p + a.F, left, up, lh);
-        }
-      }
+    for (int e = 0; e < 8; ++e) h[e] = activate<ACT>(gate[e]) * up[e];
+    store8<T>(static_cast<E*>(a.h) + row * a.F + f, left, h);
+    if (a.gate_up) {
+      E* p = static_cast<E*>(a.gate_up) + row * a.C + f;
+      store8<T>(p, left, gate);
+      store8<T>(p + a.F, left, up);
+    }
   }
 };
 

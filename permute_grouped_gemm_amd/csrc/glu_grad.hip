@@ -55,35 +55,41 @@ struct GluGradOp {
   static __device__ __forceinline__ int64_t weight(const Args& a, const MTile& t) { return t.g * a.F * a.R; }
   static __device__ __forceinline__ int64_t first_column(int ct, int bn) { return static_cast<int64_t>(ct) * bn; }
 
-  template <class T, int FM, int FN>
-  static __device__ __forceinline__ void store(const Args& a, const MTile& t, int64_t c, int step, int m0, int lane,
-                                               const f32x16_t (&acc)[FM][FN]) {
+  static __device__ __forceinline__ int64_t columns(const Args& a) { return a.F; }
+
+  template <class T, int B, class Acc, class Column>
+  static __device__ __forceinline__ void adjust(const Args&, const MTile&, int, int, Acc&, Column) {}
+
+  // 8 gate and 8 up values
+  template <class T>
+  struct Side {
+    Raw8<T> gate, up;
+  };
+
+  template <class T>
+  static __device__ __forceinline__ Side<T> fetch(const Args& a, const MTile& t, int m, int64_t f, int64_t left) {
+    const typename T::elem* p = static_cast<const typename T::elem*>(a.gate_up) + int64_t(t.row0 + m) * a.C + f;
+    return {load_raw8<T>(p, left), load_raw8<T>(p + a.F, left)};
+  }
+
+  template <class T>
+  static __device__ __forceinline__ void piece(const Args& a, const MTile& t, int m, int64_t f, int64_t left,
+                                               const float (&dh)[8], const Side<T>& side) {
     using E = typename T::elem;
-    const int lr = lane & 31, lh = lane >> 5;
+    const int64_t row = t.row0 + m, at = row * a.C + f;
+    float gate[8], up[8], h[8];
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const int64_t f = c + j * step;
-        const int m = m0 + i * 32 + lr;
-        const int64_t left = m < t.rows ? a.F - f : 0;
-        const int64_t row = t.row0 + m, at = row * a.C + f;
-        float gate[16], up[16], h[16];
-        load_block<T>(static_cast<const E*>(a.gate_up) + at, left, gate, lh);
-        load_block<T>(static_cast<const E*>(a.gate_up) + at + a.F, left, up, lh);
-#pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          const float dh = acc[i][j][v];
-          float value, slope;
-          activate_grad<ACT>(gate[v], value, slope);
-          gate[v] = dh * up[v] * slope;
-          h[v] = value * up[v];
-          up[v] = dh * value;
-        }
-        store_block<T>(static_cast<E*>(a.grad) + at, left, gate, lh);
-        store_block<T>(static_cast<E*>(a.grad) + at + a.F, left, up, lh);
-        if (a.h) store_block<T>(static_cast<E*>(a.h) + row * a.F + f, left, h, lh);
-      }
+    for (int e = 0; e < 8; ++e) {
+      float value, slope;
+      activate_grad<ACT>(to_float<T>(side.gate.e[e]), value, slope);
+      const float u = to_float<T>(side.up.e[e]);
+      gate[e] = dh[e] * u * slope;
+      up[e] = dh[e] * value;
+      h[e] = value * u;
+    }
+    store8<T>(static_cast<E*>(a.grad) + at, left, gate);
+    store8<T>(static_cast<E*>(a.grad) + at + a.F, left, up);
+    if (a.h) store8<T>(static_cast<E*>(a.h) + row * a.F + f, left, h);
   }
 };
 
@@ -205,7 +211,7 @@ void glu_grad_reg_kernel(GluGradArgs a) {
     if (kt + 1 < nk) store_stage((kt & 1) ^ 1);
     __syncthreads();
   }
-  Op::template store<T, FM, FN>(a, tile, col0 + wn * WTN, 32, wm * WTM, lane, acc);
+  store_blocks<T, Op, FM, FN>(a, tile, col0 + wn * WTN, wm * WTM, lane, acc);
 }
 
 template <class T, int BM, int ACT>

@@ -227,84 +227,92 @@ struct LoraOp {
     return {c, a.C - c};
   }
 
-  // 32 rows of z (this lane's: zrow) times 32 columns of adapter p (this lane's: c), all ranks
-  template <class T>
-  static __device__ __forceinline__ f32x16_t expand(const Args& a, const float* zrow, int32_t p, int64_t c, int lh) {
-    using E = typename T::elem;
-    const E* b = static_cast<const E*>(a.b) + static_cast<int64_t>(p) * a.rank * a.C + c;
-    const bool ok = c < a.C;
-    f32x16_t d;
-#pragma unroll
-    for (int v = 0; v < 16; ++v) d[v] = 0.0f;
-    if constexpr (T::kPerChunk == 8) {
-      for (int r = 0; r < a.rank; r += 16) {
-        float zv[8], bv[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int k = r + 8 * lh + e;
-          zv[e] = k < a.rank ? zrow[k] : 0.0f;
-          bv[e] = ok && k < a.rank ? to_float<T>(b[static_cast<int64_t>(k) * a.C]) : 0.0f;
-        }
-        u32x4_t zh, zl, bh, bl;
-        split_bf16(zv, zh, zl);
-        split_bf16(bv, bh, bl);
-        mma<TBf16>(d, bh, zh);
-        mma<TBf16>(d, bh, zl);
-        if constexpr (__is_same(T, TF16)) mma<TBf16>(d, bl, zh);
-      }
-    } else {
-      for (int r = 0; r < a.rank; r += 8) {
-        u32x4_t fz, fb;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int k = r + 4 * lh + e;
-          fz[e] = __builtin_bit_cast(uint32_t, k < a.rank ? zrow[k] : 0.0f);
-          fb[e] = __builtin_bit_cast(uint32_t, ok && k < a.rank ? b[static_cast<int64_t>(k) * a.C] : 0.0f);
-        }
-        mma<T>(d, fb, fz);
-      }
-    }
-    return d;
-  }
+  static __device__ __forceinline__ int64_t columns(const Args& a) { return a.C; }
 
-  template <class T, int FM, int FN>
-  static __device__ __forceinline__ void store(const Args& a, const MTile& t, int64_t c0, int step, int m0, int lane,
-                                               f32x16_t (&acc)[FM][FN]) {
+  // Adds z * B_p of every adapter p found among the wave's rows, adapters in
+  // increasing order, kStep ranks at a time.  Lane l has row l % B of every
+  // block of rows and column l % B of every block of columns, and place l / B
+  // along the ranks.
+  template <class T, int B, class Acc, int NI, int NJ, class Column>
+  static __device__ __forceinline__ void adjust(const Args& a, const MTile& t, int m0, int lane, Acc (&acc)[NI][NJ],
+                                                Column column) {
     using E = typename T::elem;
-    const int lr = lane & 31, lh = lane >> 5;
+    constexpr int EPC = T::kPerChunk, kStep = 64 / B * EPC, kNone = 0x7FFFFFFF;
+    if (a.part) return;
+    int32_t id[NI];
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const int m = m0 + i * 32 + lr;
-      const int64_t token = int64_t(t.row0) + m;
-      if (!a.part) {
-        const int32_t id = m < t.rows ? adapter_of(a, token) : -1;
-        const float* zrow = a.z + (int64_t(t.row0) + min(m, t.rows - 1)) * a.rank;
-        uint32_t pending = static_cast<uint32_t>(__ballot(id >= 0));
-        while (pending) {
-          const int32_t p = __shfl(id, __builtin_ctz(pending));
-          pending &= ~static_cast<uint32_t>(__ballot(id == p));
+    for (int i = 0; i < NI; ++i) {
+      const int r = m0 + i * B + lane % B;
+      id[i] = r < t.rows ? adapter_of(a, int64_t(t.row0) + r) : -1;
+    }
+    const float* z0 = a.z + (int64_t(t.row0) + m0 + lane % B) * a.rank;
+    for (int32_t last = -1;;) {
+      int32_t p = kNone;
 #pragma unroll
-          for (int j = 0; j < FN; ++j) {
-            const f32x16_t d = expand<T>(a, zrow, p, c0 + j * step + lr, lh);
+      for (int i = 0; i < NI; ++i) p = id[i] > last ? min(p, id[i]) : p;
 #pragma unroll
-            for (int v = 0; v < 16; ++v)
-              if (id == p) acc[i][j][v] += d[v];
-            __builtin_amdgcn_sched_barrier(0);   // one block at a time: registers
+      for (int d = B / 2; d; d >>= 1) p = min(p, __shfl_xor(p, d));
+      p = __builtin_amdgcn_readfirstlane(p);
+      if (p == kNone) break;
+      last = p;
+      const E* b = static_cast<const E*>(a.b) + static_cast<int64_t>(p) * a.rank * a.C;
+      for (int r = EPC * (lane / B); r - EPC * (lane / B) < a.rank; r += kStep) {
+        u32x4_t bh[NJ], bl[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const int64_t c = column(j) + lane % B;
+          float v[EPC];
+#pragma unroll
+          for (int e = 0; e < EPC; ++e)
+            v[e] = c < a.C && r + e < a.rank ? to_float<T>(b[static_cast<int64_t>(r + e) * a.C + c]) : 0.0f;
+          if constexpr (EPC == 8) split_bf16(v, bh[j], bl[j]);
+          else __builtin_memcpy(&bh[j], v, 16);
+        }
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          if (!__ballot(id[i] == p)) continue;
+          float v[EPC];
+#pragma unroll
+          for (int e = 0; e < EPC; ++e)
+            v[e] = id[i] == p && r + e < a.rank ? z0[static_cast<int64_t>(i) * B * a.rank + r + e] : 0.0f;
+          u32x4_t zh, zl;
+          if constexpr (EPC == 8) split_bf16(v, zh, zl);
+          else __builtin_memcpy(&zh, v, 16);
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            Acc d;
+#pragma unroll
+            for (int e = 0; e < B * B / 64; ++e) d[e] = 0.0f;
+            if constexpr (EPC == 8) {
+              mma_block<TBf16>(d, bh[j], zh);
+              mma_block<TBf16>(d, bh[j], zl);
+              if constexpr (__is_same(T, TF16)) mma_block<TBf16>(d, bl[j], zh);
+            } else {
+              mma<T>(d, bh[j], zh);
+            }
+#pragma unroll
+            for (int e = 0; e < B * B / 64; ++e) acc[i][j][e] = id[i] == p ? acc[i][j][e] + d[e] : acc[i][j][e];
           }
         }
       }
-#pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const int64_t c = c0 + j * step, left = m < t.rows ? a.C - c : 0;
-        float y[16];
-#pragma unroll
-        for (int v = 0; v < 16; ++v) y[v] = acc[i][j][v];
-        if (a.part)
-          store_block<TF32>(a.part + (static_cast<int64_t>(blockIdx.y) * a.T + token) * a.C + c, left, y, lh);
-        else
-          store_block<T>(static_cast<E*>(a.y) + token * a.C + c, left, y, lh);
-      }
     }
+  }
+
+  template <class T>
+  struct Side {};
+  template <class T>
+  static __device__ __forceinline__ Side<T> fetch(const Args&, const MTile&, int, int64_t, int64_t) {
+    return {};
+  }
+
+  template <class T>
+  static __device__ __forceinline__ void piece(const Args& a, const MTile& t, int m, int64_t c, int64_t left,
+                                               const float (&v)[8], const Side<T>&) {
+    const int64_t token = int64_t(t.row0) + m;
+    if (a.part)
+      store8<TF32>(a.part + (static_cast<int64_t>(blockIdx.y) * a.T + token) * a.C + c, left, v);
+    else
+      store8<T>(static_cast<typename T::elem*>(a.y) + token * a.C + c, left, v);
   }
 };
 

@@ -10,7 +10,13 @@ namespace {
 constexpr float kGeluC = 0.7978845608028654f;   // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
-__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
+// 1 / (1 + exp(-v)) from the hardware's base-2 exponential and reciprocal, each
+// within 1 ulp.  The product -v log2 e is rounded, which makes the exponential
+// off by |v| 2^-24 of itself; where it is that large a part of the sum, the
+// result is near 0.  At the ends the exponential is 0 or inf, the result 1 or 0.
+__device__ __forceinline__ float sigmoid(float v) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.4426950408889634f));
+}
 
 // silu(g) = g sigmoid(g);  gelu_tanh(g) = g sigmoid(2 c (g + a g^3)), which is
 // g (1 + tanh(c (g + a g^3))) / 2.

@@ -123,6 +123,11 @@ hipError_t launch_prep_fused(const Plan& p, const int64_t* eri, const int64_t* g
 hipError_t launch_prep_groups(const Plan& p, const int64_t* group_list, const WsView& w,
                               hipStream_t s);
 hipError_t launch_prep_index(const Plan& p, const int64_t* eri, const WsView& w, hipStream_t s);
+// The same preparation in two launches: group tables and index entries, then
+// the checks of the index.
+hipError_t launch_prep_tables(const Plan& p, const int64_t* eri, const int64_t* gl, const WsView& w,
+                              hipStream_t s);
+hipError_t launch_prep_check(const Plan& p, const int64_t* eri, const WsView& w, hipStream_t s);
 hipError_t launch_prep_verify(const Plan& p, const int64_t* eri, const WsView& w, hipStream_t s);
 
 // Columns [lo, hi) of panel `panel`.

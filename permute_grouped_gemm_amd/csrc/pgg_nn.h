@@ -13,18 +13,23 @@
 //   Op::weight(args, t)      first element of the tile's W
 //   Op::column<BN>(args, ct, n)  column of W at column n (a multiple of 4) of
 //                            the tile, and how many of W's columns follow in that run
+//   Op::columns(args)        number of output columns
 //   Op::first_column(ct, bn) output column of the tile's first one
 //   Op::kPaired              blocks of 32 columns belong together two by two and
 //                            make 32 output columns
-//   Op::store<T, FM, FN>(args, t, c, step, m0, lane, acc)
-//                            takes the accumulators: output column c of the
-//                            wave's first block, the step from one block (or
-//                            pair) to the next, the wave's first tile row m0
+//   Op::adjust<T, B>(args, t, m0, lane, acc, column)
+//                            may change a wave's accumulators acc[i][j], blocks of
+//                            B x B at tile row m0 + B i and output column column(j)
+//   Op::piece<T>(args, t, m, c, left, v, w)
+//                            takes 8 successive columns from c on of tile row m,
+//                            of which `left` exist (0 or less: none); for pairs,
+//                            v and w are those of the first and the second
+//                            block, otherwise w is what
+//   Op::fetch<T>(args, t, m, c, left)  of type Op::Side<T> had loaded for the piece
 //
 // The matrix instructions get the columns as their first operand, so that a
-// lane ends with 16 columns of one row of a 32 x 32 block: lane (lr, lh) has
-// row lr, and accumulator v is column 8 (v / 4) + 4 lh + v % 4.  Rows are then
-// stored in pieces of 16 bytes (store_block).
+// lane ends with columns of one row; two lanes of that row exchange every other
+// group of four, and rows are stored in pieces of 8 columns.
 //
 // nn_reg_kernel takes every type and alignment (loads through registers, any
 // tile); pgg_pipe.h has the kernel for many rows of aligned 16-bit data.
@@ -114,86 +119,90 @@ __device__ __forceinline__ u32x4_t read_w(const char* base, int q, int n, int la
   }
 }
 
-// A row of a 32 x 32 block between accumulators and memory.  fp32: the four
-// columns of accumulators 4 p .. 4 p + 3 are piece p.  16 bits: the halves of
-// the wave exchange every other group of four, so that a lane of the lower half
-// has 8 successive columns from 16 p on and one of the upper half from 16 p + 8.
 template <class T>
-__device__ __forceinline__ int piece_column(int p, int lh) {
-  return T::kPerChunk == 8 ? 16 * p + 8 * lh : 8 * p + 4 * lh;
+__device__ __forceinline__ void mma_block(f32x16_t& acc, u32x4_t a, u32x4_t b) {
+  mma<T>(acc, a, b);
 }
 
-// What the upper half of the wave holds in x for what the lower one holds in y.
-__device__ __forceinline__ void exchange_halves(uint32_t& x, uint32_t& y) {
-  const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
-  x = r[0];
-  y = r[1];
-}
+// 8 stored elements.
+template <class T>
+struct Raw8 {
+  typename T::elem e[8];
+};
 
 template <class T>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  return static_cast<uint32_t>(from_float<T>(lo)) | (static_cast<uint32_t>(from_float<T>(hi)) << 16);
+__device__ __forceinline__ Raw8<T> load_raw8(const typename T::elem* p, int64_t left) {
+  Raw8<T> r;
+  if (left >= 8) {
+    __builtin_memcpy(r.e, p, sizeof(r.e));
+  } else {
+#pragma unroll
+    for (int t = 0; t < 8; ++t) r.e[t] = t < left ? p[t] : typename T::elem(0);
+  }
+  return r;
 }
 
-// Stores this lane's part of a block row that starts at p, of which `left`
-// columns exist (0 or less: none, for a row past the tile).  Every lane of the
-// wave takes part.
+// 8 values to p, of which the first `left` exist, rounded once.
 template <class T>
-__device__ __forceinline__ void store_block(typename T::elem* p, int64_t left, const float (&val)[16], int lh) {
+__device__ __forceinline__ void store8(typename T::elem* p, int64_t left, const float (&v)[8]) {
   using E = typename T::elem;
-  constexpr int W = T::kPerChunk;
+  E e[8];
 #pragma unroll
-  for (int q = 0; q < 32 / (2 * W); ++q) {
-    u32x4_t v;
-    if constexpr (W == 8) {
-      uint32_t x[2], y[2];
+  for (int t = 0; t < 8; ++t) e[t] = from_float<T>(v[t]);
+  if (left >= 8) {
+    __builtin_memcpy(p, e, sizeof(e));
+  } else if (left > 0) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        x[e] = pack2<T>(val[8 * q + 2 * e], val[8 * q + 2 * e + 1]);
-        y[e] = pack2<T>(val[8 * q + 4 + 2 * e], val[8 * q + 5 + 2 * e]);
-        exchange_halves(x[e], y[e]);
-      }
-      v = u32x4_t{x[0], x[1], y[0], y[1]};
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = __builtin_bit_cast(uint32_t, val[4 * q + e]);
-    }
-    const int c = piece_column<T>(q, lh);
-    if (left >= c + W) {
-      __builtin_memcpy(p + c, &v, 16);
-    } else if (left > c) {
-      E e[W];
-      __builtin_memcpy(e, &v, 16);
-#pragma unroll
-      for (int t = 0; t < W; ++t)
-        if (c + t < left) p[c + t] = e[t];
-    }
+    for (int t = 0; t < 8; ++t)
+      if (t < left) p[t] = e[t];
   }
 }
 
-// The reverse: accumulator order from memory; what does not exist is 0.
-template <class T>
-__device__ __forceinline__ void load_block(const typename T::elem* p, int64_t left, float (&val)[16], int lh) {
-  using E = typename T::elem;
-  constexpr int W = T::kPerChunk;
+// What the upper half of the wave holds in x for what the lower one holds in y.
+__device__ __forceinline__ void exchange32(float& x, float& y) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y),
+                                                  false, false);
+  const uint32_t x1 = r[0], y1 = r[1];
+  x = __builtin_bit_cast(float, x1);
+  y = __builtin_bit_cast(float, y1);
+}
+
+// Columns of a 32 x 32 block, 32 rows to its 32 lanes per half: accumulator v
+// is column 8 (v / 4) + 4 (lane / 32) + v % 4.  Piece q (0, 1) of this lane
+// after the exchange starts at column 16 q + 8 (lane / 32).
+__device__ __forceinline__ void piece32(const f32x16_t& acc, int q, float (&v)[8]) {
 #pragma unroll
-  for (int q = 0; q < 32 / (2 * W); ++q) {
-    const int c = piece_column<T>(q, lh);
-    u32x4_t v = load16_part<T>(p + c, left - c);
-    if constexpr (W == 8) {
-      uint32_t d[4] = {v[0], v[1], v[2], v[3]};
-      exchange_halves(d[0], d[2]);
-      exchange_halves(d[1], d[3]);
+  for (int e = 0; e < 4; ++e) {
+    v[e] = acc[8 * q + e];
+    v[4 + e] = acc[8 * q + 4 + e];
+    exchange32(v[e], v[4 + e]);
+  }
+}
+
+// All of a wave's 32 x 32 blocks: first tile row m0, first output column c0.
+template <class T, class Op, int FM, int FN>
+__device__ __forceinline__ void store_blocks(const typename Op::Args& a, const MTile& t, int64_t c0, int m0, int lane,
+                                             f32x16_t (&acc)[FM][FN]) {
+  Op::template adjust<T, 32>(a, t, m0, lane, acc, [&](int j) { return c0 + 32 * j; });
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        val[8 * q + 2 * e] = to_float<T>(static_cast<E>(d[e] & 0xFFFFu));
-        val[8 * q + 2 * e + 1] = to_float<T>(static_cast<E>(d[e] >> 16));
-      }
-    } else {
+  for (int i = 0; i < FM; ++i) {
+    const int m = m0 + i * 32 + (lane & 31);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t u = v[e];
-        val[4 * q + e] = __builtin_bit_cast(float, u);
+    for (int j = 0; j < FN; j += Op::kPaired ? 2 : 1) {
+      const int64_t c = c0 + (Op::kPaired ? j / 2 : j) * 32;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float v[8];
+        piece32(acc[i][j], q, v);
+        const int64_t at = c + 16 * q + 8 * (lane >> 5);
+        const int64_t left = m < t.rows ? Op::columns(a) - at : 0;
+        if constexpr (Op::kPaired) {
+          float w[8];
+          piece32(acc[i][j + 1], q, w);
+          Op::template piece<T>(a, t, m, at, left, v, w);
+        } else {
+          Op::template piece<T>(a, t, m, at, left, v, Op::template fetch<T>(a, t, m, at, left));
+        }
       }
     }
   }
@@ -334,8 +343,8 @@ void nn_reg_kernel(typename Op::Args a) {
     if (kt + 1 < nk) store_stage((kt & 1) ^ 1);
     __syncthreads();
   }
-  Op::template store<T, FM, FN>(a, tile, Op::first_column(ct, BN) + wn * (Op::kPaired ? WTN / 2 : WTN), 32,
-                                wm * WTM, lane, acc);
+  store_blocks<T, Op, FM, FN>(a, tile, Op::first_column(ct, BN) + wn * (Op::kPaired ? WTN / 2 : WTN), wm * WTM, lane,
+                              acc);
 }
 
 template <class T, class Op, int BM, int BN, int WM, int WN, int EU>

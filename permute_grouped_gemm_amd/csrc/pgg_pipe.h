@@ -8,20 +8,19 @@
 // of R contiguous reduction elements, one per output column (read like A).
 //
 // 8 waves (2 along rows x 4 along columns, two per SIMD), 128 x 64
-// accumulators each: four blocks of 32 rows and two of 32 columns, of which
-// block j sits at tile column 128 j + 32 wn, so that the columns of all waves'
-// first blocks are one run of 128 and those of the second blocks another.  (A
-// gated product puts gate columns in one run and up columns in the other.)
+// accumulators each, in 16 x 16 blocks.  Its columns are two runs of 32, run j
+// at tile column 128 j + 32 wn, so that all waves' first runs make one of 128
+// and the second runs another.  (A gated product puts gate columns in one and
+// up columns in the other.)
 //
 // A stage is 64 reduction elements: 64 KiB of LDS in four quarters A0 A1 B0 B1
-// of 16 KiB, A0 holding the first two row blocks of every wave, B0 the first
-// column block.  It is multiplied in four phases of 8 matrix instructions per
-// wave, A0 B0, A0 B1, A1 B1, A1 B0, and each phase has two halves: fetch
+// of 16 KiB, A0 holding the first 64 rows of every wave, B0 the first run of
+// columns.  It is multiplied in four phases of 16 matrix instructions per wave, A0 B0, A0 B1, A1 B1, A1 B0, and each phase has two halves: fetch
 // (fragments from LDS to registers, two direct-to-LDS loads of a later stage)
 // and multiply.  The first wave of every SIMD runs one half ahead of the
 // second, with a workgroup barrier between halves, so that on each SIMD one
 // wave always multiplies while the other fetches, and the loads are spread
-// evenly over time.  The 8 matrix instructions of a half take 256 cycles, the
+// evenly over time.  The 16 matrix instructions of a half take 256 cycles, the
 // fetch of four waves at most 12 reads each, 192 cycles of LDS.
 //
 // A quarter is refilled, for the stage after next, as soon as both waves of
@@ -61,6 +60,58 @@ __device__ __forceinline__ void plain_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// 16 x 16 blocks: lane l holds 8 reduction elements, from 8 (l / 16) on, of row
+// l % 16 of either operand, and of the result column l % 16, rows 4 (l / 16) on.
+template <class T>
+__device__ __forceinline__ void mma_block(f32x4_t& acc, u32x4_t a, u32x4_t b) {
+  if constexpr (__is_same(T, TBf16))
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b),
+                                                  acc, 0, 0, 0);
+  else
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b),
+                                                 acc, 0, 0, 0);
+}
+
+// Two neighbouring 16 x 16 blocks, columns first: accumulator v of lane l is
+// column 4 (l / 16) + v of row l % 16.  After the exchange between the odd
+// groups of 16 lanes of x and the even ones of y, lane l holds 8 successive
+// columns from run_column(l) on.
+__device__ __forceinline__ int run_column(int lane) { return 16 * ((lane >> 4) & 1) + 8 * (lane >> 5); }
+
+__device__ __forceinline__ void piece16(const f32x4_t& x, const f32x4_t& y, float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float xe = x[e], ye = y[e];
+    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, xe), __builtin_bit_cast(uint32_t, ye),
+                                                    false, false);
+    const uint32_t x1 = r[0], y1 = r[1];
+    v[e] = __builtin_bit_cast(float, x1);
+    v[4 + e] = __builtin_bit_cast(float, y1);
+  }
+}
+
+// 8 consecutive k, from 32 s + 8 (lane / 16) on, of column n + lane % 16 of a
+// quarter of 256-byte rows.  As read_w of pgg_nn.h, with the 32-byte halves of
+// a segment exchanged in every other 8 rows, since the lanes read together
+// cover the same 16 columns of rows k.. and k + 8...
+__device__ __forceinline__ uint32_t quarter_offset(int k, int b) {
+  return static_cast<uint32_t>(k * 256 + (((b >> 6) ^ (k & 3)) << 6) + ((b & 63) ^ (((k >> 3) & 1) << 5)));
+}
+
+__device__ __forceinline__ u32x4_t read_quarter(const char* base, int s, int n, int lane) {
+  const int i = lane & 15;
+  const int k = 32 * s + 8 * (lane >> 4) + (i >> 2);
+  const int b = 2 * (n + 4 * (i & 3));
+  u32x2_t part[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    auto p = (__attribute__((address_space(3))) h16x4_t*)(
+        (__attribute__((address_space(3))) char*)(base + quarter_offset(k + 4 * u, b)));
+    part[u] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4f16(p));
+  }
+  return u32x4_t{part[0][0], part[0][1], part[1][0], part[1][1]};
+}
+
 template <bool B>
 struct Whole {
   static constexpr bool value = B;
@@ -84,7 +135,7 @@ void pipe_kernel(typename Op::Args a) {
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave & 1, wn = wave >> 1;
-  const int lr = lane & 31, lh = lane >> 5;
+  const int lr = lane & 15, lg = lane >> 4;
 
   // Load u of quarter A_h of this wave: 8 tile rows 128 u + 64 h + 8 wave + ...,
   // 128 bytes each; LDS slot lane % 8 of a row holds chunk `chunk`.
@@ -101,7 +152,7 @@ void pipe_kernel(typename Op::Args a) {
       oa[h][u] = static_cast<uint32_t>((Op::src(a, tile, r) - row_base) * R * 2) + chunk * 16;
     }
   // Load u of quarter B_j.  NT: 8 columns' rows, as for A.  Otherwise 4 rows of
-  // k, 256 bytes each, whose 64-byte segments sit at s ^ (k & 3).
+  // k, 256 bytes each, whose 16-byte chunks sit where quarter_offset puts them.
   const E* W = static_cast<const E*>(a.W) + Op::weight(a, tile);
   const int kq = lane >> 4;                                     // which of the 4 rows
   const char* pb;
@@ -118,7 +169,7 @@ void pipe_kernel(typename Op::Args a) {
       }
   } else {
     pb = reinterpret_cast<const char*>(W);
-    const int n = ((((lane & 15) >> 2) ^ kq) << 5) | ((lane & 3) << 3);
+    const int n = ((((lane & 15) >> 2) ^ kq) << 5) | (((lane & 3) ^ (wave & 2)) << 3);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int64_t c = Op::half_column(a, ct, j, n);
@@ -154,46 +205,48 @@ void pipe_kernel(typename Op::Args a) {
       else dma16(k < R ? static_cast<const void*>(p + ob[j][u]) : zero, m0 + u * 8192);
     }
   };
-  // fragments of a quarter: q-th 16 reduction elements
+  // fragments of a quarter, [16 rows or columns][32 reduction elements]
   const char* base = reinterpret_cast<const char*>(lds);
   auto read_rows = [&](const char* quarter, int row, int q) {
-    return *reinterpret_cast<const u32x4_t*>(quarter + (row + lr) * 128 + a_slot(lr, 2 * q + lh) * 16);
+    return *reinterpret_cast<const u32x4_t*>(quarter + (row + lr) * 128 + a_slot(lr, 4 * q + lg) * 16);
   };
-  auto read_a = [&](int kt, int h, u32x4_t (&f)[2][4]) {
+  auto read_a = [&](int kt, int h, u32x4_t (&f)[4][2]) {
     const char* st = base + (kt & 1) * kStageBytes + kA + h * kQuarter;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int q = 0; q < 2; ++q)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) f[i][q] = read_rows(st, wm * 64 + i * 32, q);
+      for (int i = 0; i < 4; ++i) f[i][q] = read_rows(st, wm * 64 + i * 16, q);
   };
-  auto read_b = [&](int kt, int j, u32x4_t (&f)[4]) {
+  auto read_b = [&](int kt, int j, u32x4_t (&f)[2][2]) {
     const char* st = base + (kt & 1) * kStageBytes + kB + j * kQuarter;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if constexpr (NT) f[q] = read_rows(st, wn * 32, q);
-      else f[q] = read_w<T, 256>(st, q, wn * 32, lane);
-    }
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        if constexpr (NT) f[n][q] = read_rows(st, wn * 32 + n * 16, q);
+        else f[n][q] = read_quarter(st, q, wn * 32 + n * 16, lane);
+      }
   };
 
-  f32x16_t acc[4][2];
+  f32x4_t acc[8][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-  auto multiply = [&](int h, int j, const u32x4_t (&fa)[2][4], const u32x4_t (&fb)[4]) {
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  auto multiply = [&](int h, int j, const u32x4_t (&fa)[4][2], const u32x4_t (&fb)[2][2]) {
     __builtin_amdgcn_s_setprio(1);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int q = 0; q < 2; ++q)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) mma<T>(acc[2 * h + i][j], fb[q], fa[i][q]);
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) mma_block<T>(acc[4 * h + i][2 * j + n], fb[n][q], fa[i][q]);
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_setprio(0);
   };
 
-  u32x4_t fa[2][4], fb0[4], fb1[4];
+  u32x4_t fa[4][2], fb0[2][2], fb1[2][2];
   auto stage = [&](int kt, auto whole) {
     read_a(kt, 0, fa);
     read_b(kt, 0, fb0);
@@ -235,7 +288,42 @@ void pipe_kernel(typename Op::Args a) {
   for (; kt < nk; ++kt) stage(kt, no);
   if (wave < 4) plain_barrier();
   fetched_barrier<0>();   // the zeros past the reduction have landed before LDS is released
-  Op::template store<T, 4, 2>(a, tile, Op::first_column(ct, 256) + wn * 32, 128, wm * 128, lane, acc);
+
+  const int64_t c0 = Op::first_column(ct, 256) + wn * 32;
+  Op::template adjust<T, 16>(a, tile, wm * 128, lane, acc, [&](int j) { return c0 + 128 * (j >> 1) + 16 * (j & 1); });
+  auto row = [&](int i) { return wm * 128 + i * 16 + lr; };
+  auto left = [&](int i, int64_t c) { return row(i) < tile.rows ? Op::columns(a) - c : 0; };
+  const int64_t c1 = c0 + run_column(lane);
+  if constexpr (Op::kPaired) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float v[8], w[8];
+      piece16(acc[i][0], acc[i][1], v);
+      piece16(acc[i][2], acc[i][3], w);
+      Op::template piece<T>(a, tile, row(i), c1, left(i, c1), v, w);
+    }
+  } else {
+    // what the pieces need from memory is loaded kAhead rows of blocks ahead
+    constexpr int kAhead = 3;
+    typename Op::template Side<T> side[kAhead][2];
+    auto fetch = [&](int i) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        side[i % kAhead][j] = Op::template fetch<T>(a, tile, row(i), c1 + 128 * j, left(i, c1 + 128 * j));
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch(i);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float v[8];
+        piece16(acc[i][2 * j], acc[i][2 * j + 1], v);
+        Op::template piece<T>(a, tile, row(i), c1 + 128 * j, left(i, c1 + 128 * j), v, side[i % kAhead][j]);
+      }
+      if (i + kAhead < 8) fetch(i + kAhead);
+    }
+  }
 }
 
 template <class T, class Op, bool NT>

@@ -519,6 +519,7 @@ pgg_status make_glu_plan(const pgg_moe_glu_desc* d, Plan* p) {
   // tiles of 128 rows and 128 columns where rows are not 16-byte aligned are four
   // times as many as the plan's; a launch holds fewer than 2^32 lanes
   if (int64_t(p->max_tiles) * p->n_col_tiles >= (int64_t(1) << 21)) return PGG_ERR_UNSUPPORTED;
+  p->fused_prep = p->M <= 1024;
   return PGG_OK;
 }
 

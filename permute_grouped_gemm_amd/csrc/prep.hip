@@ -30,6 +30,29 @@ __global__ __launch_bounds__(256) void prep_verify_kernel(PrepArgs a, const int6
   if (t < a.M) verify_one(a, eri, w, t);
 }
 
+// Workgroup 0: header and group tables.  The others: the index entries, without
+// the header (which workgroup 0 may not have reset yet); prep_check_kernel
+// reports what they skip.
+__global__ __launch_bounds__(kPrepThreads) void prep_tables_kernel(PrepArgs a, const int64_t* eri,
+                                                                   const int64_t* gl, WsView w) {
+  __shared__ long long scratch[2 * kPrepThreads];
+  if (blockIdx.x == 0) {
+    reset_header(w.hdr);
+    __syncthreads();
+    groups_phase(a, gl, w, scratch, scratch + kPrepThreads);
+    return;
+  }
+  const int64_t t = static_cast<int64_t>(blockIdx.x - 1) * blockDim.x + threadIdx.x;
+  if (t < a.M && eri[t] >= 0 && eri[t] < a.M) index_one(a, eri, w, t);
+}
+
+__global__ __launch_bounds__(256) void prep_check_kernel(PrepArgs a, const int64_t* eri, WsView w) {
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (t >= a.M) return;
+  if (eri[t] < 0 || eri[t] >= a.M) set_error(w.hdr, PGG_DEV_INDEX_RANGE, t);
+  else verify_one(a, eri, w, t);
+}
+
 }  // namespace
 
 hipError_t launch_prep_fused(const Plan& p, const int64_t* eri, const int64_t* gl,
@@ -42,6 +65,19 @@ hipError_t launch_prep_fused(const Plan& p, const int64_t* eri, const int64_t* g
 
 hipError_t launch_prep_groups(const Plan& p, const int64_t* gl, const WsView& w, hipStream_t s) {
   hipLaunchKernelGGL(prep_groups_kernel, dim3(1), dim3(kPrepThreads), 0, s, prep_args(p), gl, w);
+  return hipGetLastError();
+}
+
+hipError_t launch_prep_tables(const Plan& p, const int64_t* eri, const int64_t* gl, const WsView& w,
+                              hipStream_t s) {
+  const unsigned blocks = 1 + static_cast<unsigned>((p.M + kPrepThreads - 1) / kPrepThreads);
+  hipLaunchKernelGGL(prep_tables_kernel, dim3(blocks), dim3(kPrepThreads), 0, s, prep_args(p), eri, gl, w);
+  return hipGetLastError();
+}
+
+hipError_t launch_prep_check(const Plan& p, const int64_t* eri, const WsView& w, hipStream_t s) {
+  const unsigned blocks = static_cast<unsigned>((p.M + 255) / 256);
+  hipLaunchKernelGGL(prep_check_kernel, dim3(blocks), dim3(256), 0, s, prep_args(p), eri, w);
   return hipGetLastError();
 }
 
