@@ -93,8 +93,8 @@ struct GluOp {
     const int64_t row = t.row0 + m;
     if (a.part) {
       float* p = a.part + (static_cast<int64_t>(blockIdx.y) * a.M + row) * a.C + f;
-      store8<TF32>(p, left, gate);
-      store8<TF32>(p + a.F, left, up);
+      store8<TF32, false>(p, left, gate);
+      store8<TF32, false>(p + a.F, left, up);
       return;
     }
     float h[8];

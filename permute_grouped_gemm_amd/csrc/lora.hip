@@ -310,7 +310,7 @@ struct LoraOp {
                                                const float (&v)[8], const Side<T>&) {
     const int64_t token = int64_t(t.row0) + m;
     if (a.part)
-      store8<TF32>(a.part + (static_cast<int64_t>(blockIdx.y) * a.T + token) * a.C + c, left, v);
+      store8<TF32, false>(a.part + (static_cast<int64_t>(blockIdx.y) * a.T + token) * a.C + c, left, v);
     else
       store8<T>(static_cast<typename T::elem*>(a.y) + token * a.C + c, left, v);
   }

@@ -124,17 +124,26 @@ __device__ __forceinline__ void mma_block(f32x16_t& acc, u32x4_t a, u32x4_t b) {
   mma<T>(acc, a, b);
 }
 
+// Vectors at any address.
+typedef u32x4_t __attribute__((aligned(2))) u32x4_any_t;
+
 // 8 stored elements.
 template <class T>
 struct Raw8 {
   typename T::elem e[8];
 };
 
+// From memory that is read once: the non-temporal hint leaves the caches to the
+// operands, which many tiles share.
 template <class T>
 __device__ __forceinline__ Raw8<T> load_raw8(const typename T::elem* p, int64_t left) {
   Raw8<T> r;
   if (left >= 8) {
-    __builtin_memcpy(r.e, p, sizeof(r.e));
+    u32x4_t x[sizeof(r.e) / 16];
+#pragma unroll
+    for (unsigned q = 0; q < sizeof(r.e) / 16; ++q)
+      x[q] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any_t*>(p) + q);
+    __builtin_memcpy(r.e, x, sizeof(r.e));
   } else {
 #pragma unroll
     for (int t = 0; t < 8; ++t) r.e[t] = t < left ? p[t] : typename T::elem(0);
@@ -142,15 +151,22 @@ __device__ __forceinline__ Raw8<T> load_raw8(const typename T::elem* p, int64_t 
   return r;
 }
 
-// 8 values to p, of which the first `left` exist, rounded once.
-template <class T>
+// 8 values to p, of which the first `left` exist, rounded once; NT: with the
+// non-temporal hint, for results that this call does not read again.
+template <class T, bool NT = true>
 __device__ __forceinline__ void store8(typename T::elem* p, int64_t left, const float (&v)[8]) {
   using E = typename T::elem;
   E e[8];
 #pragma unroll
   for (int t = 0; t < 8; ++t) e[t] = from_float<T>(v[t]);
   if (left >= 8) {
-    __builtin_memcpy(p, e, sizeof(e));
+    u32x4_t x[sizeof(e) / 16];
+    __builtin_memcpy(x, e, sizeof(e));
+#pragma unroll
+    for (unsigned q = 0; q < sizeof(e) / 16; ++q) {
+      if constexpr (NT) __builtin_nontemporal_store(x[q], reinterpret_cast<u32x4_any_t*>(p) + q);
+      else reinterpret_cast<u32x4_any_t*>(p)[q] = x[q];
+    }
   } else if (left > 0) {
 #pragma unroll
     for (int t = 0; t < 8; ++t)

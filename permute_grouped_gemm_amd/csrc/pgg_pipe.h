@@ -304,7 +304,7 @@ void pipe_kernel(typename Op::Args a) {
     }
   } else {
     // what the pieces need from memory is loaded kAhead rows of blocks ahead
-    constexpr int kAhead = 3;
+    constexpr int kAhead = 2;
     typename Op::template Side<T> side[kAhead][2];
     auto fetch = [&](int i) {
 #pragma unroll
