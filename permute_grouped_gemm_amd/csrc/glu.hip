@@ -20,7 +20,7 @@
 #include <algorithm>
 
 #include "pgg_act.h"
-#include "pgg_pipe.h"
+#include "pgg_few.h"
 
 namespace pgg {
 
@@ -82,6 +82,9 @@ struct GluOp {
   }
 
   static __device__ __forceinline__ int64_t columns(const Args& a) { return a.F; }
+  static __device__ __forceinline__ int extra(const Args&) { return 0; }
+  template <class T>
+  static __device__ __forceinline__ void extra_work(const Args&, int) {}
 
   template <class T, int B, class Acc, class Column>
   static __device__ __forceinline__ void adjust(const Args&, const MTile&, int, int, Acc&, Column) {}
@@ -92,7 +95,7 @@ struct GluOp {
     using E = typename T::elem;
     const int64_t row = t.row0 + m;
     if (a.part) {
-      float* p = a.part + (static_cast<int64_t>(blockIdx.y) * a.M + row) * a.C + f;
+      float* p = a.part + (static_cast<int64_t>(t.pad) * a.M + row) * a.C + f;
       store8<TF32, false>(p, left, gate);
       store8<TF32, false>(p + a.F, left, up);
       return;
@@ -141,13 +144,14 @@ hipError_t launch_reg(const Plan& p, GluArgs a, hipStream_t s) {
 
 template <class T, int ACT>
 hipError_t launch_16(const Plan& p, GluArgs a, bool aligned, hipStream_t s) {
-  if (p.regime == kStream) return launch_reg<T, 32, 256, 1, 4, 2, ACT>(p, a, s);
-  // the pipeline's 32-bit byte offsets: into all of x, and into 64 rows of W
-  if (!aligned || p.batch * a.R >= (int64_t(1) << 31) || a.C >= (int64_t(1) << 25))
-    return launch_reg<T, 128, 128, 2, 2, 2, ACT>(p, a, s);
+  // the direct-to-LDS kernels' 32-bit byte offsets: into all of x, and into 64 rows of W
+  aligned = aligned && p.batch * a.R < (int64_t(1) << 31) && a.C < (int64_t(1) << 25);
   a.n_slots = p.max_tiles;
   a.n_col_tiles = static_cast<int32_t>((a.F + 127) / 128);
-  return launch_pipe<T, GluOp<ACT>, false>(a, s);
+  if (p.regime == kStream)
+    return aligned ? launch_few<T, GluOp<ACT>, 32>(a, 0, p.ksplit, s) : launch_reg<T, 32, 256, 1, 4, 2, ACT>(p, a, s);
+  if (!aligned) return launch_reg<T, 128, 128, 2, 2, 2, ACT>(p, a, s);
+  return launch_pipe<T, GluOp<ACT>, false>(a, 1, s);
 }
 
 template <class T, int ACT>
@@ -160,9 +164,13 @@ hipError_t finish(const GluArgs& a, int32_t ksplit, hipStream_t s) {
 template <int ACT>
 hipError_t launch_act(const Plan& p, const GluArgs& a, bool aligned, hipStream_t s) {
   hipError_t e;
-  if (p.dtype == PGG_F32) return launch_reg<TF32, 128, 128, 2, 2, 2, ACT>(p, a, s);
-  e = p.dtype == PGG_BF16 ? launch_16<TBf16, ACT>(p, a, aligned, s) : launch_16<TF16, ACT>(p, a, aligned, s);
+  if (p.dtype == PGG_F32)
+    e = p.regime == kStream ? launch_reg<TF32, 32, 256, 1, 4, 2, ACT>(p, a, s)
+                            : launch_reg<TF32, 128, 128, 2, 2, 2, ACT>(p, a, s);
+  else
+    e = p.dtype == PGG_BF16 ? launch_16<TBf16, ACT>(p, a, aligned, s) : launch_16<TF16, ACT>(p, a, aligned, s);
   if (e != hipSuccess || p.ksplit == 1) return e;
+  if (p.dtype == PGG_F32) return finish<TF32, ACT>(a, p.ksplit, s);
   return p.dtype == PGG_BF16 ? finish<TBf16, ACT>(a, p.ksplit, s) : finish<TF16, ACT>(a, p.ksplit, s);
 }
 

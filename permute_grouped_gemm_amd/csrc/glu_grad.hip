@@ -27,7 +27,7 @@ struct GluGradArgs {
   const MTile* tiles;
   void* grad;               // [M, C]
   void* h;                  // [M, F] or NULL
-  int64_t R, C, F;
+  int64_t R, C, F, kspan;
   int32_t bm;               // rows of a table entry
   int32_t n_slots, n_col_tiles;
 };
@@ -214,29 +214,29 @@ void glu_grad_reg_kernel(GluGradArgs a) {
   store_blocks<T, Op, FM, FN>(a, tile, col0 + wn * WTN, wm * WTM, lane, acc);
 }
 
-template <class T, int BM, int ACT>
+template <class T, int BM, int WM, int EU, int ACT>
 hipError_t launch_reg(const Plan& p, GluGradArgs a, hipStream_t s) {
   constexpr int BN = 128;
   a.n_slots = p.max_tiles * (p.bm / BM);
   a.n_col_tiles = static_cast<int32_t>((a.F + BN - 1) / BN);
   unsigned tiles = static_cast<unsigned>(a.n_slots) * static_cast<unsigned>(a.n_col_tiles);
   tiles = (tiles + 8 * 32 - 1) / (8 * 32) * (8 * 32);
-  hipLaunchKernelGGL((glu_grad_reg_kernel<T, GluGradOp<ACT>, BM, BN, 2, 2, 2>), dim3(tiles), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((glu_grad_reg_kernel<T, GluGradOp<ACT>, BM, BN, WM, 4 / WM, EU>), dim3(tiles), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
 template <class T, int ACT>
 hipError_t launch_typed(const Plan& p, GluGradArgs a, bool aligned, hipStream_t s) {
-  if (p.bm == 64) return launch_reg<T, 64, ACT>(p, a, s);
+  if (p.bm == 32) return launch_reg<T, 32, 1, 4, ACT>(p, a, s);
   if constexpr (T::kPerChunk == 8) {
     // the pipeline's 32-bit byte offsets: into 256 rows of either operand
     if (aligned && p.bm == 256 && a.R < (int64_t(1) << 23)) {
       a.n_slots = p.max_tiles;
       a.n_col_tiles = static_cast<int32_t>((a.F + 255) / 256);
-      return launch_pipe<T, GluGradOp<ACT>, true>(a, s);
+      return launch_pipe<T, GluGradOp<ACT>, true>(a, 1, s);
     }
   }
-  return launch_reg<T, 128, ACT>(p, a, s);
+  return launch_reg<T, 128, 2, 2, ACT>(p, a, s);
 }
 
 template <int ACT>
@@ -260,6 +260,7 @@ hipError_t launch_glu_grad(const Plan& p, int32_t act, const void* grad_y, const
   a.R = p.N;          // the plan keeps the reduction in N and the columns in K
   a.F = p.K;
   a.C = 2 * p.K;
+  a.kspan = p.N;
   a.bm = p.bm;
   return act == PGG_ACT_SILU ? launch_act<PGG_ACT_SILU>(p, a, aligned, s)
                              : launch_act<PGG_ACT_GELU_TANH>(p, a, aligned, s);

@@ -30,7 +30,7 @@
 // split order and the tokens' z * B_p.
 #include <algorithm>
 
-#include "pgg_pipe.h"
+#include "pgg_few.h"
 #include "pgg_prep.h"
 
 namespace pgg {
@@ -51,6 +51,7 @@ struct LoraArgs {
   int64_t R, C, T, kspan;
   int64_t P;
   int32_t rank;
+  int32_t few;              // few tokens: z comes with the product, lora_finish_kernel adds z * B_p
   int32_t n_slots, n_col_tiles;
 };
 
@@ -78,68 +79,92 @@ __device__ void check_ids(const LoraArgs& a) {
   }
 }
 
-// Row of accumulator v in a 32 x 32 block (its column is the lane's place in its half).
-__device__ __forceinline__ int acc_row(int v, int lh) { return 8 * (v >> 2) + 4 * lh + (v & 3); }
-
 // ---------------------------------------------------------------- z, many tokens
 
-// 32 tokens x 32 ranks per workgroup (blockIdx.y: which 32 ranks), the
-// reduction split over its four waves and added in wave order.  The last
-// workgroup along x checks the ids.
-template <class T>
-__global__ __launch_bounds__(256) void lora_shrink_kernel(LoraArgs a) {
+// 32 tokens x 16 NB ranks per workgroup (blockIdx.y: which ranks), the
+// reduction split over its eight waves and added in wave order.  Bound by
+// reading x once: a load takes 64 bytes of 16 rows, and eight waves with 4 x
+// (2 + NB) loads each keep them coming.  The last workgroup along x checks the ids.
+template <class T, int NB>
+__global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a) {
   using E = typename T::elem;
-  constexpr int EPC = T::kPerChunk, kStep = 2 * EPC, kUnroll = 4;
-  __shared__ float red[4][32][33];
+  constexpr int EPC = T::kPerChunk, kStep = 4 * EPC, kUnroll = NB == 4 ? 2 : 4, kWaves = 8;
+  __shared__ float red[kWaves][32][16 * NB + 4];
   if (blockIdx.x == gridDim.x - 1) {
     if (blockIdx.y == 0) check_ids(a);
     return;
   }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int lr = lane & 31, lh = lane >> 5;
+  const int lr = lane & 15, lg = lane >> 4;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * 32;
   const int rows = static_cast<int>(min<int64_t>(32, a.T - t0));
-  const int r0 = blockIdx.y * 32;
+  const int r0 = blockIdx.y * 16 * NB;
   const int64_t R = a.R;
-  const int32_t id = lr < rows ? adapter_of(a, t0 + lr) : -1;
+  const int32_t id = (lane & 31) < rows ? adapter_of(a, t0 + (lane & 31)) : -1;
   // this wave's part of the reduction, in whole steps
   const int64_t steps = (R + kStep - 1) / kStep;
-  const int64_t per = (steps + 3) / 4;
+  const int64_t per = (steps + kWaves - 1) / kWaves;
   const int64_t s0 = min<int64_t>(steps, wave * per), s1 = min<int64_t>(steps, s0 + per);
-  const E* x = static_cast<const E*>(a.A) + (t0 + min(lr, rows - 1)) * R;
+  const int64_t s_whole = min<int64_t>(s1, R / kStep);
+  const E* x[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) x[i] = static_cast<const E*>(a.A) + (t0 + min(16 * i + lr, rows - 1)) * R + lg * EPC;
   uint32_t pending = static_cast<uint32_t>(__ballot(id >= 0));
   while (pending) {
     const int32_t p = __shfl(id, __builtin_ctz(pending));
     const uint32_t mine = static_cast<uint32_t>(__ballot(id == p));
     pending &= ~mine;
-    const E* ar = static_cast<const E*>(a.a) + (static_cast<int64_t>(p) * a.rank + min(r0 + lr, a.rank - 1)) * R;
-    f32x16_t acc;
+    const E* ar[NB];
 #pragma unroll
-    for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
+    for (int b = 0; b < NB; ++b)
+      ar[b] = static_cast<const E*>(a.a) +
+              (static_cast<int64_t>(p) * a.rank + min(r0 + 16 * b + lr, a.rank - 1)) * R + lg * EPC;
+    f32x4_t acc[2][NB];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) acc[i][b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     int64_t s = s0;
-    for (; s + kUnroll <= s1 && (s + kUnroll) * kStep <= R; s += kUnroll) {
-      u32x4_t fx[kUnroll], fw[kUnroll];
+    for (; s + kUnroll <= s_whole; s += kUnroll) {
+      u32x4_t fx[kUnroll][2], fw[kUnroll][NB];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const int64_t k = (s + u) * kStep + lh * EPC;
-        fx[u] = load16(x + k);
-        fw[u] = load16(ar + k);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) fx[u][i] = load16(x[i] + (s + u) * kStep);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) fw[u][b] = load16(ar[b] + (s + u) * kStep);
       }
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) mma<T>(acc, fx[u], fw[u]);
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) mma_block<T>(acc[i][b], fw[u][b], fx[u][i]);
     }
     for (; s < s1; ++s) {
-      const int64_t k = s * kStep + lh * EPC;
-      mma<T>(acc, load16_part<T>(x + k, R - k), load16_part<T>(ar + k, R - k));
-    }
+      const int64_t left = R - s * kStep - lg * EPC;
 #pragma unroll
-    for (int v = 0; v < 16; ++v) red[wave][acc_row(v, lh)][lr] = acc[v];
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          mma_block<T>(acc[i][b], load16_part<T>(ar[b] + s * kStep, left), load16_part<T>(x[i] + s * kStep, left));
+    }
+    // lane: token 16 i + lr, ranks 16 b + 4 lg ..
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        *reinterpret_cast<f32x4_t*>(&red[wave][16 * i + lr][16 * b + 4 * lg]) = acc[i][b];
     __syncthreads();
     const float scale = a.scales[p];
-    for (int e = threadIdx.x; e < 32 * 32; e += 256) {
-      const int m = e >> 5, r = e & 31;
-      if (((mine >> m) & 1) && r0 + r < a.rank)
-        a.z[(t0 + m) * a.rank + r0 + r] = scale * (((red[0][m][r] + red[1][m][r]) + red[2][m][r]) + red[3][m][r]);
+    for (int e = threadIdx.x; e < 32 * 16 * NB; e += 512) {
+      const int m = e / (16 * NB), r = e % (16 * NB);
+      if (((mine >> m) & 1) && r0 + r < a.rank) {
+        float sum = red[0][m][r];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) sum += red[w][m][r];
+        a.z[(t0 + m) * a.rank + r0 + r] = scale * sum;
+      }
     }
     __syncthreads();
   }
@@ -229,6 +254,14 @@ struct LoraOp {
 
   static __device__ __forceinline__ int64_t columns(const Args& a) { return a.C; }
 
+  // few tokens: workgroups that compute z, and one that checks the ids
+  static __device__ __forceinline__ int extra(const Args& a) { return a.few ? static_cast<int>(a.T) + 1 : 0; }
+  template <class T>
+  static __device__ __forceinline__ void extra_work(const Args& a, int i) {
+    if (i == a.T) check_ids(a);
+    else shrink_token<T>(a, i);
+  }
+
   // Adds z * B_p of every adapter p found among the wave's rows, adapters in
   // increasing order, kStep ranks at a time.  Lane l has row l % B of every
   // block of rows and column l % B of every block of columns, and place l / B
@@ -238,7 +271,8 @@ struct LoraOp {
                                                 Column column) {
     using E = typename T::elem;
     constexpr int EPC = T::kPerChunk, kStep = 64 / B * EPC, kNone = 0x7FFFFFFF;
-    if (a.part) return;
+    // with splits, the first one; with few tokens, lora_finish_kernel does it
+    if (a.few || t.pad != 0) return;
     int32_t id[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
@@ -310,13 +344,14 @@ struct LoraOp {
                                                const float (&v)[8], const Side<T>&) {
     const int64_t token = int64_t(t.row0) + m;
     if (a.part)
-      store8<TF32, false>(a.part + (static_cast<int64_t>(blockIdx.y) * a.T + token) * a.C + c, left, v);
+      store8<TF32, false>(a.part + (static_cast<int64_t>(t.pad) * a.T + token) * a.C + c, left, v);
     else
       store8<T>(static_cast<typename T::elem*>(a.y) + token * a.C + c, left, v);
   }
 };
 
-// Adds the splits' partial products in split order and the token's z * B_p.
+// Adds the splits' partial products in split order and, with few tokens, the
+// token's z * B_p.
 template <class T>
 __global__ __launch_bounds__(256) void lora_finish_kernel(LoraArgs a, int32_t ksplit) {
   using E = typename T::elem;
@@ -325,11 +360,13 @@ __global__ __launch_bounds__(256) void lora_finish_kernel(LoraArgs a, int32_t ks
   for (int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < n; e += step) {
     const int64_t t = e / a.C, c = e - t * a.C;
     float sum = a.part[e];
+#pragma unroll 8
     for (int32_t s = 1; s < ksplit; ++s) sum += a.part[s * n + e];
-    const int32_t p = adapter_of(a, t);
+    const int32_t p = a.few ? adapter_of(a, t) : -1;
     if (p >= 0) {
       const E* b = static_cast<const E*>(a.b) + static_cast<int64_t>(p) * a.rank * a.C + c;
       float d = 0.0f;
+#pragma unroll 8
       for (int32_t r = 0; r < a.rank; ++r) d = fmaf(a.z[t * a.rank + r], to_float<T>(b[r * a.C]), d);
       sum += d;
     }
@@ -338,37 +375,49 @@ __global__ __launch_bounds__(256) void lora_finish_kernel(LoraArgs a, int32_t ks
 }
 
 template <class T, int BM, int BN, int WM, int WN>
-hipError_t launch_tiles(LoraArgs a, const LoraPlan& p, hipStream_t s) {
+hipError_t launch_reg(LoraArgs a, const LoraPlan& p, hipStream_t s) {
   a.n_slots = static_cast<int32_t>((a.T + BM - 1) / BM);
   a.n_col_tiles = static_cast<int32_t>((a.C + BN - 1) / BN);
   return launch_nn_reg<T, LoraOp, BM, BN, WM, WN, 2>(a, p.ksplit, s);
 }
 
+template <class T, int NB>
+hipError_t launch_shrink(const LoraArgs& a, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>((a.T + 31) / 32 + 1), static_cast<unsigned>((a.rank + 16 * NB - 1) / (16 * NB)));
+  hipLaunchKernelGGL((lora_shrink_kernel<T, NB>), grid, dim3(512), 0, s, a);
+  return hipGetLastError();
+}
+
 template <class T>
 hipError_t launch_typed(const LoraPlan& p, LoraArgs a, bool aligned, hipStream_t s) {
-  if (a.T <= kLoraFewTokens) {
+  // the direct-to-LDS kernels' 32-bit byte offsets: into 256 rows of x and 64 rows of W
+  const bool direct = T::kPerChunk == 8 && aligned && a.R < (int64_t(1) << 23) && a.C < (int64_t(1) << 25);
+  hipError_t e = hipSuccess;
+  if (!a.few) {
+    e = a.rank <= 16 ? launch_shrink<T, 1>(a, s) : a.rank <= 32 ? launch_shrink<T, 2>(a, s) : launch_shrink<T, 4>(a, s);
+  } else if (!direct) {
     hipLaunchKernelGGL((lora_shrink_few_kernel<T>), dim3(static_cast<unsigned>(a.T + 1)), dim3(256), 0, s, a);
-  } else {
-    const dim3 grid(static_cast<unsigned>((a.T + 31) / 32 + 1), static_cast<unsigned>((a.rank + 31) / 32));
-    hipLaunchKernelGGL((lora_shrink_kernel<T>), grid, dim3(256), 0, s, a);
+    e = hipGetLastError();
   }
-  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if constexpr (T::kPerChunk == 8) {
-    if (p.tile == kLoraRows32) {
-      e = launch_tiles<T, 32, 256, 1, 4>(a, p, s);
-    } else if (p.tile == kLoraRows256 && aligned && a.R < (int64_t(1) << 23) && a.C < (int64_t(1) << 25)) {
-      // (32-bit byte offsets into 256 rows of x and 64 rows of W)
+    a.n_col_tiles = static_cast<int32_t>((a.C + 255) / 256);
+    if (a.few && direct) {
+      a.n_slots = 1;
+      e = a.T <= 32 ? launch_few<T, LoraOp, 32>(a, static_cast<int32_t>(a.T) + 1, p.ksplit, s)
+                    : launch_few<T, LoraOp, 64>(a, static_cast<int32_t>(a.T) + 1, p.ksplit, s);
+    } else if (a.few) {
+      e = launch_reg<T, 32, 256, 1, 4>(a, p, s);
+    } else if (p.pipe && direct) {
       a.n_slots = static_cast<int32_t>((a.T + 255) / 256);
-      a.n_col_tiles = static_cast<int32_t>((a.C + 255) / 256);
-      e = launch_pipe<T, LoraOp, false>(a, s);
+      e = launch_pipe<T, LoraOp, false>(a, p.ksplit, s);
     } else {
-      e = launch_tiles<T, 128, 128, 2, 2>(a, p, s);
+      e = launch_reg<T, 128, 128, 2, 2>(a, p, s);
     }
   } else {
-    e = p.tile == kLoraRows32 ? launch_tiles<T, 32, 128, 1, 4>(a, p, s) : launch_tiles<T, 128, 128, 2, 2>(a, p, s);
+    e = a.few ? launch_reg<T, 32, 128, 1, 4>(a, p, s) : launch_reg<T, 128, 128, 2, 2>(a, p, s);
   }
-  if (e != hipSuccess || p.ksplit == 1) return e;
+  if (e != hipSuccess || !a.part) return e;
   const int64_t blocks = std::min<int64_t>((a.T * a.C + 255) / 256, 4096);
   hipLaunchKernelGGL((lora_finish_kernel<T>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a, p.ksplit);
   return hipGetLastError();
@@ -388,7 +437,8 @@ hipError_t launch_lora(const LoraPlan& p, const void* x, const void* weight, con
   g.scales = scales;
   g.z = reinterpret_cast<float*>(base + p.off_z);
   g.y = y;
-  g.part = p.ksplit > 1 ? reinterpret_cast<float*>(base + p.off_part) : nullptr;
+  g.few = p.few;
+  g.part = p.few || p.ksplit > 1 ? reinterpret_cast<float*>(base + p.off_part) : nullptr;
   g.hdr = reinterpret_cast<WsHeader*>(base + p.off_header);
   g.R = p.K;
   g.C = p.N;

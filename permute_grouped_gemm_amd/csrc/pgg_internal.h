@@ -202,11 +202,11 @@ hipError_t launch_glu_grad(const Plan& p, int32_t act, const void* grad_y, const
                            void* grad, void* h, bool aligned, const WsView& w, hipStream_t s);
 
 // Shared projection with low-rank adapters.
-enum LoraTile : int32_t { kLoraRows32 = 0, kLoraRows128 = 1, kLoraRows256 = 2 };
-constexpr int64_t kLoraFewTokens = 64;
 struct LoraPlan {
   int64_t T, K, N, P;
-  int32_t rank, dtype, tile;
+  int32_t rank, dtype;
+  bool few;             // few tokens: one tile of rows, the reduction split, z beside it
+  bool pipe;            // 16-bit types with 16-byte rows: 256 x 256 tiles
   int32_t ksplit;       // reduction splits (1: none)
   int64_t kspan;        // reduction elements per split
   size_t off_header, off_z, off_part, total;

@@ -7,8 +7,9 @@
 //
 //   Op::Args                 kernel arguments, with A, W, R (the reduction), C
 //                            (the row length of W), n_slots, n_col_tiles, and
-//                            kspan (reduction elements of one blockIdx.y)
-//   Op::tile(args, slot, t)  rows [t.row0, t.row0 + t.rows) of group t.g; false: no tile
+//                            kspan (reduction elements of one split)
+//   Op::tile<BM>(args, slot, t)  rows [t.row0, t.row0 + t.rows) of group t.g; false:
+//                            no tile.  (The kernels put the split into t.pad.)
 //   Op::src(args, t, r)      row of A that tile row r reads
 //   Op::weight(args, t)      first element of the tile's W
 //   Op::column<BN>(args, ct, n)  column of W at column n (a multiple of 4) of
@@ -252,9 +253,16 @@ void nn_reg_kernel(typename Op::Args a) {
   __shared__ u32x4_t lds[2][A_CHUNKS + B_CHUNKS];
 
   int slot, ct;
-  if (!raster<8, 4>(blockIdx.x, a.n_slots, a.n_col_tiles, slot, ct)) return;
+  if constexpr (BM == 32) {   // few rows: columns fastest, over all XCDs
+    ct = blockIdx.x % a.n_col_tiles;
+    slot = blockIdx.x / a.n_col_tiles;
+    if (slot >= a.n_slots) return;
+  } else {
+    if (!raster<8, 4>(blockIdx.x, a.n_slots, a.n_col_tiles, slot, ct)) return;
+  }
   MTile tile;
   if (!Op::template tile<BM>(a, slot, tile)) return;
+  tile.pad = blockIdx.y;
   const int rows = tile.rows;
   const int64_t C = a.C;
   const int64_t kbeg = static_cast<int64_t>(blockIdx.y) * a.kspan;

@@ -64,12 +64,19 @@ __device__ __forceinline__ void plain_barrier() {
 // l % 16 of either operand, and of the result column l % 16, rows 4 (l / 16) on.
 template <class T>
 __device__ __forceinline__ void mma_block(f32x4_t& acc, u32x4_t a, u32x4_t b) {
-  if constexpr (__is_same(T, TBf16))
+  if constexpr (__is_same(T, TBf16)) {
     acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b),
                                                   acc, 0, 0, 0);
-  else
+  } else if constexpr (__is_same(T, TF32)) {   // 4 elements, from 4 (l / 16) on: one instruction each
+    const f32x4_t fa = __builtin_bit_cast(f32x4_t, a), fb = __builtin_bit_cast(f32x4_t, b);
+    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(fa[0], fb[0], acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(fa[1], fb[1], acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(fa[2], fb[2], acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(fa[3], fb[3], acc, 0, 0, 0);
+  } else {
     acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b),
                                                  acc, 0, 0, 0);
+  }
 }
 
 // Two neighbouring 16 x 16 blocks, columns first: accumulator v of lane l is
@@ -112,6 +119,47 @@ __device__ __forceinline__ u32x4_t read_quarter(const char* base, int s, int n, 
   return u32x4_t{part[0][0], part[0][1], part[1][0], part[1][1]};
 }
 
+// A wave's accumulators: NI blocks of 16 rows from tile row m0 on, and two runs
+// of 32 columns, the first from output column c0 on.
+template <class T, class Op, int NI>
+__device__ __forceinline__ void store_runs(const typename Op::Args& a, const MTile& tile, int64_t c0, int m0, int lane,
+                                           f32x4_t (&acc)[NI][4]) {
+  Op::template adjust<T, 16>(a, tile, m0, lane, acc, [&](int j) { return c0 + 128 * (j >> 1) + 16 * (j & 1); });
+  auto row = [&](int i) { return m0 + i * 16 + (lane & 15); };
+  auto left = [&](int i, int64_t c) { return row(i) < tile.rows ? Op::columns(a) - c : 0; };
+  const int64_t c1 = c0 + run_column(lane);
+  if constexpr (Op::kPaired) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      float v[8], w[8];
+      piece16(acc[i][0], acc[i][1], v);
+      piece16(acc[i][2], acc[i][3], w);
+      Op::template piece<T>(a, tile, row(i), c1, left(i, c1), v, w);
+    }
+  } else {
+    // what the pieces need from memory is loaded kAhead rows of blocks ahead
+    constexpr int kAhead = 2;
+    typename Op::template Side<T> side[kAhead][2];
+    auto fetch = [&](int i) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        side[i % kAhead][j] = Op::template fetch<T>(a, tile, row(i), c1 + 128 * j, left(i, c1 + 128 * j));
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch(i);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float v[8];
+        piece16(acc[i][2 * j], acc[i][2 * j + 1], v);
+        Op::template piece<T>(a, tile, row(i), c1 + 128 * j, left(i, c1 + 128 * j), v, side[i % kAhead][j]);
+      }
+      if (i + kAhead < NI) fetch(i + kAhead);
+    }
+  }
+}
+
 template <bool B>
 struct Whole {
   static constexpr bool value = B;
@@ -129,7 +177,11 @@ void pipe_kernel(typename Op::Args a) {
   if (!raster<8, 4>(blockIdx.x, a.n_slots, a.n_col_tiles, slot, ct)) return;
   MTile tile;
   if (!Op::template tile<256>(a, slot, tile)) return;
+  tile.pad = blockIdx.y;
+  // this workgroup's split of the reduction
   const int64_t R = a.R, C = a.C;
+  const int64_t kbeg = static_cast<int64_t>(blockIdx.y) * a.kspan;
+  const int64_t span = min<int64_t>(R - kbeg, a.kspan);
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -142,7 +194,7 @@ void pipe_kernel(typename Op::Args a) {
   const int l8 = lane >> 3;
   const int chunk = a_slot(8 * wave + l8, lane & 7);
   const int64_t row_base = Op::src_base(a, tile);
-  const char* pa = reinterpret_cast<const char*>(static_cast<const E*>(a.A) + row_base * R);
+  const char* pa = reinterpret_cast<const char*>(static_cast<const E*>(a.A) + row_base * R + kbeg);
   uint32_t oa[2][2];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
@@ -153,7 +205,7 @@ void pipe_kernel(typename Op::Args a) {
     }
   // Load u of quarter B_j.  NT: 8 columns' rows, as for A.  Otherwise 4 rows of
   // k, 256 bytes each, whose 16-byte chunks sit where quarter_offset puts them.
-  const E* W = static_cast<const E*>(a.W) + Op::weight(a, tile);
+  const E* W = static_cast<const E*>(a.W) + Op::weight(a, tile) + kbeg * (NT ? 1 : C);
   const int kq = lane >> 4;                                     // which of the 4 rows
   const char* pb;
   uint32_t ob[2][2];
@@ -181,8 +233,8 @@ void pipe_kernel(typename Op::Args a) {
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(lds));
   const void* zero = &kZero16;
 
-  const int nk = static_cast<int>((R + 63) >> 6);
-  const int n_full = static_cast<int>(R >> 6);      // stages without a tail
+  const int nk = static_cast<int>((span + 63) >> 6);
+  const int n_full = static_cast<int>(span >> 6);      // stages without a tail
   // The two loads of a quarter for stage kt.  Whole: the stage lies inside the
   // reduction.  Otherwise elements past it read zeros (also whole stages, as
   // every phase issues its two loads).
@@ -192,7 +244,7 @@ void pipe_kernel(typename Op::Args a) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       if constexpr (decltype(whole)::value) dma16_off(p, oa[h][u], m0 + u * 8192);
-      else dma16(kt * 64 + chunk * 8 < R ? static_cast<const void*>(p + oa[h][u]) : zero, m0 + u * 8192);
+      else dma16(kt * 64 + chunk * 8 < span ? static_cast<const void*>(p + oa[h][u]) : zero, m0 + u * 8192);
     }
   };
   auto load_b = [&](int kt, int j, auto whole) {
@@ -202,7 +254,7 @@ void pipe_kernel(typename Op::Args a) {
     for (int u = 0; u < 2; ++u) {
       const int64_t k = static_cast<int64_t>(kt) * 64 + (NT ? chunk * 8 : 32 * u + 4 * wave + kq);
       if constexpr (decltype(whole)::value) dma16_off(p, ob[j][u], m0 + u * 8192);
-      else dma16(k < R ? static_cast<const void*>(p + ob[j][u]) : zero, m0 + u * 8192);
+      else dma16(k < span ? static_cast<const void*>(p + ob[j][u]) : zero, m0 + u * 8192);
     }
   };
   // fragments of a quarter, [16 rows or columns][32 reduction elements]
@@ -289,48 +341,14 @@ void pipe_kernel(typename Op::Args a) {
   if (wave < 4) plain_barrier();
   fetched_barrier<0>();   // the zeros past the reduction have landed before LDS is released
 
-  const int64_t c0 = Op::first_column(ct, 256) + wn * 32;
-  Op::template adjust<T, 16>(a, tile, wm * 128, lane, acc, [&](int j) { return c0 + 128 * (j >> 1) + 16 * (j & 1); });
-  auto row = [&](int i) { return wm * 128 + i * 16 + lr; };
-  auto left = [&](int i, int64_t c) { return row(i) < tile.rows ? Op::columns(a) - c : 0; };
-  const int64_t c1 = c0 + run_column(lane);
-  if constexpr (Op::kPaired) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float v[8], w[8];
-      piece16(acc[i][0], acc[i][1], v);
-      piece16(acc[i][2], acc[i][3], w);
-      Op::template piece<T>(a, tile, row(i), c1, left(i, c1), v, w);
-    }
-  } else {
-    // what the pieces need from memory is loaded kAhead rows of blocks ahead
-    constexpr int kAhead = 2;
-    typename Op::template Side<T> side[kAhead][2];
-    auto fetch = [&](int i) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        side[i % kAhead][j] = Op::template fetch<T>(a, tile, row(i), c1 + 128 * j, left(i, c1 + 128 * j));
-    };
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) fetch(i);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float v[8];
-        piece16(acc[i][2 * j], acc[i][2 * j + 1], v);
-        Op::template piece<T>(a, tile, row(i), c1 + 128 * j, left(i, c1 + 128 * j), v, side[i % kAhead][j]);
-      }
-      if (i + kAhead < 8) fetch(i + kAhead);
-    }
-  }
+  store_runs<T, Op, 8>(a, tile, Op::first_column(ct, 256) + wn * 32, wm * 128, lane, acc);
 }
 
 template <class T, class Op, bool NT>
-hipError_t launch_pipe(const typename Op::Args& a, hipStream_t s) {
+hipError_t launch_pipe(const typename Op::Args& a, int ksplit, hipStream_t s) {
   unsigned tiles = static_cast<unsigned>(a.n_slots) * static_cast<unsigned>(a.n_col_tiles);
   tiles = (tiles + 8 * 32 - 1) / (8 * 32) * (8 * 32);   // whole raster rounds
-  hipLaunchKernelGGL((pipe_kernel<T, Op, NT>), dim3(tiles), dim3(512), 0, s, a);
+  hipLaunchKernelGGL((pipe_kernel<T, Op, NT>), dim3(tiles, static_cast<unsigned>(ksplit)), dim3(512), 0, s, a);
   return hipGetLastError();
 }
 

@@ -497,6 +497,22 @@ pgg_status check_gate_desc(const pgg_moe_gate_desc* d) {
   return PGG_OK;
 }
 
+namespace {
+
+// Splits of a reduction of n elements for `busy` tiles: enough that about
+// `target` workgroups run, each with at least min_span elements (a multiple of 64).
+template <class Span>
+void split_reduction(int64_t n, int64_t busy, int64_t target, int64_t min_span, int32_t* ksplit, Span* kspan) {
+  constexpr int64_t kStage = 64, kMost = 64;
+  int64_t split = std::min<int64_t>((target + busy / 2) / busy, n / min_span);
+  split = std::max<int64_t>(1, std::min<int64_t>(split, kMost));
+  const int64_t span = ((n + split - 1) / split + kStage - 1) / kStage * kStage;
+  *kspan = static_cast<Span>(span);
+  *ksplit = static_cast<int32_t>((n + span - 1) / span);
+}
+
+}  // namespace
+
 pgg_status make_glu_plan(const pgg_moe_glu_desc* d, Plan* p) {
   if (!d || !p) return PGG_ERR_INVALID_ARG;
   if (d->act != PGG_ACT_SILU && d->act != PGG_ACT_GELU_TANH) return PGG_ERR_INVALID_ARG;
@@ -520,6 +536,29 @@ pgg_status make_glu_plan(const pgg_moe_glu_desc* d, Plan* p) {
   // times as many as the plan's; a launch holds fewer than 2^32 lanes
   if (int64_t(p->max_tiles) * p->n_col_tiles >= (int64_t(1) << 21)) return PGG_ERR_UNSUPPORTED;
   p->fused_prep = p->M <= 1024;
+  // Few rows per expert: m-tiles of 32 rows x 256 columns (128 of h), the
+  // reduction split until about 512 workgroups have work, two per compute unit.
+  if (p->M <= 64 * p->G) {
+    p->regime = kStream;
+    p->bm = 32;
+    p->bn = 256;
+    p->max_tiles = static_cast<int32_t>((p->M + 31) / 32 + p->G);
+    p->n_col_tiles = static_cast<int32_t>((p->K + 255) / 256);
+  }
+  p->max_tiles = static_cast<int32_t>(std::min<int64_t>(p->max_tiles, p->M));   // each holds a row at least
+  if (p->regime == kStream) {
+    split_reduction(p->N, int64_t(p->max_tiles) * p->n_col_tiles, 512, p->dtype == PGG_F32 ? 32 : 256, &p->ksplit, &p->kspan);
+  }
+  p->tc = p->max_tiles;
+  size_t off = p->off_tiles;
+  off = align_up(off + sizeof(MTile) * size_t(p->max_tiles), kRegionAlign);
+  p->off_chunks = off;   off = align_up(off + sizeof(int32_t) * size_t(p->max_chunks + 1), kRegionAlign);
+  p->off_inv = off;      off = align_up(off + sizeof(int32_t) * size_t(p->M), kRegionAlign);
+  p->off_ori = off;      off = align_up(off + sizeof(int32_t) * size_t(p->M), kRegionAlign);
+  p->table_bytes = p->off_ring = off;
+  p->ring_bytes = p->ksplit > 1 ? size_t(p->ksplit) * size_t(p->M) * size_t(p->K) * sizeof(float) : 0;
+  p->ring_rows = 0;
+  p->total = align_up(off + p->ring_bytes, kRegionAlign);
   return PGG_OK;
 }
 
@@ -539,9 +578,9 @@ pgg_status make_glu_grad_plan(const pgg_moe_glu_grad_desc* d, Plan* p) {
   q.panel_cols = F;
   q.dtype = d->grad_y_dtype;
   q.regime = q.dtype == PGG_F32 ? kF32 : kLarge;
-  q.bm = M <= 64 * G ? 64 : q.dtype == PGG_F32 ? 128 : 256;
+  q.bm = M <= 64 * G ? 32 : q.dtype == PGG_F32 ? 128 : 256;
   q.bn = 128;
-  const int64_t max_tiles = (M + q.bm - 1) / q.bm + G;
+  const int64_t max_tiles = std::min<int64_t>(M, (M + q.bm - 1) / q.bm + G);   // each holds a row at least
   const int64_t col_tiles = (F + q.bn - 1) / q.bn;
   // launches of fewer than 2^32 lanes, also as tiles of 128 rows
   if (max_tiles * col_tiles >= (int64_t(1) << 22)) return PGG_ERR_UNSUPPORTED;
@@ -579,30 +618,21 @@ pgg_status make_lora_plan(const pgg_lora_desc* d, LoraPlan* p) {
   q.dtype = d->dtype;
   const bool f32 = q.dtype == PGG_F32;
   auto tiles = [&](int64_t bm, int64_t bn) { return ((q.T + bm - 1) / bm) * ((q.N + bn - 1) / bn); };
-  int64_t count;
-  if (q.T <= kLoraFewTokens) {
-    q.tile = kLoraRows32;
-    count = tiles(32, f32 ? 128 : 256);
-  } else if (!f32 && tiles(256, 256) >= 160) {
-    q.tile = kLoraRows256;
-    count = tiles(256, 256);
-  } else {
-    q.tile = kLoraRows128;
-    count = tiles(128, 128);
-  }
   if (tiles(32, 128) >= (int64_t(1) << 23)) return PGG_ERR_UNSUPPORTED;   // launches of fewer than 2^32 lanes
-  // Splits of the reduction until about 512 workgroups stream (two per compute
-  // unit), each of at least 256 elements.
-  constexpr int64_t kStage = 64, kMinSpan = 256, kTarget = 512;
-  int64_t split = q.tile == kLoraRows256 ? 1 : std::min<int64_t>(kTarget / count, q.K / kMinSpan);
-  split = std::max<int64_t>(1, std::min<int64_t>(split, 64));
-  q.kspan = ((q.K + split - 1) / split + kStage - 1) / kStage * kStage;
-  q.ksplit = static_cast<int32_t>((q.K + q.kspan - 1) / q.kspan);
+  // Up to 64 tokens the projection is bound by reading W: one tile of rows, the
+  // reduction split over about 512 workgroups, two per compute unit.  Above
+  // that, the 256 x 256 tiles (one workgroup per compute unit) or the 128 x 128
+  // ones (two), split where there are too few of them.
+  q.few = q.T <= 64;
+  q.pipe = !q.few && !f32 && q.K % 8 == 0 && q.N % 8 == 0;
+  if (q.few) split_reduction(q.K, tiles(64, f32 ? 128 : 256), 512, 192, &q.ksplit, &q.kspan);
+  else if (q.pipe) split_reduction(q.K, tiles(256, 256), 256, 512, &q.ksplit, &q.kspan);
+  else split_reduction(q.K, tiles(128, 128), 512, 512, &q.ksplit, &q.kspan);
   size_t off = 0;
   q.off_header = off; off = align_up(off + sizeof(WsHeader), kRegionAlign);
   q.off_z = off;      off = align_up(off + sizeof(float) * size_t(q.T) * size_t(q.rank), kRegionAlign);
   q.off_part = off;
-  if (q.ksplit > 1)
+  if (q.few || q.ksplit > 1)
     off = align_up(off + sizeof(float) * size_t(q.ksplit) * size_t(q.T) * size_t(q.N), kRegionAlign);
   q.total = off;
   *p = q;
