@@ -787,8 +787,9 @@ def _value_type(t, name, dim):
 
 
 def _on_stream(stream, dev):
-    """Handle of ``stream``, or of the current stream of ``dev``."""
-    return int((torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream)
+    """Handle of ``stream``, or of the current stream of ``dev`` (asked for
+    directly: a Stream object would cost a small call 2 of its 10 us)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else int(stream.cuda_stream)
 
 
 def _fresh(shape, dtype, dev, stream):

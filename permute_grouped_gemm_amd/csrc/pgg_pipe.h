@@ -7,7 +7,8 @@
 // with the transposing ds_read_b64_tr_b16, as in pgg_nn.h), or NT = true, rows
 // of R contiguous reduction elements, one per output column (read like A).
 //
-// 8 waves (2 along rows x 4 along columns, two per SIMD), 128 x 64
+// 8 waves (2 along rows x 4 along columns; the two of a SIMD differ in their
+// rows), 128 x 64
 // accumulators each, in 16 x 16 blocks.  Its columns are two runs of 32, run j
 // at tile column 128 j + 32 wn, so that all waves' first runs make one of 128
 // and the second runs another.  (A gated product puts gate columns in one and
@@ -186,7 +187,9 @@ void pipe_kernel(typename Op::Args a) {
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave & 1, wn = wave >> 1;
+  const int wm = wave >> 2, wn = wave & 3;
+  // quarters A_h of this wave that hold rows of the tile: the others are not multiplied
+  const bool has0 = tile.rows > wm * 128, has1 = tile.rows > wm * 128 + 64;
   const int lr = lane & 15, lg = lane >> 4;
 
   // Load u of quarter A_h of this wave: 8 tile rows 128 u + 64 h + 8 wave + ...,
@@ -299,29 +302,32 @@ void pipe_kernel(typename Op::Args a) {
   };
 
   u32x4_t fa[4][2], fb0[2][2], fb1[2][2];
-  auto stage = [&](int kt, auto whole) {
-    read_a(kt, 0, fa);
-    read_b(kt, 0, fb0);
+  auto stage = [&](int kt, auto whole, auto full) {
+    const bool work0 = decltype(full)::value || has0, work1 = decltype(full)::value || has1;
+    if (work0) {
+      read_a(kt, 0, fa);
+      read_b(kt, 0, fb0);
+    }
     load_a(kt + 1, 1, whole);
     fetched_barrier<10>();
-    multiply(0, 0, fa, fb0);
+    if (work0) multiply(0, 0, fa, fb0);
     plain_barrier();
 
-    read_b(kt, 1, fb1);
+    if (work0) read_b(kt, 1, fb1);
     load_a(kt + 2, 0, whole);
     fetched_barrier<10>();
-    multiply(0, 1, fa, fb1);
+    if (work0) multiply(0, 1, fa, fb1);
     plain_barrier();
 
-    read_a(kt, 1, fa);
+    if (work1) read_a(kt, 1, fa);
     load_b(kt + 2, 0, whole);
     fetched_barrier<-1>();
-    multiply(1, 1, fa, fb1);
+    if (work1) multiply(1, 1, fa, fb1);
     plain_barrier();
 
     load_b(kt + 2, 1, whole);
     fetched_barrier<10>();
-    multiply(1, 0, fa, fb0);
+    if (work1) multiply(1, 0, fa, fb0);
     plain_barrier();
   };
   const Whole<true> yes;
@@ -336,8 +342,11 @@ void pipe_kernel(typename Op::Args a) {
   fetched_barrier<10>();
   if (wave >= 4) plain_barrier();   // the second wave of each SIMD: half a phase behind
   int kt = 0;
-  for (; kt + 2 < n_full; ++kt) stage(kt, yes);
-  for (; kt < nk; ++kt) stage(kt, no);
+  if (tile.rows > 192)
+    for (; kt + 2 < n_full; ++kt) stage(kt, yes, yes);
+  else
+    for (; kt + 2 < n_full; ++kt) stage(kt, yes, no);
+  for (; kt < nk; ++kt) stage(kt, no, yes);
   if (wave < 4) plain_barrier();
   fetched_barrier<0>();   // the zeros past the reduction have landed before LDS is released
 
