@@ -29,6 +29,8 @@ namespace {
 struct GluArgs {
   const void* A;            // x [batch, R]
   const void* W;            // weight [G, R, C]
+  const void* A_end;        // where they end
+  const void* W_end;
   const WsHeader* hdr;
   const MTile* tiles;
   const int32_t* ori;       // expanded row -> original position
@@ -187,6 +189,9 @@ hipError_t launch_glu(const Plan& p, int32_t act, const void* x, const void* wei
   a.h = h;
   a.gate_up = gate_up;
   a.part = p.ksplit > 1 ? w.ring : nullptr;
+  const size_t es = p.dtype == PGG_F32 ? 4 : 2;
+  a.A_end = static_cast<const char*>(x) + es * p.batch * p.N;
+  a.W_end = static_cast<const char*>(weight) + es * p.G * p.N * p.K;
   a.R = p.N;          // the plan keeps the reduction in N and the columns in K
   a.C = p.K;
   a.F = p.K / 2;

@@ -22,6 +22,8 @@ namespace {
 struct GluGradArgs {
   const void* A;            // grad_y [M, R]
   const void* W;            // weight [G, F, R]
+  const void* A_end;        // where they end
+  const void* W_end;
   const void* gate_up;      // [M, C]
   const WsHeader* hdr;
   const MTile* tiles;
@@ -113,7 +115,7 @@ void glu_grad_reg_kernel(GluGradArgs a) {
   __shared__ u32x4_t lds[2][A_CHUNKS + B_CHUNKS];
 
   int slot, ct;
-  if (!raster<8, 4>(blockIdx.x, a.n_slots, a.n_col_tiles, slot, ct)) return;
+  if (!tile_place(a, slot, ct)) return;
   MTile tile;
   if (!Op::template tile<BM>(a, slot, tile)) return;
   const int64_t col0 = Op::first_column(ct, BN);
@@ -150,10 +152,10 @@ void glu_grad_reg_kernel(GluGradArgs a) {
     } else {
 #pragma unroll
       for (int s = 0; s < A_PER_T; ++s)
-        ra[s] = load16_part<T>(arow[s] + k0, D - k0 - (tid + s * NT) % kChunks * EPC);
+        ra[s] = load16_part<T>(arow[s] + k0, D - k0 - (tid + s * NT) % kChunks * EPC, a.A_end);
 #pragma unroll
       for (int s = 0; s < B_PER_T; ++s)
-        rb[s] = load16_part<T>(brow[s] + k0, D - k0 - (tid + s * NT) % kChunks * EPC);
+        rb[s] = load16_part<T>(brow[s] + k0, D - k0 - (tid + s * NT) % kChunks * EPC, a.W_end);
     }
   };
   auto store_stage = [&](int buf) {
@@ -219,9 +221,7 @@ hipError_t launch_reg(const Plan& p, GluGradArgs a, hipStream_t s) {
   constexpr int BN = 128;
   a.n_slots = p.max_tiles * (p.bm / BM);
   a.n_col_tiles = static_cast<int32_t>((a.F + BN - 1) / BN);
-  unsigned tiles = static_cast<unsigned>(a.n_slots) * static_cast<unsigned>(a.n_col_tiles);
-  tiles = (tiles + 8 * 32 - 1) / (8 * 32) * (8 * 32);
-  hipLaunchKernelGGL((glu_grad_reg_kernel<T, GluGradOp<ACT>, BM, BN, WM, 4 / WM, EU>), dim3(tiles), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((glu_grad_reg_kernel<T, GluGradOp<ACT>, BM, BN, WM, 4 / WM, EU>), dim3(tile_blocks(a)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -257,6 +257,9 @@ hipError_t launch_glu_grad(const Plan& p, int32_t act, const void* grad_y, const
   a.tiles = w.tiles;
   a.grad = grad;
   a.h = h;
+  const size_t es = p.dtype == PGG_F32 ? 4 : 2;
+  a.A_end = static_cast<const char*>(grad_y) + es * p.M * p.N;
+  a.W_end = static_cast<const char*>(weight) + es * p.G * p.K * p.N;
   a.R = p.N;          // the plan keeps the reduction in N and the columns in K
   a.F = p.K;
   a.C = 2 * p.K;

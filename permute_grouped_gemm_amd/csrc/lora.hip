@@ -40,8 +40,11 @@ namespace {
 struct LoraArgs {
   const void* A;            // x [T, R]
   const void* W;            // weight [R, C]
+  const void* A_end;        // where they end
+  const void* W_end;
   const void* a;            // [P, rank, R]
   const void* b;            // [P, rank, C]
+  const void* a_end;        // where a ends
   const int64_t* ids;       // [T]
   const float* scales;      // [P]
   float* z;                 // [T, rank]
@@ -152,7 +155,8 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a) {
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int b = 0; b < NB; ++b)
-          mma_block<T>(acc[i][b], load16_part<T>(ar[b] + s * kStep, left), load16_part<T>(x[i] + s * kStep, left));
+          mma_block<T>(acc[i][b], load16_part<T>(ar[b] + s * kStep, left, a.a_end),
+                       load16_part<T>(x[i] + s * kStep, left, a.A_end));
     }
     // lane: token 16 i + lr, ranks 16 b + 4 lg ..
 #pragma unroll
@@ -206,8 +210,8 @@ __device__ __forceinline__ void shrink_few(const LoraArgs& a, int block) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int64_t at = k + u * 64 * EPC;
-      vx[u] = load16_part<T>(x + at, a.R - at);
-      vw[u] = load16_part<T>(ar + at, a.R - at);
+      vx[u] = load16_part<T>(x + at, a.R - at, a.A_end);
+      vw[u] = load16_part<T>(ar + at, a.R - at, a.a_end);
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -463,6 +467,10 @@ hipError_t launch_lora(const LoraPlan& p, const void* x, const void* weight, con
   g.few = p.few;
   g.part = p.few || p.ksplit > 1 ? reinterpret_cast<float*>(base + p.off_part) : nullptr;
   g.hdr = reinterpret_cast<WsHeader*>(base + p.off_header);
+  const size_t es = p.dtype == PGG_F32 ? 4 : 2;
+  g.A_end = static_cast<const char*>(x) + es * p.T * p.K;
+  g.W_end = static_cast<const char*>(weight) + es * p.K * p.N;
+  g.a_end = static_cast<const char*>(a) + es * p.P * p.rank * p.K;
   g.R = p.K;
   g.C = p.N;
   g.T = p.T;

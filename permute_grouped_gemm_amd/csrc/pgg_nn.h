@@ -5,7 +5,8 @@
 // for a block of rows that share the [R, C] matrix W.  What differs between
 // the operators that use them comes as an Op:
 //
-//   Op::Args                 kernel arguments, with A, W, R (the reduction), C
+//   Op::Args                 kernel arguments, with A, W and where they end
+//                            (A_end, W_end), R (the reduction), C
 //                            (the row length of W), n_slots, n_col_tiles, and
 //                            kspan (reduction elements of one split)
 //   Op::tile<BM>(args, slot, t)  rows [t.row0, t.row0 + t.rows) of group t.g; false:
@@ -71,18 +72,48 @@ __device__ __forceinline__ u32x4_t load16(const E* p) {
   return v;
 }
 
-// The same with only the first `left` elements read, zeros after them.
+// The same of which only the first `left` elements count: zeros after them.
+// Reads up to 16 bytes from p on, but nothing at `end` or past it.
 template <class T>
-__device__ __forceinline__ u32x4_t load16_part(const typename T::elem* p, int64_t left) {
+__device__ __forceinline__ u32x4_t load16_part(const typename T::elem* p, int64_t left, const void* end) {
   using E = typename T::elem;
   constexpr int EPC = T::kPerChunk;
-  if (left >= EPC) return load16(p);
-  E e[EPC];
+  u32x4_t v = {0u, 0u, 0u, 0u};
+  if (left <= 0) return v;
+  if (p + EPC <= static_cast<const E*>(end)) {
+    v = load16(p);
+    if (left >= EPC) return v;
 #pragma unroll
-  for (int t = 0; t < EPC; ++t) e[t] = t < left ? p[t] : E(0);
-  u32x4_t v;
-  __builtin_memcpy(&v, e, sizeof(v));
+    for (int w = 0; w < 4; ++w) {   // element w EPC / 4 and, of 16 bits, the one after it
+      const int k = w * EPC / 4;
+      if (k >= left) v[w] = 0u;
+      else if (EPC == 8 && k + 1 >= left) v[w] &= 0xFFFFu;
+    }
+  } else {
+    E e[EPC];
+#pragma unroll
+    for (int t = 0; t < EPC; ++t) e[t] = t < left && p + t < static_cast<const E*>(end) ? p[t] : E(0);
+    __builtin_memcpy(&v, e, sizeof(v));
+  }
   return v;
+}
+
+// Tile of a workgroup: in the XCD raster where the launch fills the chip, and
+// otherwise columns fastest, so that few tiles spread over all XCDs.
+template <class Args>
+__device__ __forceinline__ bool tile_place(const Args& a, int& slot, int& ct) {
+  const int tiles = a.n_slots * a.n_col_tiles;
+  if (tiles >= 256) return raster<8, 4>(blockIdx.x, a.n_slots, a.n_col_tiles, slot, ct);
+  ct = static_cast<int>(blockIdx.x) % a.n_col_tiles;
+  slot = static_cast<int>(blockIdx.x) / a.n_col_tiles;
+  return slot < a.n_slots;
+}
+
+// Workgroups along x that tile_place needs.
+template <class Args>
+unsigned tile_blocks(const Args& a) {
+  const unsigned tiles = static_cast<unsigned>(a.n_slots) * static_cast<unsigned>(a.n_col_tiles);
+  return tiles >= 256 ? (tiles + 255) / 256 * 256 : tiles;   // whole raster rounds
 }
 
 __device__ __forceinline__ int a_slot(int r, int c) { return c ^ ((r >> 1) & 7); }
@@ -253,12 +284,12 @@ void nn_reg_kernel(typename Op::Args a) {
   __shared__ u32x4_t lds[2][A_CHUNKS + B_CHUNKS];
 
   int slot, ct;
-  if constexpr (BM == 32) {   // few rows: columns fastest, over all XCDs
+  if constexpr (BM == 32) {   // few rows: columns fastest, whatever the number of tiles
     ct = blockIdx.x % a.n_col_tiles;
     slot = blockIdx.x / a.n_col_tiles;
     if (slot >= a.n_slots) return;
   } else {
-    if (!raster<8, 4>(blockIdx.x, a.n_slots, a.n_col_tiles, slot, ct)) return;
+    if (!tile_place(a, slot, ct)) return;
   }
   MTile tile;
   if (!Op::template tile<BM>(a, slot, tile)) return;
@@ -280,34 +311,36 @@ void nn_reg_kernel(typename Op::Args a) {
     const int q = tid + s * NT;
     arow[s] = static_cast<const E*>(a.A) + Op::src(a, tile, min(q / kChunks, rows - 1)) * a.R + (q % kChunks) * EPC;
   }
+  // Columns past the matrix are not stored, so a chunk may hold anything there:
+  // it is read whole, from the row's end on into the next row, and a chunk
+  // outside altogether is read from the run's start.
   const E* W = static_cast<const E*>(a.W) + Op::weight(a, tile);
-  ColumnRun run[B_PER_T];
-  bool whole = true;
+  int64_t col[B_PER_T];
 #pragma unroll
   for (int s = 0; s < B_PER_T; ++s) {
     const int q = tid + s * NT;
-    run[s] = Op::template column<BN>(a, ct, (q % kRowChunks) * EPC);
-    whole = whole && run[s].left >= EPC;
+    const ColumnRun run = Op::template column<BN>(a, ct, (q % kRowChunks) * EPC);
+    col[s] = run.left > 0 ? run.first : run.first + run.left - Op::columns(a);
   }
-  whole = __syncthreads_and(whole);
 
   u32x4_t ra[A_PER_T], rb[B_PER_T];
   auto load_stage = [&](int kt) {
     const int64_t k0 = kbeg + static_cast<int64_t>(kt) * BK;
     const E* wk = W + k0 * C;
-    if (whole && k0 + BK <= kend) {
+    // inside the reduction, and a chunk may run past the stage's last row
+    if (k0 + BK <= kend && wk + BK * C + EPC <= static_cast<const E*>(a.W_end)) {
 #pragma unroll
       for (int s = 0; s < A_PER_T; ++s) ra[s] = load16(arow[s] + k0);
 #pragma unroll
-      for (int s = 0; s < B_PER_T; ++s) rb[s] = load16(wk + (tid + s * NT) / kRowChunks * C + run[s].first);
+      for (int s = 0; s < B_PER_T; ++s) rb[s] = load16(wk + (tid + s * NT) / kRowChunks * C + col[s]);
     } else {
 #pragma unroll
       for (int s = 0; s < A_PER_T; ++s)
-        ra[s] = load16_part<T>(arow[s] + k0, kend - k0 - (tid + s * NT) % kChunks * EPC);
+        ra[s] = load16_part<T>(arow[s] + k0, kend - k0 - (tid + s * NT) % kChunks * EPC, a.A_end);
 #pragma unroll
       for (int s = 0; s < B_PER_T; ++s) {
         const int k = (tid + s * NT) / kRowChunks;
-        rb[s] = load16_part<T>(wk + k * C + run[s].first, k0 + k < kend ? run[s].left : 0);
+        rb[s] = load16_part<T>(wk + k * C + col[s], k0 + k < kend ? EPC : 0, a.W_end);
       }
     }
   };
@@ -373,8 +406,7 @@ void nn_reg_kernel(typename Op::Args a) {
 
 template <class T, class Op, int BM, int BN, int WM, int WN, int EU>
 hipError_t launch_nn_reg(const typename Op::Args& a, int ksplit, hipStream_t s) {
-  unsigned tiles = static_cast<unsigned>(a.n_slots) * static_cast<unsigned>(a.n_col_tiles);
-  tiles = (tiles + 8 * 32 - 1) / (8 * 32) * (8 * 32);   // whole raster rounds
+  const unsigned tiles = BM == 32 ? static_cast<unsigned>(a.n_slots) * a.n_col_tiles : tile_blocks(a);
   hipLaunchKernelGGL((nn_reg_kernel<T, Op, BM, BN, WM, WN, EU>), dim3(tiles, static_cast<unsigned>(ksplit)),
                      dim3(WM * WN * 64), 0, s, a);
   return hipGetLastError();

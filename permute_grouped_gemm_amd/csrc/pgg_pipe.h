@@ -175,7 +175,7 @@ void pipe_kernel(typename Op::Args a) {
   __shared__ u32x4_t lds[2 * kStageBytes / 16];
 
   int slot, ct;
-  if (!raster<8, 4>(blockIdx.x, a.n_slots, a.n_col_tiles, slot, ct)) return;
+  if (!tile_place(a, slot, ct)) return;
   MTile tile;
   if (!Op::template tile<256>(a, slot, tile)) return;
   tile.pad = blockIdx.y;
@@ -355,9 +355,7 @@ void pipe_kernel(typename Op::Args a) {
 
 template <class T, class Op, bool NT>
 hipError_t launch_pipe(const typename Op::Args& a, int ksplit, hipStream_t s) {
-  unsigned tiles = static_cast<unsigned>(a.n_slots) * static_cast<unsigned>(a.n_col_tiles);
-  tiles = (tiles + 8 * 32 - 1) / (8 * 32) * (8 * 32);   // whole raster rounds
-  hipLaunchKernelGGL((pipe_kernel<T, Op, NT>), dim3(tiles, static_cast<unsigned>(ksplit)), dim3(512), 0, s, a);
+  hipLaunchKernelGGL((pipe_kernel<T, Op, NT>), dim3(tile_blocks(a), static_cast<unsigned>(ksplit)), dim3(512), 0, s, a);
   return hipGetLastError();
 }
 
