@@ -213,7 +213,7 @@ void glu_grad_reg_kernel(GluGradArgs a) {
     if (kt + 1 < nk) store_stage((kt & 1) ^ 1);
     __syncthreads();
   }
-  store_blocks<T, Op, FM, FN>(a, tile, col0 + wn * WTN, wm * WTM, lane, acc);
+  store_blocks<T, Op, false, FM, FN>(a, tile, col0 + wn * WTN, wm * WTM, lane, acc);
 }
 
 template <class T, int BM, int WM, int EU, int ACT>

@@ -27,7 +27,8 @@
 // With few tokens the projection is bound by reading W once and the launches:
 // the reduction is split over workgroups, the first launch also computes z,
 // token by token, in spare workgroups, and a second one adds the splits in
-// split order and the tokens' z * B_p.
+// split order and the tokens' z * B_p.  Batches too small to fill the chip with
+// tiles split the reduction and finish in the same way.
 #include <algorithm>
 
 #include "pgg_few.h"
@@ -54,7 +55,7 @@ struct LoraArgs {
   int64_t R, C, T, kspan;
   int64_t P;
   int32_t rank;
-  int32_t few;              // few tokens: z comes with the product, lora_finish_kernel adds z * B_p
+  int32_t few;              // few tokens: z comes with the product
   int32_t n_slots, n_col_tiles;
 };
 
@@ -181,56 +182,71 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a) {
 
 // ---------------------------------------------------------------- z, few tokens
 
-// One workgroup per token and four ranks, a wave per rank: lanes run along the
-// reduction, kUnroll loads of each operand at a time, and their sums are added
-// over a fixed tree.  Workgroup `blocks` checks the ids.
-__host__ __device__ __forceinline__ int few_blocks(int64_t tokens, int32_t rank) {
-  return static_cast<int>(tokens) * ((rank + 3) / 4);
+// A workgroup takes a token and 4 RW ranks of it, RW to a wave.  Lanes run along
+// the reduction, 2 or 4 loads of every row at a time, and their sums are added
+// over a fixed tree.  RW = 1 makes the most workgroups, for the fewest tokens;
+// RW = 4 reads x a quarter as often.  Workgroup rank_blocks<RW> checks the ids.
+template <int RW>
+__host__ __device__ __forceinline__ int rank_blocks(int64_t tokens, int32_t rank) {
+  return static_cast<int>(tokens) * ((rank + 4 * RW - 1) / (4 * RW));
 }
 
-template <class T>
-__device__ __forceinline__ void shrink_few(const LoraArgs& a, int block) {
+template <class T, int RW>
+__device__ __forceinline__ void shrink_token(const LoraArgs& a, int block) {
   using E = typename T::elem;
-  constexpr int EPC = T::kPerChunk, kUnroll = 4;
-  if (block == few_blocks(a.T, a.rank)) {
+  constexpr int EPC = T::kPerChunk, kUnroll = RW == 1 ? 4 : 2;
+  if (block == rank_blocks<RW>(a.T, a.rank)) {
     check_ids(a);
     return;
   }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int per = (a.rank + 3) / 4;
+  const int per = (a.rank + 4 * RW - 1) / (4 * RW);
   const int64_t t = block / per;
-  const int r = block % per * 4 + wave;
+  const int r = (block % per * 4 + wave) * RW;
   const int32_t p = adapter_of(a, t);
   if (p < 0 || r >= a.rank) return;
   const E* x = static_cast<const E*>(a.A) + t * a.R;
-  const E* ar = static_cast<const E*>(a.a) + (static_cast<int64_t>(p) * a.rank + r) * a.R;
-  float sum[kUnroll] = {};
+  const E* ar[RW];
+#pragma unroll
+  for (int i = 0; i < RW; ++i)
+    ar[i] = static_cast<const E*>(a.a) + (static_cast<int64_t>(p) * a.rank + min(r + i, a.rank - 1)) * a.R;
+  float sum[RW][kUnroll] = {};
   for (int64_t k = lane * EPC; k < a.R; k += 64 * EPC * kUnroll) {
-    u32x4_t vx[kUnroll], vw[kUnroll];
+    u32x4_t vx[kUnroll], vw[RW][kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int64_t at = k + u * 64 * EPC;
       vx[u] = load16_part<T>(x + at, a.R - at, a.A_end);
-      vw[u] = load16_part<T>(ar + at, a.R - at, a.a_end);
+#pragma unroll
+      for (int i = 0; i < RW; ++i) vw[i][u] = load16_part<T>(ar[i] + at, a.R - at, a.a_end);
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      E ex[EPC], ew[EPC];
+      E ex[EPC];
       __builtin_memcpy(ex, &vx[u], 16);
-      __builtin_memcpy(ew, &vw[u], 16);
 #pragma unroll
-      for (int e = 0; e < EPC; ++e) sum[u] = fmaf(to_float<T>(ex[e]), to_float<T>(ew[e]), sum[u]);
+      for (int i = 0; i < RW; ++i) {
+        E ew[EPC];
+        __builtin_memcpy(ew, &vw[i][u], 16);
+#pragma unroll
+        for (int e = 0; e < EPC; ++e) sum[i][u] = fmaf(to_float<T>(ex[e]), to_float<T>(ew[e]), sum[i][u]);
+      }
     }
   }
-  float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  const float scale = a.scales[p];
 #pragma unroll
-  for (int d = 32; d; d >>= 1) total += __shfl_xor(total, d);
-  if (lane == 0) a.z[t * a.rank + r] = a.scales[p] * total;
+  for (int i = 0; i < RW; ++i) {
+    float total = sum[i][0] + sum[i][1];
+    if constexpr (kUnroll == 4) total += sum[i][2] + sum[i][3];
+#pragma unroll
+    for (int d = 32; d; d >>= 1) total += __shfl_xor(total, d);
+    if (lane == 0 && r + i < a.rank) a.z[t * a.rank + r + i] = scale * total;
+  }
 }
 
-template <class T>
-__global__ __launch_bounds__(256) void lora_shrink_few_kernel(LoraArgs a) {
-  shrink_few<T>(a, blockIdx.x);
+template <class T, int RW>
+__global__ __launch_bounds__(256) void lora_shrink_token_kernel(LoraArgs a) {
+  shrink_token<T, RW>(a, blockIdx.x);
 }
 
 // ---------------------------------------------------------------- the shared product
@@ -282,76 +298,92 @@ struct LoraOp {
   static __device__ __forceinline__ int64_t columns(const Args& a) { return a.C; }
 
   // few tokens: workgroups that compute z, and one that checks the ids
-  static __host__ __device__ __forceinline__ int extra(const Args& a) { return a.few ? few_blocks(a.T, a.rank) + 1 : 0; }
+  static __host__ __device__ __forceinline__ int extra(const Args& a) { return a.few ? rank_blocks<1>(a.T, a.rank) + 1 : 0; }
   template <class T>
   static __device__ __forceinline__ void extra_work(const Args& a, int i) {
-    shrink_few<T>(a, i);
+    shrink_token<T, 1>(a, i);
   }
 
-  // Adds z * B_p of every adapter p found among the wave's rows, adapters in
-  // increasing order, kStep ranks at a time.  Lane l has row l % B of every
-  // block of rows and column l % B of every block of columns, and place l / B
-  // along the ranks.
+  // Adds z * B_p of every adapter p found among the wave's rows, four blocks of
+  // rows and kStep ranks at a time: the rows' z first, then the adapters in
+  // increasing order.  Lane l has row l % B of every block of rows and column
+  // l % B of every block of columns, and place l / B along the ranks.
   template <class T, int B, class Acc, int NI, int NJ, class Column>
   static __device__ __forceinline__ void adjust(const Args& a, const MTile& t, int m0, int lane, Acc (&acc)[NI][NJ],
                                                 Column column) {
     using E = typename T::elem;
-    constexpr int EPC = T::kPerChunk, kStep = 64 / B * EPC, kNone = 0x7FFFFFFF;
-    // with splits, the first one; with few tokens, lora_finish_kernel does it
-    if (a.few || t.pad != 0) return;
-    int32_t id[NI];
+    constexpr int EPC = T::kPerChunk, kStep = 64 / B * EPC, kNone = 0x7FFFFFFF, kGroup = NI < 4 ? NI : 4;
+    if (a.part) return;   // split: lora_finish_kernel does it
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int r = m0 + i * B + lane % B;
-      id[i] = r < t.rows ? adapter_of(a, int64_t(t.row0) + r) : -1;
-    }
-    const float* z0 = a.z + (int64_t(t.row0) + m0 + lane % B) * a.rank;
-    for (int32_t last = -1;;) {
-      int32_t p = kNone;
+    for (int g = 0; g < NI; g += kGroup) {
+      int32_t id[kGroup];
 #pragma unroll
-      for (int i = 0; i < NI; ++i) p = id[i] > last ? min(p, id[i]) : p;
+      for (int i = 0; i < kGroup; ++i) {
+        const int row = m0 + (g + i) * B + lane % B;
+        id[i] = row < t.rows ? adapter_of(a, int64_t(t.row0) + row) : -1;
+      }
+      const float* z0 = a.z + (int64_t(t.row0) + m0 + g * B + lane % B) * a.rank;
+      for (int r0 = 0; r0 < a.rank; r0 += kStep) {
+        const int r = r0 + EPC * (lane / B);
+        u32x4_t zh[kGroup], zl[kGroup];
 #pragma unroll
-      for (int d = B / 2; d; d >>= 1) p = min(p, __shfl_xor(p, d));
-      p = __builtin_amdgcn_readfirstlane(p);
-      if (p == kNone) break;
-      last = p;
-      const E* b = static_cast<const E*>(a.b) + static_cast<int64_t>(p) * a.rank * a.C;
-      for (int r = EPC * (lane / B); r - EPC * (lane / B) < a.rank; r += kStep) {
-        u32x4_t bh[NJ], bl[NJ];
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          const int64_t c = column(j) + lane % B;
+        for (int i = 0; i < kGroup; ++i) {
+          const float* z = z0 + static_cast<int64_t>(i) * B * a.rank + r;
           float v[EPC];
+          if (id[i] >= 0 && r + EPC <= a.rank) {
+            __builtin_memcpy(v, z, sizeof(v));
+          } else {
 #pragma unroll
-          for (int e = 0; e < EPC; ++e)
-            v[e] = c < a.C && r + e < a.rank ? to_float<T>(b[static_cast<int64_t>(r + e) * a.C + c]) : 0.0f;
-          if constexpr (EPC == 8) split_bf16(v, bh[j], bl[j]);
-          else __builtin_memcpy(&bh[j], v, 16);
+            for (int e = 0; e < EPC; ++e) v[e] = id[i] >= 0 && r + e < a.rank ? z[e] : 0.0f;
+          }
+          if constexpr (EPC == 8) split_bf16(v, zh[i], zl[i]);
+          else __builtin_memcpy(&zh[i], v, 16);
         }
+        for (int32_t last = -1;;) {
+          int32_t p = kNone;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          if (!__ballot(id[i] == p)) continue;
-          float v[EPC];
+          for (int i = 0; i < kGroup; ++i) p = id[i] > last ? min(p, id[i]) : p;
 #pragma unroll
-          for (int e = 0; e < EPC; ++e)
-            v[e] = id[i] == p && r + e < a.rank ? z0[static_cast<int64_t>(i) * B * a.rank + r + e] : 0.0f;
-          u32x4_t zh, zl;
-          if constexpr (EPC == 8) split_bf16(v, zh, zl);
-          else __builtin_memcpy(&zh, v, 16);
+          for (int d = B / 2; d; d >>= 1) p = min(p, __shfl_xor(p, d));
+          p = __builtin_amdgcn_readfirstlane(p);
+          if (p == kNone) break;
+          last = p;
+          const E* b = static_cast<const E*>(a.b) + (static_cast<int64_t>(p) * a.rank + r) * a.C;
+          E raw[NJ][EPC];
 #pragma unroll
           for (int j = 0; j < NJ; ++j) {
-            Acc d;
+            const int64_t c = column(j) + lane % B;
 #pragma unroll
-            for (int e = 0; e < B * B / 64; ++e) d[e] = 0.0f;
+            for (int e = 0; e < EPC; ++e) raw[j][e] = c < a.C && r + e < a.rank ? b[e * a.C + c] : E(0);
+          }
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            u32x4_t bh, bl;
             if constexpr (EPC == 8) {
-              mma_block<TBf16>(d, bh[j], zh);
-              mma_block<TBf16>(d, bh[j], zl);
-              if constexpr (__is_same(T, TF16)) mma_block<TBf16>(d, bl[j], zh);
+              float v[EPC];
+#pragma unroll
+              for (int e = 0; e < EPC; ++e) v[e] = to_float<T>(raw[j][e]);
+              split_bf16(v, bh, bl);
             } else {
-              mma<T>(d, bh[j], zh);
+              __builtin_memcpy(&bh, raw[j], 16);
             }
 #pragma unroll
-            for (int e = 0; e < B * B / 64; ++e) acc[i][j][e] = id[i] == p ? acc[i][j][e] + d[e] : acc[i][j][e];
+            for (int i = 0; i < kGroup; ++i) {
+              Acc d;
+#pragma unroll
+              for (int e = 0; e < B * B / 64; ++e) d[e] = 0.0f;
+              if constexpr (EPC == 8) {
+                mma_block<TBf16>(d, bh, zh[i]);
+                mma_block<TBf16>(d, bh, zl[i]);
+                if constexpr (__is_same(T, TF16)) mma_block<TBf16>(d, bl, zh[i]);
+              } else {
+                mma<T>(d, bh, zh[i]);
+              }
+#pragma unroll
+              for (int e = 0; e < B * B / 64; ++e)
+                acc[g + i][j][e] = id[i] == p ? acc[g + i][j][e] + d[e] : acc[g + i][j][e];
+            }
+            __builtin_amdgcn_sched_barrier(0);   // one block of columns at a time: registers
           }
         }
       }
@@ -376,28 +408,51 @@ struct LoraOp {
   }
 };
 
-// Adds the splits' partial products in split order and, with few tokens, the
-// token's z * B_p.
-template <class T>
+// Adds the splits' partial products in split order and the token's z * B_p, for
+// V successive columns per thread (V = 4: C is a multiple of 4).
+template <class T, int V>
 __global__ __launch_bounds__(256) void lora_finish_kernel(LoraArgs a, int32_t ksplit) {
   using E = typename T::elem;
+  struct alignas(V * 4) Floats { float v[V]; };
+  struct alignas(sizeof(E)) Elems { E v[V]; };
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
   const int64_t n = a.T * a.C;
-  for (int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < n; e += step) {
-    const int64_t t = e / a.C, c = e - t * a.C;
-    float sum = a.part[e];
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n / V; i += step) {
+    const int64_t e = i * V, t = e / a.C, c = e - t * a.C;
+    Floats sum = *reinterpret_cast<const Floats*>(a.part + e);
 #pragma unroll 8
-    for (int32_t s = 1; s < ksplit; ++s) sum += a.part[s * n + e];
-    const int32_t p = a.few ? adapter_of(a, t) : -1;
+    for (int32_t s = 1; s < ksplit; ++s) {
+      const Floats f = *reinterpret_cast<const Floats*>(a.part + s * n + e);
+#pragma unroll
+      for (int k = 0; k < V; ++k) sum.v[k] += f.v[k];
+    }
+    const int32_t p = adapter_of(a, t);
     if (p >= 0) {
       const E* b = static_cast<const E*>(a.b) + static_cast<int64_t>(p) * a.rank * a.C + c;
-      float d = 0.0f;
+      Floats d = {};
 #pragma unroll 8
-      for (int32_t r = 0; r < a.rank; ++r) d = fmaf(a.z[t * a.rank + r], to_float<T>(b[r * a.C]), d);
-      sum += d;
+      for (int32_t r = 0; r < a.rank; ++r) {
+        Elems x;
+        __builtin_memcpy(&x, b + r * a.C, sizeof(x));
+        const float z = a.z[t * a.rank + r];
+#pragma unroll
+        for (int k = 0; k < V; ++k) d.v[k] = fmaf(z, to_float<T>(x.v[k]), d.v[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < V; ++k) sum.v[k] += d.v[k];
     }
-    static_cast<E*>(a.y)[e] = from_float<T>(sum);
+    Elems y;
+#pragma unroll
+    for (int k = 0; k < V; ++k) y.v[k] = from_float<T>(sum.v[k]);
+    __builtin_memcpy(static_cast<E*>(a.y) + e, &y, sizeof(y));
   }
+}
+
+template <class T, int V>
+hipError_t launch_finish(const LoraArgs& a, int32_t ksplit, hipStream_t s) {
+  const int64_t blocks = std::min<int64_t>((a.T * a.C / V + 255) / 256, 4096);
+  hipLaunchKernelGGL((lora_finish_kernel<T, V>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a, ksplit);
+  return hipGetLastError();
 }
 
 template <class T, int BM, int BN, int WM, int WN>
@@ -414,18 +469,27 @@ hipError_t launch_shrink(const LoraArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <class T, int RW>
+hipError_t launch_shrink_token(const LoraArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((lora_shrink_token_kernel<T, RW>), dim3(static_cast<unsigned>(rank_blocks<RW>(a.T, a.rank)) + 1),
+                     dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+// Up to this many tokens z is computed token by token: a token reads its whole
+// adapter, but workgroups are many and their reads contiguous.
+constexpr int64_t kTokenByToken = 1024;
+
 template <class T>
 hipError_t launch_typed(const LoraPlan& p, LoraArgs a, bool aligned, hipStream_t s) {
   // the direct-to-LDS kernels' 32-bit byte offsets: into 256 rows of x and 64 rows of W
   const bool direct = T::kPerChunk == 8 && aligned && a.R < (int64_t(1) << 23) && a.C < (int64_t(1) << 25);
   hipError_t e = hipSuccess;
-  if (!a.few) {
+  // z: beside the product, token by token, or in tiles
+  if (a.few && !direct) e = launch_shrink_token<T, 1>(a, s);
+  else if (!a.few && a.T <= kTokenByToken) e = launch_shrink_token<T, 4>(a, s);
+  else if (!a.few)
     e = a.rank <= 16 ? launch_shrink<T, 1>(a, s) : a.rank <= 32 ? launch_shrink<T, 2>(a, s) : launch_shrink<T, 4>(a, s);
-  } else if (!direct) {
-    hipLaunchKernelGGL((lora_shrink_few_kernel<T>), dim3(static_cast<unsigned>(few_blocks(a.T, a.rank) + 1)), dim3(256),
-                       0, s, a);
-    e = hipGetLastError();
-  }
   if (e != hipSuccess) return e;
   if constexpr (T::kPerChunk == 8) {
     a.n_col_tiles = static_cast<int32_t>((a.C + 255) / 256);
@@ -445,9 +509,8 @@ hipError_t launch_typed(const LoraPlan& p, LoraArgs a, bool aligned, hipStream_t
     e = a.few ? launch_reg<T, 32, 128, 1, 4>(a, p, s) : launch_reg<T, 128, 128, 2, 2>(a, p, s);
   }
   if (e != hipSuccess || !a.part) return e;
-  const int64_t blocks = std::min<int64_t>((a.T * a.C + 255) / 256, 4096);
-  hipLaunchKernelGGL((lora_finish_kernel<T>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a, p.ksplit);
-  return hipGetLastError();
+  // four columns per thread once that leaves a thread for every lane of the chip's 1024 SIMDs
+  return a.C % 4 == 0 && a.T * a.C >= 4 * 65536 ? launch_finish<T, 4>(a, p.ksplit, s) : launch_finish<T, 1>(a, p.ksplit, s);
 }
 
 }  // namespace

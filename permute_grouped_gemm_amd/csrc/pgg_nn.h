@@ -20,7 +20,7 @@
 //   Op::kPaired              blocks of 32 columns belong together two by two and
 //                            make 32 output columns
 //   Op::adjust<T, B>(args, t, m0, lane, acc, column)
-//                            may change a wave's accumulators acc[i][j], blocks of
+//                            (tiles of more than 64 rows) may change a wave's accumulators acc[i][j], blocks of
 //                            B x B at tile row m0 + B i and output column column(j)
 //   Op::piece<T>(args, t, m, c, left, v, w)
 //                            takes 8 successive columns from c on of tile row m,
@@ -228,10 +228,10 @@ __device__ __forceinline__ void piece32(const f32x16_t& acc, int q, float (&v)[8
 }
 
 // All of a wave's 32 x 32 blocks: first tile row m0, first output column c0.
-template <class T, class Op, int FM, int FN>
+template <class T, class Op, bool ADJUST, int FM, int FN>
 __device__ __forceinline__ void store_blocks(const typename Op::Args& a, const MTile& t, int64_t c0, int m0, int lane,
                                              f32x16_t (&acc)[FM][FN]) {
-  Op::template adjust<T, 32>(a, t, m0, lane, acc, [&](int j) { return c0 + 32 * j; });
+  if constexpr (ADJUST) Op::template adjust<T, 32>(a, t, m0, lane, acc, [&](int j) { return c0 + 32 * j; });
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int m = m0 + i * 32 + (lane & 31);
@@ -400,7 +400,7 @@ void nn_reg_kernel(typename Op::Args a) {
     if (kt + 1 < nk) store_stage((kt & 1) ^ 1);
     __syncthreads();
   }
-  store_blocks<T, Op, FM, FN>(a, tile, Op::first_column(ct, BN) + wn * (Op::kPaired ? WTN / 2 : WTN), wm * WTM, lane,
+  store_blocks<T, Op, (BM > 32), FM, FN>(a, tile, Op::first_column(ct, BN) + wn * (Op::kPaired ? WTN / 2 : WTN), wm * WTM, lane,
                               acc);
 }
 

@@ -124,8 +124,7 @@ __device__ __forceinline__ u32x4_t read_quarter(const char* base, int s, int n, 
 // of 32 columns, the first from output column c0 on.
 template <class T, class Op, int NI>
 __device__ __forceinline__ void store_runs(const typename Op::Args& a, const MTile& tile, int64_t c0, int m0, int lane,
-                                           f32x4_t (&acc)[NI][4]) {
-  Op::template adjust<T, 16>(a, tile, m0, lane, acc, [&](int j) { return c0 + 128 * (j >> 1) + 16 * (j & 1); });
+                                           const f32x4_t (&acc)[NI][4]) {
   auto row = [&](int i) { return m0 + i * 16 + (lane & 15); };
   auto left = [&](int i, int64_t c) { return row(i) < tile.rows ? Op::columns(a) - c : 0; };
   const int64_t c1 = c0 + run_column(lane);
@@ -350,7 +349,9 @@ void pipe_kernel(typename Op::Args a) {
   if (wave < 4) plain_barrier();
   fetched_barrier<0>();   // the zeros past the reduction have landed before LDS is released
 
-  store_runs<T, Op, 8>(a, tile, Op::first_column(ct, 256) + wn * 32, wm * 128, lane, acc);
+  const int64_t c0 = Op::first_column(ct, 256) + wn * 32;
+  Op::template adjust<T, 16>(a, tile, wm * 128, lane, acc, [&](int j) { return c0 + 128 * (j >> 1) + 16 * (j & 1); });
+  store_runs<T, Op, 8>(a, tile, c0, wm * 128, lane, acc);
 }
 
 template <class T, class Op, bool NT>
