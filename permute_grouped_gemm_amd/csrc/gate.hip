@@ -11,15 +11,17 @@
 //   or with renorm and u = softmax of the chosen logits
 //   grad_l_{e_j} = u_j * (d_j - sum_m d_m u_m), plus grad_lse * p_e everywhere.
 //
-// Both read the logits once and are bound by that read for large batches and
-// by the launch for small ones.  A row belongs to 16, 32 or 64 neighbouring
-// lanes, so one wave takes up to four rows.  The forward keeps the row in
+// Both read the logits once; small batches are bound by the launch, large ones
+// by the picks (forward) and by reading and writing (gradient).  A row belongs
+// to 16, 32 or 64 neighbouring lanes, so one wave takes up to four rows, and a
+// lane holds chunks of four successive experts.  The forward keeps the row in
 // registers, as the logits and as order-preserving integer keys: picking the
 // largest is then an integer maximum over the lanes (row rotations of the
 // data-parallel primitives, no LDS), followed by a minimum over the indices
 // that hold it, and only the owner's entry is struck out before the next
 // pick.  Against one row per wave this shares the fixed cost of a pick, about
-// 40 instructions, between four rows.
+// 40 instructions, between four rows.  In the gradient, lane j of a row takes
+// pick j and hands its d_j to the expert's lane through LDS.
 //
 // Sums and maxima are fp32 and are added in a fixed order.
 #include "pgg_device.h"
@@ -110,6 +112,20 @@ __device__ __forceinline__ float row_max_float(float v) {
 // The largest logit, as softmax subtracts it: 0 for a row of -inf.
 __device__ __forceinline__ float pivot(float m) { return m == kNegInf ? 0.0f : m; }
 
+// Four successive entries from e on; past E: -inf.
+template <class T>
+__device__ __forceinline__ void load4(const typename T::elem* row, int e, int E, float (&v)[4]) {
+  typename T::elem x[4];
+  if (e + 4 <= E) {
+    __builtin_memcpy(x, row + e, sizeof(x));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = to_float<T>(x[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = e + i < E ? to_float<T>(row[e + i]) : kNegInf;
+  }
+}
+
 // The k picks are kept LPR to a register: pick j by lane j % LPR.
 template <int LPR>
 constexpr int kPickRegs = (PGG_GATE_MAX_TOPK + LPR - 1) / LPR;
@@ -144,7 +160,8 @@ __device__ __forceinline__ void finish_row(const GateArgs& a, const typename T::
   }
 }
 
-// E <= LPR * EPL: the row lives in registers, entry i of lane c is expert i * LPR + c.
+// E <= LPR * EPL: the row lives in registers, entry i of lane c is expert
+// 4 (i / 4 * LPR + c) + i % 4.
 template <class T, int LPR, int EPL>
 __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
   using E = typename T::elem;
@@ -154,17 +171,15 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
   const bool live = t < a.T;
   const int64_t tr = live ? t : a.T - 1;
   const E* __restrict__ row = static_cast<const E*>(a.logits) + tr * a.E;
+  auto expert = [&](int i) { return 4 * (i / 4 * LPR + lane) + i % 4; };
   float l[EPL];
   uint32_t key[EPL];
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = i * LPR + lane;
-    l[i] = e < a.E ? to_float<T>(row[e]) : kNegInf;
-  }
+  for (int i = 0; i < EPL; i += 4) load4<T>(row, expert(i), a.E, *reinterpret_cast<float(*)[4]>(&l[i]));
   float m = l[0];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const int e = i * LPR + lane;
+    const int e = expert(i);
     const float b = a.bias && e < a.E ? a.bias[e] : 0.0f;
     key[i] = e < a.E ? order_key(l[i] + b) : 0u;
     m = (l[i] != l[i] || l[i] > m) ? l[i] : m;
@@ -181,18 +196,18 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
     sel[s] = 0;
     for (int j = 0; j < min(LPR, a.k - s * LPR); ++j) {
       uint32_t best = key[0];
-      uint32_t at = lane;
+      uint32_t at = expert(0);
 #pragma unroll
       for (int i = 1; i < EPL; ++i)
         if (key[i] > best) {
           best = key[i];
-          at = i * LPR + lane;
+          at = expert(i);
         }
       const uint32_t top_key = row_max<LPR>(best);
       const uint32_t e = row_min<LPR>(best == top_key ? at : 0xFFFFFFFFu);
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
-        if (e == static_cast<uint32_t>(i * LPR + lane)) key[i] = 0u;
+        if (e == static_cast<uint32_t>(expert(i))) key[i] = 0u;
       if (lane == j) sel[s] = static_cast<int32_t>(e);
     }
   }
@@ -247,89 +262,102 @@ __global__ __launch_bounds__(kGateThreads) void gate_long_kernel(GateArgs a) {
   finish_row<T, LPR>(a, row, t, lane, sel, top, total);
 }
 
-// LPR lanes per row, kPer entries per lane and step.  Every lane of a row walks
-// the row's k picks by itself (the loads hit one address, so L1 serves them),
-// which needs no exchange between lanes.
-template <class T, int LPR>
-__global__ __launch_bounds__(kGateThreads) void gate_grad_kernel(GateGradArgs a) {
+// LPR lanes per row, rows of one wave only; E floats of LDS per row, which hold
+// d_j at the picks and kUnpicked elsewhere.
+constexpr uint32_t kUnpicked = 0x7FC0DEADu;   // a NaN that no product makes
+
+template <class T, int LPR, int THREADS>
+__global__ __launch_bounds__(THREADS) void gate_grad_kernel(GateGradArgs a) {
   using E = typename T::elem;
-  constexpr int kPer = 4;
+  extern __shared__ uint32_t picked_rows[];
   const int lane = threadIdx.x % LPR;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kGateThreads / LPR) + threadIdx.x / LPR;
-  if (t >= a.T) return;
-  const E* __restrict__ row = static_cast<const E*>(a.logits) + t * a.E;
-  const int64_t* __restrict__ ids = a.ids + t * a.k;
-  const float* __restrict__ gp = a.grad_probs + t * a.k;
-  const float lse = a.lse[t];
-  const float glse = a.grad_lse ? a.grad_lse[t] : 0.0f;
-  // an id outside the experts selects nothing
-  auto chosen = [&](int j) { return static_cast<uint64_t>(ids[j]) < static_cast<uint64_t>(a.E); };
-  auto logit = [&](int j) { return chosen(j) ? to_float<T>(row[ids[j]]) : kNegInf; };
-  // p = exp(l - pivot) * inv, the weights the picks come from
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (THREADS / LPR) + threadIdx.x / LPR;
+  const bool live = t < a.T;
+  const int64_t tr = live ? t : a.T - 1;   // whole waves stay together
+  const E* __restrict__ row = static_cast<const E*>(a.logits) + tr * a.E;
+  uint32_t* picked = picked_rows + threadIdx.x / LPR * a.E;
+  const float lse = a.lse[tr];
+  const float glse = a.grad_lse ? a.grad_lse[tr] : 0.0f;
+  // this lane's picks; an id outside the experts selects nothing
+  int32_t id[kPickRegs<LPR>];
+  float d[kPickRegs<LPR>], l[kPickRegs<LPR>];
+#pragma unroll
+  for (int s = 0; s < kPickRegs<LPR>; ++s) {
+    const int j = s * LPR + lane;
+    const int64_t e = j < a.k ? a.ids[tr * a.k + j] : -1;
+    id[s] = static_cast<uint64_t>(e) < static_cast<uint64_t>(a.E) ? static_cast<int32_t>(e) : -1;
+    d[s] = id[s] >= 0 ? a.grad_probs[tr * a.k + j] * a.scale : 0.0f;
+    l[s] = id[s] >= 0 ? to_float<T>(row[id[s]]) : kNegInf;
+  }
+  for (int e = lane; e < a.E; e += LPR) picked[e] = kUnpicked;
+  // p = exp(l - top) * inv, the weights the picks come from
   float top = lse, inv = 1.0f;
   if (a.renorm) {
-    float m = kNegInf;
-    for (int j = 0; j < a.k; ++j) {
-      const float v = logit(j);
-      m = (v != v || v > m) ? v : m;
-    }
-    top = pivot(m);
-    float z = 0.0f;
-    for (int j = 0; j < a.k; ++j) z += expf(logit(j) - top);
-    inv = z > 0.0f ? 1.0f / z : 1.0f;
+    float m = l[0];
+#pragma unroll
+    for (int s = 1; s < kPickRegs<LPR>; ++s) m = (l[s] != l[s] || l[s] > m) ? l[s] : m;
+    top = row_max_float<LPR>(m);
   }
   top = pivot(top);
+  float p[kPickRegs<LPR>], sum = 0.0f;
+#pragma unroll
+  for (int s = 0; s < kPickRegs<LPR>; ++s) {
+    p[s] = expf(l[s] - top);
+    sum += p[s];
+  }
+  if (a.renorm) {
+    sum = row_sum<LPR>(sum);
+    inv = sum > 0.0f ? 1.0f / sum : 1.0f;
+  }
   float mean = 0.0f;   // sum_j d_j p_j
-  for (int j = 0; j < a.k; ++j)
-    if (chosen(j)) mean += gp[j] * a.scale * (expf(logit(j) - top) * inv);
-  for (int e0 = 0; e0 < a.E; e0 += LPR * kPer) {
-    float d[kPer];
-    bool hit[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      d[i] = 0.0f;
-      hit[i] = false;
+  for (int s = 0; s < kPickRegs<LPR>; ++s)
+    if (id[s] >= 0) mean += d[s] * (p[s] * inv);
+  mean = row_sum<LPR>(mean);
+  // LDS operations of a wave are done in order; only the compiler has to keep it
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+  for (int s = 0; s < kPickRegs<LPR>; ++s)
+    if (id[s] >= 0) picked[id[s]] = __builtin_bit_cast(uint32_t, d[s]);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  if (!live) return;
+  E* out = static_cast<E*>(a.grad_logits) + t * a.E;
+  for (int e0 = 4 * lane; e0 < a.E; e0 += 4 * LPR) {
+    float x[4];
+    load4<T>(row, e0, a.E, x);
+    E g[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = e0 + i < a.E ? picked[e0 + i] : kUnpicked;
+      const bool hit = u != kUnpicked;
+      const float di = hit ? __builtin_bit_cast(float, u) : 0.0f;
+      const float q = lse == kNegInf ? 0.0f : expf(x[i] - lse);
+      float v;
+      if (a.renorm) v = hit ? expf(x[i] - top) * inv * (di - mean) : 0.0f;
+      else v = q * (di - mean);
+      if (a.grad_lse) v += glse * q;
+      g[i] = from_float<T>(v);
     }
-    for (int j = 0; j < a.k; ++j) {
-      const int64_t id = ids[j];
-      const float dj = gp[j] * a.scale;
+    if (e0 + 4 <= a.E) {
+      __builtin_memcpy(out + e0, g, sizeof(g));
+    } else {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (id == e0 + i * LPR + lane) {
-          d[i] += dj;
-          hit[i] = true;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = e0 + i * LPR + lane;
-      if (e < a.E) {
-        const float l = to_float<T>(row[e]);
-        const float p = lse == kNegInf ? 0.0f : expf(l - lse);
-        float g;
-        if (a.renorm)
-          g = hit[i] ? expf(l - top) * inv * (d[i] - mean) : 0.0f;
-        else
-          g = p * (d[i] - mean);
-        if (a.grad_lse) g += glse * p;
-        static_cast<E*>(a.grad_logits)[t * a.E + e] = from_float<T>(g);
-      }
+      for (int i = 0; i < 4; ++i)
+        if (e0 + i < a.E) out[e0 + i] = g[i];
     }
   }
 }
 
-template <int LPR>
+template <int LPR, int THREADS = kGateThreads>
 dim3 rows_grid(int64_t T) {
-  constexpr int64_t per = kGateThreads / LPR;
+  constexpr int64_t per = THREADS / LPR;
   return dim3(static_cast<unsigned>((T + per - 1) / per));
 }
 
 template <class T>
 hipError_t launch_gate_typed(const GateArgs& a, hipStream_t s) {
   const dim3 b(kGateThreads);
-  if (a.E <= 16) hipLaunchKernelGGL((gate_kernel<T, 16, 1>), rows_grid<16>(a.T), b, 0, s, a);
-  else if (a.E <= 32) hipLaunchKernelGGL((gate_kernel<T, 16, 2>), rows_grid<16>(a.T), b, 0, s, a);
-  else if (a.E <= 64) hipLaunchKernelGGL((gate_kernel<T, 16, 4>), rows_grid<16>(a.T), b, 0, s, a);
+  if (a.E <= 64) hipLaunchKernelGGL((gate_kernel<T, 16, 4>), rows_grid<16>(a.T), b, 0, s, a);
   else if (a.E <= 128) hipLaunchKernelGGL((gate_kernel<T, 16, 8>), rows_grid<16>(a.T), b, 0, s, a);
   else if (a.E <= 256) hipLaunchKernelGGL((gate_kernel<T, 16, 16>), rows_grid<16>(a.T), b, 0, s, a);
   else if (a.E <= 512) hipLaunchKernelGGL((gate_kernel<T, 32, 16>), rows_grid<32>(a.T), b, 0, s, a);
@@ -338,13 +366,20 @@ hipError_t launch_gate_typed(const GateArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <class T, int LPR, int THREADS>
+hipError_t launch_gate_grad_rows(const GateGradArgs& a, hipStream_t s) {
+  const size_t lds = sizeof(uint32_t) * (THREADS / LPR) * static_cast<size_t>(a.E);
+  hipLaunchKernelGGL((gate_grad_kernel<T, LPR, THREADS>), (rows_grid<LPR, THREADS>(a.T)), dim3(THREADS), lds, s, a);
+  return hipGetLastError();
+}
+
+// 16 KiB of LDS at most per workgroup, but one row always fits (32 KiB)
 template <class T>
 hipError_t launch_gate_grad_typed(const GateGradArgs& a, hipStream_t s) {
-  const dim3 b(kGateThreads);
-  if (a.E <= 64) hipLaunchKernelGGL((gate_grad_kernel<T, 16>), rows_grid<16>(a.T), b, 0, s, a);
-  else if (a.E <= 128) hipLaunchKernelGGL((gate_grad_kernel<T, 32>), rows_grid<32>(a.T), b, 0, s, a);
-  else hipLaunchKernelGGL((gate_grad_kernel<T, 64>), rows_grid<64>(a.T), b, 0, s, a);
-  return hipGetLastError();
+  if (a.E <= 64) return launch_gate_grad_rows<T, 16, 256>(a, s);
+  if (a.E <= 128) return launch_gate_grad_rows<T, 32, 256>(a, s);
+  if (a.E <= 1024) return launch_gate_grad_rows<T, 64, 256>(a, s);
+  return launch_gate_grad_rows<T, 64, 64>(a, s);
 }
 
 }  // namespace

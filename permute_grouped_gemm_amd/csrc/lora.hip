@@ -66,16 +66,23 @@ __device__ __forceinline__ int32_t adapter_of(const LoraArgs& a, int64_t t) {
   return p >= 0 && p < a.P ? static_cast<int32_t>(p) : -1;
 }
 
-// One workgroup: the header, with the smallest token whose id is past the adapters.
+// One workgroup: the header, with the smallest token whose id is past the
+// adapters.  The loads are independent, eight at a time.
 __device__ void check_ids(const LoraArgs& a) {
   __shared__ unsigned long long bad;
   if (threadIdx.x == 0) bad = ~0ull;
   __syncthreads();
-  for (int64_t t = threadIdx.x; t < a.T; t += blockDim.x)
-    if (a.ids[t] >= a.P) {
-      atomicMin(&bad, static_cast<unsigned long long>(t));
-      break;
-    }
+  int64_t mine = a.T;
+  const int64_t step = static_cast<int64_t>(blockDim.x) * 8;
+  for (int64_t t = threadIdx.x; t < a.T; t += step) {
+    int64_t id[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) id[u] = a.ids[min(t + u * static_cast<int64_t>(blockDim.x), a.T - 1)];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (id[u] >= a.P) mine = min(mine, min(t + u * static_cast<int64_t>(blockDim.x), a.T - 1));
+  }
+  if (mine < a.T) atomicMin(&bad, static_cast<unsigned long long>(mine));
   __syncthreads();
   if (threadIdx.x == 0) {
     reset_header(a.hdr);
@@ -90,8 +97,9 @@ __device__ void check_ids(const LoraArgs& a) {
 // reading x once: a load takes 64 bytes of 16 rows, and eight waves with 4 x
 // (2 + NB) loads each keep them coming.  Workgroups go to the 8 XCDs in turn, and
 // each XCD takes a run of tokens, so that the adapter of a request is fetched by
-// one L2 and not by eight (78 -> 60 us at 13824 tokens of 7168, 60 adapters of
-// rank 16 in runs of 300).  The last workgroup along x checks the ids.
+// one L2 and not by eight (2.2 -> 1.8 million lines from memory at 13824 tokens
+// of 7168, 60 adapters of rank 16 in runs of 300: 69 us, 198 MB of x alone take
+// about 40).  The last workgroup along x checks the ids.
 template <class T, int NB>
 __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a) {
   using E = typename T::elem;
@@ -110,11 +118,9 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a) {
   const int r0 = blockIdx.y * 16 * NB;
   const int64_t R = a.R;
   const int32_t id = (lane & 31) < rows ? adapter_of(a, t0 + (lane & 31)) : -1;
-  // this wave's part of the reduction, in whole steps
-  const int64_t steps = (R + kStep - 1) / kStep;
-  const int64_t per = (steps + kWaves - 1) / kWaves;
-  const int64_t s0 = min<int64_t>(steps, wave * per), s1 = min<int64_t>(steps, s0 + per);
-  const int64_t s_whole = min<int64_t>(s1, R / kStep);
+  // the waves take kUnroll steps of the reduction in turn: together they read
+  // 8 x 256 successive bytes of every row
+  const int64_t steps = (R + kStep - 1) / kStep, whole = R / kStep;
   const E* x[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) x[i] = static_cast<const E*>(a.A) + (t0 + min(16 * i + lr, rows - 1)) * R + lg * EPC;
@@ -133,15 +139,25 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a) {
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int b = 0; b < NB; ++b) acc[i][b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    int64_t s = s0;
-    for (; s + kUnroll <= s_whole; s += kUnroll) {
+    for (int64_t s = wave * kUnroll; s < steps; s += kWaves * kUnroll) {
       u32x4_t fx[kUnroll][2], fw[kUnroll][NB];
+      if (s + kUnroll <= whole) {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
+        for (int u = 0; u < kUnroll; ++u) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) fx[u][i] = load16(x[i] + (s + u) * kStep);
+          for (int i = 0; i < 2; ++i) fx[u][i] = load16(x[i] + (s + u) * kStep);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) fw[u][b] = load16(ar[b] + (s + u) * kStep);
+          for (int b = 0; b < NB; ++b) fw[u][b] = load16(ar[b] + (s + u) * kStep);
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          const int64_t left = R - (s + u) * kStep - lg * EPC;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) fx[u][i] = load16_part<T>(x[i] + (s + u) * kStep, left, a.A_end);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) fw[u][b] = load16_part<T>(ar[b] + (s + u) * kStep, left, a.a_end);
+        }
       }
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u)
@@ -149,15 +165,6 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a) {
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int b = 0; b < NB; ++b) mma_block<T>(acc[i][b], fw[u][b], fx[u][i]);
-    }
-    for (; s < s1; ++s) {
-      const int64_t left = R - s * kStep - lg * EPC;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-          mma_block<T>(acc[i][b], load16_part<T>(ar[b] + s * kStep, left, a.a_end),
-                       load16_part<T>(x[i] + s * kStep, left, a.A_end));
     }
     // lane: token 16 i + lr, ranks 16 b + 4 lg ..
 #pragma unroll
