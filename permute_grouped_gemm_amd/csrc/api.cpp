@@ -581,9 +581,6 @@ pgg_status pgg_moe_glu(const pgg_moe_glu_desc* desc, const void* x, const void* 
   if (!is_aligned(workspace, kWorkspaceAlign) || !is_aligned(expanded_row_idx, 8) || !is_aligned(group_list, 8) ||
       !is_aligned(x, es) || !is_aligned(weight, es) || !is_aligned(h, es) || !is_aligned(gate_up, es))
     return PGG_ERR_MISALIGNED;
-  // rows of x, and the gate and the up half of every weight row
-  const bool aligned = is_aligned(x, 16) && is_aligned(weight, 16) && (size_t(p.N) * es) % 16 == 0 &&
-                       (size_t(p.K / 2) * es) % 16 == 0;
   const WsView w = ws_view(p, workspace);
   hipError_t e;
   if (p.fused_prep) {
@@ -601,7 +598,7 @@ pgg_status pgg_moe_glu(const pgg_moe_glu_desc* desc, const void* x, const void* 
   }
   if (e == hipSuccess) {
     TimedLaunch t("glu", stream);
-    e = launch_glu(p, desc->act, x, weight, h, gate_up, aligned, w, stream);
+    e = launch_glu(p, desc->act, x, weight, h, gate_up, workspace, stream);
   }
   return e == hipSuccess ? PGG_OK : PGG_ERR_HIP;
 }
@@ -627,7 +624,6 @@ pgg_status pgg_moe_glu_grad(const pgg_moe_glu_grad_desc* desc, const void* grad_
   if (!is_aligned(workspace, kWorkspaceAlign) || !is_aligned(group_list, 8) || !is_aligned(grad_y, es) ||
       !is_aligned(weight, es) || !is_aligned(gate_up, es) || !is_aligned(grad_gate_up, es) || !is_aligned(h, es))
     return PGG_ERR_MISALIGNED;
-  const bool aligned = is_aligned(grad_y, 16) && is_aligned(weight, 16) && (size_t(p.N) * es) % 16 == 0;
   const WsView w = ws_view(p, workspace);
   hipError_t e;
   {
@@ -636,7 +632,7 @@ pgg_status pgg_moe_glu_grad(const pgg_moe_glu_grad_desc* desc, const void* grad_
   }
   if (e == hipSuccess) {
     TimedLaunch t("glu_grad", stream);
-    e = launch_glu_grad(p, desc->act, grad_y, weight, gate_up, grad_gate_up, h, aligned, w, stream);
+    e = launch_glu_grad(p, desc->act, grad_y, weight, gate_up, grad_gate_up, h, workspace, stream);
   }
   return e == hipSuccess ? PGG_OK : PGG_ERR_HIP;
 }
@@ -662,10 +658,8 @@ pgg_status pgg_lora_fwd(const pgg_lora_desc* desc, const void* x, const void* we
   if (!is_aligned(workspace, kWorkspaceAlign) || !is_aligned(adapter_ids, 8) || !is_aligned(scales, 4) ||
       !is_aligned(x, es) || !is_aligned(weight, es) || !is_aligned(a, es) || !is_aligned(b, es) || !is_aligned(y, es))
     return PGG_ERR_MISALIGNED;
-  const bool aligned = is_aligned(x, 16) && is_aligned(weight, 16) && (size_t(p.K) * es) % 16 == 0 &&
-                       (size_t(p.N) * es) % 16 == 0;
   TimedLaunch t("lora", stream);
-  return launch_lora(p, x, weight, a, b, adapter_ids, scales, y, workspace, aligned, stream) == hipSuccess
+  return launch_lora(p, x, weight, a, b, adapter_ids, scales, y, workspace, stream) == hipSuccess
              ? PGG_OK : PGG_ERR_HIP;
 }
 

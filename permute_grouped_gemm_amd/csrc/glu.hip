@@ -16,7 +16,9 @@
 // pgg_nn.h; with few rows per expert the reduction is split over workgroups so
 // that enough of them stream weights, the fp32 partial products of the splits
 // go to the workspace, and a second kernel adds them in split order and applies
-// the activation.
+// the activation.  Rows of x or W that are not 16-byte aligned are copied to
+// padded rows first where the product is large enough to pay for it (the plan
+// says so); otherwise the tiles that load through registers take them.
 #include <algorithm>
 
 #include "pgg_act.h"
@@ -38,6 +40,7 @@ struct GluArgs {
   void* gate_up;            // [M, C] or NULL
   float* part;              // split partials [ksplit, M, C], or NULL
   int64_t R, C, F, M, kspan;
+  int64_t lda, ldw, Fw;     // row strides of A and W; columns from gate to up in a W row
   uint32_t topk;
   int32_t bm;               // rows of a table entry
   int32_t n_slots, n_col_tiles;
@@ -65,7 +68,7 @@ struct GluOp {
   }
 
   static __device__ __forceinline__ int64_t weight(const Args& a, const MTile& t) {
-    return static_cast<int64_t>(t.g) * a.R * a.C;
+    return t.g * a.R * a.ldw;
   }
 
   static constexpr bool kPaired = true;
@@ -80,7 +83,7 @@ struct GluOp {
 
   // run j (0: gate, 1: up), column n; past the end: a valid one, not stored
   static __device__ __forceinline__ int64_t half_column(const Args& a, int ct, int j, int n) {
-    return j * a.F + min<int64_t>(first_column(ct, 256) + n, a.F - 8);
+    return j * a.Fw + min<int64_t>(first_column(ct, 256) + n, a.Fw - 8);
   }
 
   static __device__ __forceinline__ int64_t columns(const Args& a) { return a.F; }
@@ -144,16 +147,36 @@ hipError_t launch_reg(const Plan& p, GluArgs a, hipStream_t s) {
   return launch_nn_reg<T, GluOp<ACT>, BM, BN, WM, WN, EU>(a, p.ksplit, s);
 }
 
+// What the direct-to-LDS kernels need: 16-byte rows, and 32-bit byte offsets
+// into all of x and into 64 rows of W.
+bool direct(const Plan& p, const GluArgs& a) {
+  auto fits = [](const void* ptr, int64_t ld) { return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && ld % 8 == 0; };
+  return fits(a.A, a.lda) && fits(a.W, a.ldw) && a.Fw % 8 == 0 && p.batch * a.lda < (int64_t(1) << 31) &&
+         a.ldw < (int64_t(1) << 25);
+}
+
 template <class T, int ACT>
-hipError_t launch_16(const Plan& p, GluArgs a, bool aligned, hipStream_t s) {
-  // the direct-to-LDS kernels' 32-bit byte offsets: into all of x, and into 64 rows of W
-  aligned = aligned && p.batch * a.R < (int64_t(1) << 31) && a.C < (int64_t(1) << 25);
+hipError_t launch_16(const Plan& p, GluArgs a, void* padded_x, void* padded_w, hipStream_t s) {
   a.n_slots = p.max_tiles;
   a.n_col_tiles = static_cast<int32_t>((a.F + 127) / 128);
   if (p.regime == kStream)
-    return aligned ? launch_few<T, GluOp<ACT>, 32>(a, 0, p.ksplit, s) : launch_reg<T, 32, 256, 1, 4, 2, ACT>(p, a, s);
-  if (!aligned) return launch_reg<T, 128, 128, 2, 2, 2, ACT>(p, a, s);
-  return launch_pipe<T, GluOp<ACT>, false>(a, 1, s);
+    return direct(p, a) ? launch_few<T, GluOp<ACT>, 32>(a, 0, p.ksplit, s)
+                        : launch_reg<T, 32, 256, 1, 4, 2, ACT>(p, a, s);
+  GluArgs b = a;   // with the operands that the plan lays out anew
+  if (p.pad_a) {
+    b.A = padded_x;
+    b.lda = p.lda;
+  }
+  if (p.pad_w) {
+    b.W = padded_w;
+    b.ldw = p.ldw;
+    b.Fw = p.ldw / 2;
+  }
+  if (!direct(p, b)) return launch_reg<T, 128, 128, 2, 2, 2, ACT>(p, a, s);
+  hipError_t e = hipSuccess;
+  if (p.pad_a) e = launch_pad_rows(a.A, padded_x, p.batch, a.R, b.lda, s);
+  if (e == hipSuccess && p.pad_w) e = launch_pad_rows(a.W, padded_w, p.G * a.R * 2, a.F, b.Fw, s);
+  return e == hipSuccess ? launch_pipe<T, GluOp<ACT>, false>(b, 1, s) : e;
 }
 
 template <class T, int ACT>
@@ -164,13 +187,13 @@ hipError_t finish(const GluArgs& a, int32_t ksplit, hipStream_t s) {
 }
 
 template <int ACT>
-hipError_t launch_act(const Plan& p, const GluArgs& a, bool aligned, hipStream_t s) {
+hipError_t launch_act(const Plan& p, const GluArgs& a, void* px, void* pw, hipStream_t s) {
   hipError_t e;
   if (p.dtype == PGG_F32)
     e = p.regime == kStream ? launch_reg<TF32, 32, 256, 1, 4, 2, ACT>(p, a, s)
                             : launch_reg<TF32, 128, 128, 2, 2, 2, ACT>(p, a, s);
   else
-    e = p.dtype == PGG_BF16 ? launch_16<TBf16, ACT>(p, a, aligned, s) : launch_16<TF16, ACT>(p, a, aligned, s);
+    e = p.dtype == PGG_BF16 ? launch_16<TBf16, ACT>(p, a, px, pw, s) : launch_16<TF16, ACT>(p, a, px, pw, s);
   if (e != hipSuccess || p.ksplit == 1) return e;
   if (p.dtype == PGG_F32) return finish<TF32, ACT>(a, p.ksplit, s);
   return p.dtype == PGG_BF16 ? finish<TBf16, ACT>(a, p.ksplit, s) : finish<TF16, ACT>(a, p.ksplit, s);
@@ -179,7 +202,8 @@ hipError_t launch_act(const Plan& p, const GluArgs& a, bool aligned, hipStream_t
 }  // namespace
 
 hipError_t launch_glu(const Plan& p, int32_t act, const void* x, const void* weight, void* h, void* gate_up,
-                      bool aligned, const WsView& w, hipStream_t s) {
+                      void* ws, hipStream_t s) {
+  const WsView w = ws_view(p, ws);
   GluArgs a;
   a.A = x;
   a.W = weight;
@@ -194,13 +218,17 @@ hipError_t launch_glu(const Plan& p, int32_t act, const void* x, const void* wei
   a.W_end = static_cast<const char*>(weight) + es * p.G * p.N * p.K;
   a.R = p.N;          // the plan keeps the reduction in N and the columns in K
   a.C = p.K;
-  a.F = p.K / 2;
+  a.F = a.Fw = p.K / 2;
+  a.lda = p.N;
+  a.ldw = p.K;
   a.M = p.M;
   a.kspan = p.kspan;
   a.topk = static_cast<uint32_t>(p.topk);
   a.bm = p.bm;
-  return act == PGG_ACT_SILU ? launch_act<PGG_ACT_SILU>(p, a, aligned, s)
-                             : launch_act<PGG_ACT_GELU_TANH>(p, a, aligned, s);
+  void* px = static_cast<char*>(ws) + p.off_pad_a;
+  void* pw = static_cast<char*>(ws) + p.off_pad_w;
+  return act == PGG_ACT_SILU ? launch_act<PGG_ACT_SILU>(p, a, px, pw, s)
+                             : launch_act<PGG_ACT_GELU_TANH>(p, a, px, pw, s);
 }
 
 }  // namespace pgg

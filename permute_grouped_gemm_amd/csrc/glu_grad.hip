@@ -30,6 +30,7 @@ struct GluGradArgs {
   void* grad;               // [M, C]
   void* h;                  // [M, F] or NULL
   int64_t R, C, F, kspan;
+  int64_t lda, ldw;         // row strides of A and W
   int32_t bm;               // rows of a table entry
   int32_t n_slots, n_col_tiles;
 };
@@ -54,7 +55,7 @@ struct GluGradOp {
 
   static __device__ __forceinline__ int64_t src_base(const Args&, const MTile& t) { return t.row0; }
   static __device__ __forceinline__ int64_t src(const Args&, const MTile& t, int r) { return int64_t(t.row0) + r; }
-  static __device__ __forceinline__ int64_t weight(const Args& a, const MTile& t) { return t.g * a.F * a.R; }
+  static __device__ __forceinline__ int64_t weight(const Args& a, const MTile& t) { return t.g * a.F * a.ldw; }
   static __device__ __forceinline__ int64_t first_column(int ct, int bn) { return static_cast<int64_t>(ct) * bn; }
 
   static __device__ __forceinline__ int64_t columns(const Args& a) { return a.F; }
@@ -132,13 +133,13 @@ void glu_grad_reg_kernel(GluGradArgs a) {
 #pragma unroll
   for (int s = 0; s < A_PER_T; ++s) {
     const int q = tid + s * NT;
-    arow[s] = static_cast<const E*>(a.A) + Op::src(a, tile, min(q / kChunks, tile.rows - 1)) * D + (q % kChunks) * EPC;
+    arow[s] = static_cast<const E*>(a.A) + Op::src(a, tile, min(q / kChunks, tile.rows - 1)) * a.lda + (q % kChunks) * EPC;
   }
 #pragma unroll
   for (int s = 0; s < B_PER_T; ++s) {
     const int q = tid + s * NT;
     const int64_t f = min<int64_t>(col0 + q / kChunks, a.F - 1);
-    brow[s] = static_cast<const E*>(a.W) + Op::weight(a, tile) + f * D + (q % kChunks) * EPC;
+    brow[s] = static_cast<const E*>(a.W) + Op::weight(a, tile) + f * a.ldw + (q % kChunks) * EPC;
   }
 
   u32x4_t ra[A_PER_T], rb[B_PER_T];
@@ -225,30 +226,48 @@ hipError_t launch_reg(const Plan& p, GluGradArgs a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// What the direct-to-LDS kernel needs: 16-byte rows, and 32-bit byte offsets
+// into 256 rows of either operand.
+bool direct(const GluGradArgs& a) {
+  auto fits = [](const void* ptr, int64_t ld) { return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && ld % 8 == 0; };
+  return fits(a.A, a.lda) && fits(a.W, a.ldw) && a.lda < (int64_t(1) << 23);
+}
+
 template <class T, int ACT>
-hipError_t launch_typed(const Plan& p, GluGradArgs a, bool aligned, hipStream_t s) {
+hipError_t launch_typed(const Plan& p, GluGradArgs a, void* padded_a, void* padded_w, hipStream_t s) {
   if (p.bm == 32) return launch_reg<T, 32, 1, 4, ACT>(p, a, s);
   if constexpr (T::kPerChunk == 8) {
-    // the pipeline's 32-bit byte offsets: into 256 rows of either operand
-    if (aligned && p.bm == 256 && a.R < (int64_t(1) << 23)) {
-      a.n_slots = p.max_tiles;
-      a.n_col_tiles = static_cast<int32_t>((a.F + 255) / 256);
-      return launch_pipe<T, GluGradOp<ACT>, true>(a, 1, s);
+    GluGradArgs b = a;   // with the operands that the plan lays out anew
+    if (p.pad_a) {
+      b.A = padded_a;
+      b.W = padded_w;
+      b.lda = b.ldw = p.lda;
+    }
+    if (direct(b)) {
+      hipError_t e = hipSuccess;
+      if (p.pad_a) {
+        e = launch_pad_rows(a.A, padded_a, p.M, a.R, b.lda, s);
+        if (e == hipSuccess) e = launch_pad_rows(a.W, padded_w, p.G * a.F, a.R, b.ldw, s);
+      }
+      b.n_slots = p.max_tiles;
+      b.n_col_tiles = static_cast<int32_t>((a.F + 255) / 256);
+      return e == hipSuccess ? launch_pipe<T, GluGradOp<ACT>, true>(b, 1, s) : e;
     }
   }
   return launch_reg<T, 128, 2, 2, ACT>(p, a, s);
 }
 
 template <int ACT>
-hipError_t launch_act(const Plan& p, const GluGradArgs& a, bool aligned, hipStream_t s) {
-  if (p.dtype == PGG_F32) return launch_typed<TF32, ACT>(p, a, aligned, s);
-  return p.dtype == PGG_BF16 ? launch_typed<TBf16, ACT>(p, a, aligned, s) : launch_typed<TF16, ACT>(p, a, aligned, s);
+hipError_t launch_act(const Plan& p, const GluGradArgs& a, void* pa, void* pw, hipStream_t s) {
+  if (p.dtype == PGG_F32) return launch_typed<TF32, ACT>(p, a, pa, pw, s);
+  return p.dtype == PGG_BF16 ? launch_typed<TBf16, ACT>(p, a, pa, pw, s) : launch_typed<TF16, ACT>(p, a, pa, pw, s);
 }
 
 }  // namespace
 
 hipError_t launch_glu_grad(const Plan& p, int32_t act, const void* grad_y, const void* weight, const void* gate_up,
-                           void* grad, void* h, bool aligned, const WsView& w, hipStream_t s) {
+                           void* grad, void* h, void* ws, hipStream_t s) {
+  const WsView w = ws_view(p, ws);
   GluGradArgs a;
   a.A = grad_y;
   a.W = weight;
@@ -264,9 +283,12 @@ hipError_t launch_glu_grad(const Plan& p, int32_t act, const void* grad_y, const
   a.F = p.K;
   a.C = 2 * p.K;
   a.kspan = p.N;
+  a.lda = a.ldw = p.N;
   a.bm = p.bm;
-  return act == PGG_ACT_SILU ? launch_act<PGG_ACT_SILU>(p, a, aligned, s)
-                             : launch_act<PGG_ACT_GELU_TANH>(p, a, aligned, s);
+  void* pa = static_cast<char*>(ws) + p.off_pad_a;
+  void* pw = static_cast<char*>(ws) + p.off_pad_w;
+  return act == PGG_ACT_SILU ? launch_act<PGG_ACT_SILU>(p, a, pa, pw, s)
+                             : launch_act<PGG_ACT_GELU_TANH>(p, a, pa, pw, s);
 }
 
 }  // namespace pgg

@@ -27,7 +27,8 @@
 // With few tokens the projection is bound by reading W once and the launches:
 // the reduction is split over workgroups, the first launch also computes z,
 // token by token, in spare workgroups, and a second one adds the splits in
-// split order and the tokens' z * B_p.  Batches too small to fill the chip with
+// split order and the tokens' z * B_p.  Rows of x or W that are not 16-byte
+// aligned are copied to padded rows first where the plan finds that it pays.  Batches too small to fill the chip with
 // tiles split the reduction and finish in the same way.
 #include <algorithm>
 
@@ -53,6 +54,7 @@ struct LoraArgs {
   float* part;              // split partials [ksplit, T, C], or NULL
   WsHeader* hdr;
   int64_t R, C, T, kspan;
+  int64_t lda, ldw;         // row strides of A and W
   int64_t P;
   int32_t rank;
   int32_t few;              // few tokens: z comes with the product
@@ -293,7 +295,7 @@ struct LoraOp {
 
   // past the end: a valid column, not stored
   static __device__ __forceinline__ int64_t half_column(const Args& a, int ct, int j, int n) {
-    return min<int64_t>(first_column(ct, 256) + j * 128 + n, a.C - 8);
+    return min<int64_t>(first_column(ct, 256) + j * 128 + n, a.ldw - 8);
   }
 
   template <int BN>
@@ -487,10 +489,16 @@ hipError_t launch_shrink_token(const LoraArgs& a, hipStream_t s) {
 // adapter, but workgroups are many and their reads contiguous.
 constexpr int64_t kTokenByToken = 1024;
 
+// What the direct-to-LDS kernels need: 16-byte rows, and 32-bit byte offsets
+// into 256 rows of x and 64 rows of W.
+bool direct_rows(const LoraArgs& a) {
+  auto fits = [](const void* ptr, int64_t ld) { return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && ld % 8 == 0; };
+  return fits(a.A, a.lda) && fits(a.W, a.ldw) && a.lda < (int64_t(1) << 23) && a.ldw < (int64_t(1) << 25);
+}
+
 template <class T>
-hipError_t launch_typed(const LoraPlan& p, LoraArgs a, bool aligned, hipStream_t s) {
-  // the direct-to-LDS kernels' 32-bit byte offsets: into 256 rows of x and 64 rows of W
-  const bool direct = T::kPerChunk == 8 && aligned && a.R < (int64_t(1) << 23) && a.C < (int64_t(1) << 25);
+hipError_t launch_typed(const LoraPlan& p, LoraArgs a, void* padded_x, void* padded_w, hipStream_t s) {
+  const bool direct = T::kPerChunk == 8 && direct_rows(a);
   hipError_t e = hipSuccess;
   // z: beside the product, token by token, or in tiles
   if (a.few && !direct) e = launch_shrink_token<T, 1>(a, s);
@@ -506,11 +514,24 @@ hipError_t launch_typed(const LoraPlan& p, LoraArgs a, bool aligned, hipStream_t
                     : launch_few<T, LoraOp, 64>(a, LoraOp::extra(a), p.ksplit, s);
     } else if (a.few) {
       e = launch_reg<T, 32, 256, 1, 4>(a, p, s);
-    } else if (p.pipe && direct) {
-      a.n_slots = static_cast<int32_t>((a.T + 255) / 256);
-      e = launch_pipe<T, LoraOp, false>(a, p.ksplit, s);
     } else {
-      e = launch_reg<T, 128, 128, 2, 2>(a, p, s);
+      LoraArgs b = a;   // with the operands that the plan lays out anew
+      if (p.pad_a) {
+        b.A = padded_x;
+        b.lda = p.lda;
+      }
+      if (p.pad_w) {
+        b.W = padded_w;
+        b.ldw = p.ldw;
+      }
+      b.n_slots = static_cast<int32_t>((a.T + 255) / 256);
+      if (!p.pipe || !direct_rows(b)) {
+        e = launch_reg<T, 128, 128, 2, 2>(a, p, s);
+      } else {
+        if (p.pad_a) e = launch_pad_rows(a.A, padded_x, a.T, a.R, b.lda, s);
+        if (e == hipSuccess && p.pad_w) e = launch_pad_rows(a.W, padded_w, a.R, a.C, b.ldw, s);
+        if (e == hipSuccess) e = launch_pipe<T, LoraOp, false>(b, p.ksplit, s);
+      }
     }
   } else {
     e = a.few ? launch_reg<T, 32, 128, 1, 4>(a, p, s) : launch_reg<T, 128, 128, 2, 2>(a, p, s);
@@ -523,7 +544,7 @@ hipError_t launch_typed(const LoraPlan& p, LoraArgs a, bool aligned, hipStream_t
 }  // namespace
 
 hipError_t launch_lora(const LoraPlan& p, const void* x, const void* weight, const void* a, const void* b,
-                       const int64_t* ids, const float* scales, void* y, void* ws, bool aligned, hipStream_t s) {
+                       const int64_t* ids, const float* scales, void* y, void* ws, hipStream_t s) {
   char* base = static_cast<char*>(ws);
   LoraArgs g;
   g.A = x;
@@ -542,13 +563,17 @@ hipError_t launch_lora(const LoraPlan& p, const void* x, const void* weight, con
   g.W_end = static_cast<const char*>(weight) + es * p.K * p.N;
   g.a_end = static_cast<const char*>(a) + es * p.P * p.rank * p.K;
   g.R = p.K;
+  g.lda = p.K;
+  g.ldw = p.N;
   g.C = p.N;
   g.T = p.T;
   g.kspan = p.kspan;
   g.P = p.P;
   g.rank = p.rank;
-  if (p.dtype == PGG_F32) return launch_typed<TF32>(p, g, aligned, s);
-  return p.dtype == PGG_BF16 ? launch_typed<TBf16>(p, g, aligned, s) : launch_typed<TF16>(p, g, aligned, s);
+  void* px = base + p.off_pad_a;
+  void* pw = base + p.off_pad_w;
+  if (p.dtype == PGG_F32) return launch_typed<TF32>(p, g, px, pw, s);
+  return p.dtype == PGG_BF16 ? launch_typed<TBf16>(p, g, px, pw, s) : launch_typed<TF16>(p, g, px, pw, s);
 }
 
 }  // namespace pgg

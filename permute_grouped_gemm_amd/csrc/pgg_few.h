@@ -50,7 +50,7 @@ void few_kernel(typename Op::Args a, int32_t ksplit) {
   MTile tile;
   if (!Op::template tile<BM>(a, bid / a.n_col_tiles / ksplit, tile)) return;
   tile.pad = split;
-  const int64_t R = a.R, C = a.C;
+  const int64_t R = a.R, lda = a.lda, ldw = a.ldw;
   const int64_t kbeg = static_cast<int64_t>(split) * a.kspan;
   const int64_t span = min<int64_t>(R - kbeg, a.kspan);
 
@@ -63,23 +63,23 @@ void few_kernel(typename Op::Args a, int32_t ksplit) {
   const int ar = wave * kRowsPerWave + (lane >> 2) % kRowsPerWave;
   const int chunk = (lane & 3) ^ ((ar >> 2) & 3);
   const int64_t row_base = Op::src_base(a, tile);
-  const char* pa = reinterpret_cast<const char*>(static_cast<const E*>(a.A) + row_base * R + kbeg);
-  const uint32_t oa = static_cast<uint32_t>((Op::src(a, tile, min(ar, tile.rows - 1)) - row_base) * R * 2) + chunk * 16;
+  const char* pa = reinterpret_cast<const char*>(static_cast<const E*>(a.A) + row_base * lda + kbeg);
+  const uint32_t oa = static_cast<uint32_t>((Op::src(a, tile, min(ar, tile.rows - 1)) - row_base) * lda * 2) + chunk * 16;
   // W: load u of run j, 4 rows of k
-  const char* pb = reinterpret_cast<const char*>(static_cast<const E*>(a.W) + Op::weight(a, tile) + kbeg * C);
+  const char* pb = reinterpret_cast<const char*>(static_cast<const E*>(a.W) + Op::weight(a, tile) + kbeg * ldw);
   const int n = ((((lane & 15) >> 2) ^ lg) << 5) | (((lane & 3) ^ (wave & 2)) << 3);
   uint32_t ob[2][2];
 #pragma unroll
   for (int j = 0; j < 2; ++j)
 #pragma unroll
     for (int u = 0; u < 2; ++u)
-      ob[j][u] = static_cast<uint32_t>(((16 * u + 4 * wave + lg) * C + Op::half_column(a, ct, j, n)) * 2);
+      ob[j][u] = static_cast<uint32_t>(((16 * u + 4 * wave + lg) * ldw + Op::half_column(a, ct, j, n)) * 2);
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(lds));
   const void* zero = &kZero16;
 
   auto load = [&](int kt, int slot) {
     const uint32_t m0 = lds0 + slot * kStageBytes;
-    const char* p = pb + static_cast<int64_t>(kt) * 64 * C;
+    const char* p = pb + static_cast<int64_t>(kt) * 64 * ldw;
     const char* q = pa + static_cast<int64_t>(kt) * 64;
     const bool whole = (kt + 1) * 32 <= span;
 #pragma unroll

@@ -66,6 +66,10 @@ struct Plan {
   // large tiles with about one m-tile per expert: each weight slab is read
   // once, so its loads carry the non-temporal hint
   bool stream_weights;
+  // gated products: operands copied to padded rows of lda / ldw elements first
+  bool pad_a, pad_w;
+  int64_t lda, ldw;
+  size_t off_pad_a, off_pad_w;
   // layout (byte offsets into the workspace)
   size_t off_header, off_offsets, off_tiles, off_chunks, off_inv, off_ori, off_ring, total;
   size_t ring_bytes, table_bytes;
@@ -196,10 +200,12 @@ hipError_t launch_gate_grad(const pgg_moe_gate_desc& d, const void* logits, cons
 // and only the group tables.
 pgg_status make_glu_plan(const pgg_moe_glu_desc* desc, Plan* plan);
 hipError_t launch_glu(const Plan& p, int32_t act, const void* x, const void* weight, void* h, void* gate_up,
-                      bool aligned, const WsView& w, hipStream_t s);
+                      void* ws, hipStream_t s);
 pgg_status make_glu_grad_plan(const pgg_moe_glu_grad_desc* desc, Plan* plan);
 hipError_t launch_glu_grad(const Plan& p, int32_t act, const void* grad_y, const void* weight, const void* gate_up,
-                           void* grad, void* h, bool aligned, const WsView& w, hipStream_t s);
+                           void* grad, void* h, void* ws, hipStream_t s);
+// rows x len 16-bit elements to rows of `pitch` (a multiple of 8), zeros after len.
+hipError_t launch_pad_rows(const void* src, void* dst, int64_t rows, int64_t len, int64_t pitch, hipStream_t s);
 
 // Shared projection with low-rank adapters.
 struct LoraPlan {
@@ -209,11 +215,13 @@ struct LoraPlan {
   bool pipe;            // 16-bit types with 16-byte rows: 256 x 256 tiles
   int32_t ksplit;       // reduction splits (1: none)
   int64_t kspan;        // reduction elements per split
-  size_t off_header, off_z, off_part, total;
+  bool pad_a, pad_w;    // x, W copied to padded rows of lda, ldw elements first
+  int64_t lda, ldw;
+  size_t off_header, off_z, off_part, off_pad_a, off_pad_w, total;
 };
 pgg_status make_lora_plan(const pgg_lora_desc* desc, LoraPlan* plan);
 hipError_t launch_lora(const LoraPlan& p, const void* x, const void* weight, const void* a, const void* b,
-                       const int64_t* ids, const float* scales, void* y, void* ws, bool aligned, hipStream_t s);
+                       const int64_t* ids, const float* scales, void* y, void* ws, hipStream_t s);
 
 // Forward grouped matmul with the permute gathered into the A operand:
 // y[i, :] = x[ori[i] / topK, :] · W[g(i)] for every m-tile of the plan.

@@ -5,10 +5,10 @@
 // for a block of rows that share the [R, C] matrix W.  What differs between
 // the operators that use them comes as an Op:
 //
-//   Op::Args                 kernel arguments, with A, W and where they end
-//                            (A_end, W_end), R (the reduction), C
-//                            (the row length of W), n_slots, n_col_tiles, and
-//                            kspan (reduction elements of one split)
+//   Op::Args                 kernel arguments, with A, W, where they end (A_end,
+//                            W_end) and their row strides (lda, ldw), R (the
+//                            reduction), n_slots, n_col_tiles, and kspan
+//                            (reduction elements of one split)
 //   Op::tile<BM>(args, slot, t)  rows [t.row0, t.row0 + t.rows) of group t.g; false:
 //                            no tile.  (The kernels put the split into t.pad.)
 //   Op::src(args, t, r)      row of A that tile row r reads
@@ -295,7 +295,7 @@ void nn_reg_kernel(typename Op::Args a) {
   if (!Op::template tile<BM>(a, slot, tile)) return;
   tile.pad = blockIdx.y;
   const int rows = tile.rows;
-  const int64_t C = a.C;
+  const int64_t ldw = a.ldw;
   const int64_t kbeg = static_cast<int64_t>(blockIdx.y) * a.kspan;
   const int64_t kend = min<int64_t>(a.R, kbeg + a.kspan);
 
@@ -309,7 +309,7 @@ void nn_reg_kernel(typename Op::Args a) {
 #pragma unroll
   for (int s = 0; s < A_PER_T; ++s) {
     const int q = tid + s * NT;
-    arow[s] = static_cast<const E*>(a.A) + Op::src(a, tile, min(q / kChunks, rows - 1)) * a.R + (q % kChunks) * EPC;
+    arow[s] = static_cast<const E*>(a.A) + Op::src(a, tile, min(q / kChunks, rows - 1)) * a.lda + (q % kChunks) * EPC;
   }
   // Columns past the matrix are not stored, so a chunk may hold anything there:
   // it is read whole, from the row's end on into the next row, and a chunk
@@ -326,13 +326,13 @@ void nn_reg_kernel(typename Op::Args a) {
   u32x4_t ra[A_PER_T], rb[B_PER_T];
   auto load_stage = [&](int kt) {
     const int64_t k0 = kbeg + static_cast<int64_t>(kt) * BK;
-    const E* wk = W + k0 * C;
+    const E* wk = W + k0 * ldw;
     // inside the reduction, and a chunk may run past the stage's last row
-    if (k0 + BK <= kend && wk + BK * C + EPC <= static_cast<const E*>(a.W_end)) {
+    if (k0 + BK <= kend && wk + BK * ldw + EPC <= static_cast<const E*>(a.W_end)) {
 #pragma unroll
       for (int s = 0; s < A_PER_T; ++s) ra[s] = load16(arow[s] + k0);
 #pragma unroll
-      for (int s = 0; s < B_PER_T; ++s) rb[s] = load16(wk + (tid + s * NT) / kRowChunks * C + col[s]);
+      for (int s = 0; s < B_PER_T; ++s) rb[s] = load16(wk + (tid + s * NT) / kRowChunks * ldw + col[s]);
     } else {
 #pragma unroll
       for (int s = 0; s < A_PER_T; ++s)
@@ -340,7 +340,7 @@ void nn_reg_kernel(typename Op::Args a) {
 #pragma unroll
       for (int s = 0; s < B_PER_T; ++s) {
         const int k = (tid + s * NT) / kRowChunks;
-        rb[s] = load16_part<T>(wk + k * C + col[s], k0 + k < kend ? EPC : 0, a.W_end);
+        rb[s] = load16_part<T>(wk + k * ldw + col[s], k0 + k < kend ? EPC : 0, a.W_end);
       }
     }
   };

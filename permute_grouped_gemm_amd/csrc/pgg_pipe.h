@@ -179,7 +179,7 @@ void pipe_kernel(typename Op::Args a) {
   if (!Op::template tile<256>(a, slot, tile)) return;
   tile.pad = blockIdx.y;
   // this workgroup's split of the reduction
-  const int64_t R = a.R, C = a.C;
+  const int64_t R = a.R, lda = a.lda, ldw = a.ldw;
   const int64_t kbeg = static_cast<int64_t>(blockIdx.y) * a.kspan;
   const int64_t span = min<int64_t>(R - kbeg, a.kspan);
 
@@ -196,30 +196,30 @@ void pipe_kernel(typename Op::Args a) {
   const int l8 = lane >> 3;
   const int chunk = a_slot(8 * wave + l8, lane & 7);
   const int64_t row_base = Op::src_base(a, tile);
-  const char* pa = reinterpret_cast<const char*>(static_cast<const E*>(a.A) + row_base * R + kbeg);
+  const char* pa = reinterpret_cast<const char*>(static_cast<const E*>(a.A) + row_base * lda + kbeg);
   uint32_t oa[2][2];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int r = min(128 * u + 64 * h + 8 * wave + l8, tile.rows - 1);
-      oa[h][u] = static_cast<uint32_t>((Op::src(a, tile, r) - row_base) * R * 2) + chunk * 16;
+      oa[h][u] = static_cast<uint32_t>((Op::src(a, tile, r) - row_base) * lda * 2) + chunk * 16;
     }
   // Load u of quarter B_j.  NT: 8 columns' rows, as for A.  Otherwise 4 rows of
   // k, 256 bytes each, whose 16-byte chunks sit where quarter_offset puts them.
-  const E* W = static_cast<const E*>(a.W) + Op::weight(a, tile) + kbeg * (NT ? 1 : C);
+  const E* W = static_cast<const E*>(a.W) + Op::weight(a, tile) + kbeg * (NT ? 1 : ldw);
   const int kq = lane >> 4;                                     // which of the 4 rows
   const char* pb;
   uint32_t ob[2][2];
   if constexpr (NT) {
     const int64_t c0 = Op::first_column(ct, 256);
-    pb = reinterpret_cast<const char*>(W + c0 * R);
+    pb = reinterpret_cast<const char*>(W + c0 * ldw);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int64_t c = min<int64_t>(c0 + 128 * j + 64 * u + 8 * wave + l8, a.F - 1);
-        ob[j][u] = static_cast<uint32_t>((c - c0) * R * 2) + chunk * 16;
+        ob[j][u] = static_cast<uint32_t>((c - c0) * ldw * 2) + chunk * 16;
       }
   } else {
     pb = reinterpret_cast<const char*>(W);
@@ -229,7 +229,7 @@ void pipe_kernel(typename Op::Args a) {
       const int64_t c = Op::half_column(a, ct, j, n);
 #pragma unroll
       for (int u = 0; u < 2; ++u)
-        ob[j][u] = static_cast<uint32_t>(((32 * u + 4 * wave + kq) * C + c) * 2);
+        ob[j][u] = static_cast<uint32_t>(((32 * u + 4 * wave + kq) * ldw + c) * 2);
     }
   }
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(lds));
@@ -251,7 +251,7 @@ void pipe_kernel(typename Op::Args a) {
   };
   auto load_b = [&](int kt, int j, auto whole) {
     const uint32_t m0 = lds0 + (kt & 1) * kStageBytes + kB + j * kQuarter + wave * 1024;
-    const char* p = pb + static_cast<int64_t>(kt) * (NT ? 128 : 128 * C);
+    const char* p = pb + static_cast<int64_t>(kt) * (NT ? 128 : 128 * ldw);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int64_t k = static_cast<int64_t>(kt) * 64 + (NT ? chunk * 8 : 32 * u + 4 * wave + kq);

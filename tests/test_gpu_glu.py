@@ -48,7 +48,8 @@ def _run(x, w, eri, gl, topk, row_idx_type, act, save=True):
 # that end inside K, F and the expert's rows
 GLU = [(1, 1, 1, 1, 1), (1, 2, 4, 64, 32), (5, 2, 3, 33, 7), (16, 8, 16, 2048, 128), (17, 3, 5, 1000, 72),
        (64, 2, 4, 256, 64), (100, 4, 6, 520, 200), (257, 2, 3, 129, 65), (400, 2, 2, 328, 136),
-       (300, 1, 1, 200, 264), (200, 1, 1, 40, 24), (520, 1, 2, 64, 8), (260, 1, 1, 136, 520)]
+       (300, 1, 1, 200, 264), (200, 1, 1, 40, 24), (520, 1, 2, 64, 8), (260, 1, 1, 136, 520),
+       (600, 1, 1, 67, 35), (600, 1, 1, 72, 35), (600, 1, 1, 67, 40), (90, 1, 1, 67, 40)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
@@ -116,7 +117,8 @@ def test_extreme_gates():
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("batch,topk,G,D,F", [(1, 1, 1, 1, 1), (1, 2, 4, 64, 32), (5, 2, 3, 33, 7), (40, 2, 5, 200, 136),
                                               (333, 2, 7, 203, 141), (300, 1, 1, 264, 200), (257, 2, 2, 520, 264),
-                                              (600, 2, 3, 192, 320), (200, 1, 1, 40, 24), (520, 1, 2, 64, 8)])
+                                              (600, 2, 3, 192, 320), (200, 1, 1, 40, 24), (520, 1, 2, 64, 8),
+                                              (600, 1, 1, 67, 35), (1100, 1, 2, 135, 130)])
 def test_glu_grad(batch, topk, G, D, F, dtype):
     _, gl = _routing(batch, topk, G, D + F, 0, 1.0, min(1, G - topk))
     gen = torch.Generator().manual_seed(D)
@@ -166,6 +168,33 @@ def test_glu_grad_against_differences():
 
 def rounded_bound(gy, w, gu, gl, act):
     return ref.glu_grad(gy, w, gu, gl, act)[1]
+
+
+def _moved(t):
+    """The same values at an address one element past an aligned one."""
+    big = torch.empty(t.numel() + 8, dtype=t.dtype, device=DEV)
+    out = big[1:1 + t.numel()].view(t.shape)
+    out.copy_(t)
+    return out
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("batch,topk,G,K,F", [(16, 4, 8, 128, 64), (300, 2, 2, 128, 64), (600, 1, 1, 72, 40)])
+def test_operands_at_any_address(batch, topk, G, K, F, dtype):
+    x, w, eri, gl = _make(batch, topk, G, K, F, dtype, 31)
+    wh, eh, wy, ey = ref.glu(x, w, eri, gl, topk, 0, "silu")
+    M = batch * topk
+    h, gu = _moved(torch.zeros((M, F), dtype=x.dtype)), _moved(torch.zeros((M, 2 * F), dtype=x.dtype))
+    pgg.moe_glu(_moved(x), _moved(w), eri.to(DEV), gl.to(DEV), topk, out=h, gate_up=gu)
+    ref.assert_within(h, wh, eh, "h")
+    ref.assert_within(gu, wy, ey, "gate_up")
+    w2 = w[:, :, :F].transpose(1, 2).contiguous()          # [G, F, K]
+    gy, gu = x.repeat_interleave(topk, 0).contiguous(), gu.cpu()
+    out = _moved(torch.zeros((M, 2 * F), dtype=x.dtype))
+    grad, hh = pgg.moe_glu_grad(_moved(gy), _moved(w2), _moved(gu), gl.to(DEV), out=out)
+    wg, eg, wh, eh = ref.glu_grad(gy, w2, gu, gl, "silu")
+    ref.assert_within(grad, wg, eg, "grad")
+    ref.assert_within(hh, wh, eh, "h")
 
 
 def test_wrong_routing_sets_the_error_word():

@@ -37,7 +37,9 @@ def _run(*args):
 # tokens, K, N, adapters, rank: single tokens; a few; the boundaries of the
 # tiles (32, 64, 128, 256); odd sizes; ranks that do not fill a step
 SHAPES = [(1, 1, 1, 1, 1), (1, 2048, 264, 4, 8), (2, 67, 33, 3, 5), (16, 520, 300, 20, 16), (33, 256, 129, 2, 17),
-          (64, 1000, 70, 70, 3), (65, 129, 257, 5, 33), (130, 72, 136, 1, 64), (300, 264, 520, 7, 12), (257, 99, 101, 3, 40)]
+          (64, 1000, 70, 70, 3), (65, 129, 257, 5, 33), (130, 72, 136, 1, 64), (300, 264, 520, 7, 12), (257, 99, 101, 3, 40),
+          (600, 67, 35, 4, 9), (600, 72, 35, 4, 16), (520, 67, 40, 3, 70), (90, 67, 64, 3, 8), (1100, 128, 64, 6, 16),
+          (2100, 67, 35, 4, 9)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
@@ -96,6 +98,19 @@ def test_inner_products_beyond_the_range_of_fp16(dtype):
     y = _run(x, w, a, b, ids, s)
     want, bound = ref.lora(x, w, a, b, ids, s)
     ref.assert_within(y, want, bound)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,K,N", [(8, 256, 128), (300, 128, 264), (600, 72, 40)])
+def test_operands_at_any_address(T, K, N, dtype):
+    def moved(t):
+        out = torch.empty(t.numel() + 8, dtype=t.dtype, device=DEV)[1:1 + t.numel()].view(t.shape)
+        return out.copy_(t)
+    args = _make(T, K, N, 5, 8, dtype, 12)
+    out = moved(torch.zeros((T, N), dtype=args[0].dtype))
+    pgg.lora_fwd(*[moved(t) for t in args], out=out)
+    want, bound = ref.lora(*args)
+    ref.assert_within(out, want, bound)
 
 
 def test_token_rows_do_not_depend_on_the_batch_order():
