@@ -176,7 +176,7 @@ hipError_t launch_16(const Plan& p, GluArgs a, void* padded_x, void* padded_w, h
   hipError_t e = hipSuccess;
   if (p.pad_a) e = launch_pad_rows(a.A, padded_x, p.batch, a.R, b.lda, s);
   if (e == hipSuccess && p.pad_w) e = launch_pad_rows(a.W, padded_w, p.G * a.R * 2, a.F, b.Fw, s);
-  return e == hipSuccess ? launch_pipe<T, GluOp<ACT>, false>(b, 1, s) : e;
+  return e == hipSuccess ? launch_pipe<T, GluOp<ACT>, false>(b, p.ksplit, s) : e;
 }
 
 template <class T, int ACT>

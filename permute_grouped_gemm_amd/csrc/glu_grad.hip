@@ -11,7 +11,11 @@
 //
 // Both operands hold the reduction d contiguously, the layout that MFMA
 // operands take, so tiles are staged in LDS as rows of 16-byte chunks, chunk c
-// of row r at c ^ ((r >> 1) & 7).
+// of row r at c ^ ((r >> 1) & 7).  Calls with too few tiles to fill the chip
+// split the reduction; the fp32 partial products of the splits go to the
+// workspace and a second kernel adds them in split order.
+#include <algorithm>
+
 #include "pgg_act.h"
 #include "pgg_pipe.h"
 
@@ -29,6 +33,8 @@ struct GluGradArgs {
   const MTile* tiles;
   void* grad;               // [M, C]
   void* h;                  // [M, F] or NULL
+  float* part;              // split partials of dh [ksplit, M, F], or NULL
+  int64_t M;
   int64_t R, C, F, kspan;
   int64_t lda, ldw;         // row strides of A and W
   int32_t bm;               // rows of a table entry
@@ -71,6 +77,7 @@ struct GluGradOp {
 
   template <class T>
   static __device__ __forceinline__ Side<T> fetch(const Args& a, const MTile& t, int m, int64_t f, int64_t left) {
+    if (a.part) return {};
     const typename T::elem* p = static_cast<const typename T::elem*>(a.gate_up) + int64_t(t.row0 + m) * a.C + f;
     return {load_raw8<T>(p, left), load_raw8<T>(p + a.F, left)};
   }
@@ -80,6 +87,10 @@ struct GluGradOp {
                                                const float (&dh)[8], const Side<T>& side) {
     using E = typename T::elem;
     const int64_t row = t.row0 + m, at = row * a.C + f;
+    if (a.part) {
+      store8<TF32, false>(a.part + (static_cast<int64_t>(t.pad) * a.M + row) * a.F + f, left, dh);
+      return;
+    }
     float gate[8], up[8], h[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -119,8 +130,10 @@ void glu_grad_reg_kernel(GluGradArgs a) {
   if (!tile_place(a, slot, ct)) return;
   MTile tile;
   if (!Op::template tile<BM>(a, slot, tile)) return;
+  tile.pad = blockIdx.y;
   const int64_t col0 = Op::first_column(ct, BN);
-  const int64_t D = a.R;
+  const int64_t kbeg = static_cast<int64_t>(blockIdx.y) * a.kspan;   // this workgroup's split
+  const int64_t D = min<int64_t>(a.R - kbeg, a.kspan);
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -133,13 +146,13 @@ void glu_grad_reg_kernel(GluGradArgs a) {
 #pragma unroll
   for (int s = 0; s < A_PER_T; ++s) {
     const int q = tid + s * NT;
-    arow[s] = static_cast<const E*>(a.A) + Op::src(a, tile, min(q / kChunks, tile.rows - 1)) * a.lda + (q % kChunks) * EPC;
+    arow[s] = static_cast<const E*>(a.A) + Op::src(a, tile, min(q / kChunks, tile.rows - 1)) * a.lda + kbeg + (q % kChunks) * EPC;
   }
 #pragma unroll
   for (int s = 0; s < B_PER_T; ++s) {
     const int q = tid + s * NT;
     const int64_t f = min<int64_t>(col0 + q / kChunks, a.F - 1);
-    brow[s] = static_cast<const E*>(a.W) + Op::weight(a, tile) + f * a.ldw + (q % kChunks) * EPC;
+    brow[s] = static_cast<const E*>(a.W) + Op::weight(a, tile) + f * a.ldw + kbeg + (q % kChunks) * EPC;
   }
 
   u32x4_t ra[A_PER_T], rb[B_PER_T];
@@ -222,7 +235,7 @@ hipError_t launch_reg(const Plan& p, GluGradArgs a, hipStream_t s) {
   constexpr int BN = 128;
   a.n_slots = p.max_tiles * (p.bm / BM);
   a.n_col_tiles = static_cast<int32_t>((a.F + BN - 1) / BN);
-  hipLaunchKernelGGL((glu_grad_reg_kernel<T, GluGradOp<ACT>, BM, BN, WM, 4 / WM, EU>), dim3(tile_blocks(a)), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((glu_grad_reg_kernel<T, GluGradOp<ACT>, BM, BN, WM, 4 / WM, EU>), dim3(tile_blocks(a), p.ksplit), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -251,16 +264,48 @@ hipError_t launch_typed(const Plan& p, GluGradArgs a, void* padded_a, void* padd
       }
       b.n_slots = p.max_tiles;
       b.n_col_tiles = static_cast<int32_t>((a.F + 255) / 256);
-      return e == hipSuccess ? launch_pipe<T, GluGradOp<ACT>, true>(b, 1, s) : e;
+      return e == hipSuccess ? launch_pipe<T, GluGradOp<ACT>, true>(b, p.ksplit, s) : e;
     }
   }
   return launch_reg<T, 128, 2, 2, ACT>(p, a, s);
 }
 
+// Adds the splits' partial products in split order and stores the gradients.
+template <class T, int ACT>
+__global__ __launch_bounds__(256) void glu_grad_finish_kernel(GluGradArgs a, int32_t ksplit) {
+  using E = typename T::elem;
+  if (a.hdr->err != kNoError) return;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  const int64_t n = a.M * a.F;
+  for (int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < n; e += step) {
+    const int64_t row = e / a.F, at = row * a.C + (e - row * a.F);
+    float dh = a.part[e];
+#pragma unroll 8
+    for (int32_t s = 1; s < ksplit; ++s) dh += a.part[s * n + e];
+    const E* gu = static_cast<const E*>(a.gate_up);
+    const float up = to_float<T>(gu[at + a.F]);
+    float value, slope;
+    activate_grad<ACT>(to_float<T>(gu[at]), value, slope);
+    static_cast<E*>(a.grad)[at] = from_float<T>(dh * up * slope);
+    static_cast<E*>(a.grad)[at + a.F] = from_float<T>(dh * value);
+    if (a.h) static_cast<E*>(a.h)[e] = from_float<T>(value * up);
+  }
+}
+
+template <class T, int ACT>
+hipError_t launch_all(const Plan& p, const GluGradArgs& a, void* pa, void* pw, hipStream_t s) {
+  const hipError_t e = launch_typed<T, ACT>(p, a, pa, pw, s);
+  if (e != hipSuccess || p.ksplit == 1) return e;
+  const int64_t blocks = std::min<int64_t>((a.M * a.F + 255) / 256, 2048);
+  hipLaunchKernelGGL((glu_grad_finish_kernel<T, ACT>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a,
+                     p.ksplit);
+  return hipGetLastError();
+}
+
 template <int ACT>
 hipError_t launch_act(const Plan& p, const GluGradArgs& a, void* pa, void* pw, hipStream_t s) {
-  if (p.dtype == PGG_F32) return launch_typed<TF32, ACT>(p, a, pa, pw, s);
-  return p.dtype == PGG_BF16 ? launch_typed<TBf16, ACT>(p, a, pa, pw, s) : launch_typed<TF16, ACT>(p, a, pa, pw, s);
+  if (p.dtype == PGG_F32) return launch_all<TF32, ACT>(p, a, pa, pw, s);
+  return p.dtype == PGG_BF16 ? launch_all<TBf16, ACT>(p, a, pa, pw, s) : launch_all<TF16, ACT>(p, a, pa, pw, s);
 }
 
 }  // namespace
@@ -282,7 +327,9 @@ hipError_t launch_glu_grad(const Plan& p, int32_t act, const void* grad_y, const
   a.R = p.N;          // the plan keeps the reduction in N and the columns in K
   a.F = p.K;
   a.C = 2 * p.K;
-  a.kspan = p.N;
+  a.kspan = p.kspan;
+  a.M = p.M;
+  a.part = p.ksplit > 1 ? w.ring : nullptr;
   a.lda = a.ldw = p.N;
   a.bm = p.bm;
   void* pa = static_cast<char*>(ws) + p.off_pad_a;

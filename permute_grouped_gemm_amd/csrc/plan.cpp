@@ -549,8 +549,10 @@ pgg_status make_glu_plan(const pgg_moe_glu_desc* d, Plan* p) {
   // times as many as the plan's; a launch holds fewer than 2^32 lanes
   if (int64_t(p->max_tiles) * p->n_col_tiles >= (int64_t(1) << 21)) return PGG_ERR_UNSUPPORTED;
   p->fused_prep = p->M <= 1024;
-  // Few rows per expert: m-tiles of 32 rows x 256 columns (128 of h), the
-  // reduction split until about 512 workgroups have work, two per compute unit.
+  // Few rows per expert: m-tiles of 32 rows x 256 columns (128 of h), two
+  // workgroups per compute unit; otherwise one of the large tiles, or two of
+  // 128 x 128.  Where tiles alone do not fill the chip, the reduction is split.
+  const int64_t cus = p->regime == kLarge ? 256 : 512;
   if (p->M <= 64 * p->G) {
     p->regime = kStream;
     p->bm = 32;
@@ -559,9 +561,9 @@ pgg_status make_glu_plan(const pgg_moe_glu_desc* d, Plan* p) {
     p->n_col_tiles = static_cast<int32_t>((p->K + 255) / 256);
   }
   p->max_tiles = static_cast<int32_t>(std::min<int64_t>(p->max_tiles, p->M));   // each holds a row at least
-  if (p->regime == kStream) {
-    split_reduction(p->N, int64_t(p->max_tiles) * p->n_col_tiles, 512, p->dtype == PGG_F32 ? 32 : 256, &p->ksplit, &p->kspan);
-  }
+  const int64_t busy = std::min<int64_t>(p->max_tiles, p->M / p->bm + (p->G + 1) / 2 + 1) * p->n_col_tiles;
+  split_reduction(p->N, busy, p->regime == kStream ? 512 : cus,
+                  p->regime != kStream ? 256 : p->dtype == PGG_F32 ? 32 : 128, &p->ksplit, &p->kspan);
   p->tc = p->max_tiles;
   size_t off = p->off_tiles;
   off = align_up(off + sizeof(MTile) * size_t(p->max_tiles), kRegionAlign);
@@ -621,7 +623,11 @@ pgg_status make_glu_grad_plan(const pgg_moe_glu_grad_desc* d, Plan* p) {
   q.max_chunks = 1;
   q.n_panels = 1;
   q.n_col_tiles = static_cast<int32_t>(col_tiles);
-  q.ksplit = 1;
+  // Where tiles alone do not fill the chip (one 256 x 256 tile, two of 128 x
+  // 128 or four of 32 x 128 per compute unit), the reduction is split.
+  const int64_t busy_cols = q.bm == 256 ? (F + 255) / 256 : col_tiles;
+  const int64_t busy = std::min<int64_t>(max_tiles, M / q.bm + (G + 1) / 2 + 1) * busy_cols;
+  split_reduction(D, busy, q.bm == 256 ? 256 : q.bm == 128 ? 512 : 1024, q.bm == 32 ? 128 : 256, &q.ksplit, &q.kspan);
   size_t off = 0;
   q.off_header = off;   off = align_up(off + sizeof(WsHeader), kRegionAlign);
   q.off_offsets = off;  off = align_up(off + sizeof(int64_t) * size_t(G + 1), kRegionAlign);
@@ -629,6 +635,7 @@ pgg_status make_glu_grad_plan(const pgg_moe_glu_grad_desc* d, Plan* p) {
   q.off_chunks = off;   off = align_up(off + sizeof(int32_t) * 2, kRegionAlign);
   q.off_inv = q.off_ori = q.off_ring = off;
   q.table_bytes = off;
+  if (q.ksplit > 1) off = align_up(off + size_t(q.ksplit) * size_t(M) * size_t(F) * sizeof(float), kRegionAlign);
   q.lda = q.ldw = D;
   q.off_pad_a = q.off_pad_w = off;
   q.pad_a = q.pad_w = q.bm == 256 && D % 8 != 0 && M / G >= kPadRowsGluGrad;
@@ -672,9 +679,9 @@ pgg_status make_lora_plan(const pgg_lora_desc* d, LoraPlan* p) {
   q.pipe = !q.few && !f32 && w_pays;
   q.pad_a = q.pipe && q.K % 8 != 0;
   q.pad_w = q.pipe && q.N % 8 != 0;
-  if (q.few) split_reduction(q.K, tiles(64, f32 ? 128 : 256), 512, 192, &q.ksplit, &q.kspan);
-  else if (q.pipe) split_reduction(q.K, tiles(256, 256), 256, 512, &q.ksplit, &q.kspan);
-  else split_reduction(q.K, tiles(128, 128), 512, 512, &q.ksplit, &q.kspan);
+  if (q.few) split_reduction(q.K, tiles(64, f32 ? 128 : 256), 512, 128, &q.ksplit, &q.kspan);
+  else if (q.pipe) split_reduction(q.K, tiles(256, 256), 256, 256, &q.ksplit, &q.kspan);
+  else split_reduction(q.K, tiles(128, 128), 512, 256, &q.ksplit, &q.kspan);
   size_t off = 0;
   q.off_header = off; off = align_up(off + sizeof(WsHeader), kRegionAlign);
   q.off_z = off;      off = align_up(off + sizeof(float) * size_t(q.T) * size_t(q.rank), kRegionAlign);
