@@ -17,7 +17,7 @@ __global__ __launch_bounds__(kPrepThreads) void prep_groups_kernel(PrepArgs a, c
   __shared__ long long scratch[2 * kPrepThreads];
   reset_header(w.hdr);
   __syncthreads();
-  groups_phase(a, gl, w, scratch, scratch + kPrepThreads);
+  groups_phase(a, gl, w, scratch, scratch + blockDim.x);
 }
 
 __global__ __launch_bounds__(256) void prep_index_kernel(PrepArgs a, const int64_t* eri, WsView w) {
@@ -64,7 +64,9 @@ hipError_t launch_prep_fused(const Plan& p, const int64_t* eri, const int64_t* g
 }
 
 hipError_t launch_prep_groups(const Plan& p, const int64_t* gl, const WsView& w, hipStream_t s) {
-  hipLaunchKernelGGL(prep_groups_kernel, dim3(1), dim3(kPrepThreads), 0, s, prep_args(p), gl, w);
+  // few groups: one wave, as above (7 -> 4 us at 64 groups)
+  const unsigned threads = p.M <= 4096 && p.G <= 4096 ? 64u : unsigned(kPrepThreads);
+  hipLaunchKernelGGL(prep_groups_kernel, dim3(1), dim3(threads), 0, s, prep_args(p), gl, w);
   return hipGetLastError();
 }
 
