@@ -787,8 +787,11 @@ def _value_type(t, name, dim):
 
 
 def _on_stream(stream, dev):
-    """Handle of ``stream``, or of the current stream of ``dev`` (asked for
-    directly: a Stream object would cost a small call 2 of its 10 us)."""
+    """Handle of ``stream``, or of the current stream of ``dev``, which must be
+    the current device (asked for directly: a Stream object would cost a small
+    call 2 of its 10 us)."""
+    if torch._C._cuda_getDevice() != dev.index:
+        raise PggError(ERR_INVALID_ARG, f"the inputs are on {dev}, which is not the current device")
     return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else int(stream.cuda_stream)
 
 

@@ -151,7 +151,7 @@ hipError_t launch_reg(const Plan& p, GluArgs a, hipStream_t s) {
 // into all of x and into 64 rows of W.
 bool direct(const Plan& p, const GluArgs& a) {
   auto fits = [](const void* ptr, int64_t ld) { return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && ld % 8 == 0; };
-  return fits(a.A, a.lda) && fits(a.W, a.ldw) && a.Fw % 8 == 0 && p.batch * a.lda < (int64_t(1) << 31) &&
+  return fits(a.A, a.lda) && fits(a.W, a.ldw) && a.Fw % 8 == 0 && p.batch * a.lda < (int64_t(1) << 31) - 64 &&
          a.ldw < (int64_t(1) << 25);
 }
 

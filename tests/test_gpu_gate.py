@@ -164,6 +164,24 @@ def test_gate_is_repeatable_and_follows_its_stream():
         assert torch.equal(u, v)
 
 
+def test_gate_captures_into_a_graph():
+    l = _logits(300, 60, "f16", 2).to(DEV)
+    graph = torch.cuda.CUDAGraph()
+    gp = torch.randn((300, 8), device=DEV)
+    want = pgg.moe_gate(l, 8)
+    want_grad = pgg.moe_gate_grad(l, want[2], want[0], gp)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = pgg.moe_gate(l, 8)
+        grad = pgg.moe_gate_grad(l, got[2], got[0], gp)
+    for _ in range(3):
+        for t in (*got, grad):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for u, v in zip(got, want)) and torch.equal(grad, want_grad)
+
+
 def test_gate_refusals():
     l = torch.zeros((4, 8), device=DEV)
     for call in (lambda: pgg.moe_gate(l, 0), lambda: pgg.moe_gate(l, 9), lambda: pgg.moe_gate(l.cpu(), 2),

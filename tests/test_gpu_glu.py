@@ -233,6 +233,27 @@ def test_glu_captures_into_a_graph():
             assert torch.equal(h, want) and torch.equal(gu, want_gu)
 
 
+def test_glu_grad_captures_into_a_graph():
+    gen = torch.Generator().manual_seed(9)
+    for M, G, D, F in ((40, 8, 200, 48), (700, 2, 192, 160), (600, 1, 67, 35)):
+        gl = torch.full((G,), M // G)
+        gy, w, gu = torch.randn((M, D), generator=gen), torch.randn((G, F, D), generator=gen), torch.randn((M, 2 * F), generator=gen)
+        gy, w, gu, gl = [t.to(DEV) for t in (gy.half(), (w * 0.05).half(), gu.half(), gl)]
+        ws = torch.empty(pgg.glu_grad_workspace_size(gy, w, gu, gl), dtype=torch.uint8, device=DEV)
+        out, h = pgg.moe_glu_grad(gy, w, gu, gl, workspace=ws)
+        want, want_h = out.clone(), h.clone()
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            pgg.moe_glu_grad(gy, w, gu, gl, out=out, h=h, workspace=ws)
+        for _ in range(3):
+            out.fill_(math.nan)
+            h.fill_(math.nan)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want) and torch.equal(h, want_h)
+
+
 def test_glu_refusals():
     x, w, eri, gl = [t.to(DEV) for t in _make(8, 2, 4, 32, 16, "bf16", 1)]
     short = torch.empty(64, dtype=torch.uint8, device=DEV)
