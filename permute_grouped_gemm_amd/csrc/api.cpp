@@ -582,8 +582,10 @@ pgg_status pgg_moe_glu(const pgg_moe_glu_desc* desc, const void* x, const void* 
       !is_aligned(x, es) || !is_aligned(weight, es) || !is_aligned(h, es) || !is_aligned(gate_up, es))
     return PGG_ERR_MISALIGNED;
   const WsView w = ws_view(p, workspace);
-  hipError_t e;
-  if (p.fused_prep) {
+  hipError_t e = hipSuccess;
+  if (p.local) {
+    // the tiles find their rows themselves
+  } else if (p.fused_prep) {
     TimedLaunch t("prep_fused", stream);
     e = launch_prep_fused(p, expanded_row_idx, group_list, w, stream);
   } else {
@@ -598,7 +600,7 @@ pgg_status pgg_moe_glu(const pgg_moe_glu_desc* desc, const void* x, const void* 
   }
   if (e == hipSuccess) {
     TimedLaunch t("glu", stream);
-    e = launch_glu(p, desc->act, x, weight, h, gate_up, workspace, stream);
+    e = launch_glu(p, desc->act, x, weight, h, gate_up, expanded_row_idx, group_list, workspace, stream);
   }
   return e == hipSuccess ? PGG_OK : PGG_ERR_HIP;
 }
@@ -625,14 +627,14 @@ pgg_status pgg_moe_glu_grad(const pgg_moe_glu_grad_desc* desc, const void* grad_
       !is_aligned(weight, es) || !is_aligned(gate_up, es) || !is_aligned(grad_gate_up, es) || !is_aligned(h, es))
     return PGG_ERR_MISALIGNED;
   const WsView w = ws_view(p, workspace);
-  hipError_t e;
-  {
+  hipError_t e = hipSuccess;
+  if (!p.local) {
     TimedLaunch t("prep_groups", stream);
     e = launch_prep_groups(p, group_list, w, stream);
   }
   if (e == hipSuccess) {
     TimedLaunch t("glu_grad", stream);
-    e = launch_glu_grad(p, desc->act, grad_y, weight, gate_up, grad_gate_up, h, workspace, stream);
+    e = launch_glu_grad(p, desc->act, grad_y, weight, gate_up, group_list, grad_gate_up, h, workspace, stream);
   }
   return e == hipSuccess ? PGG_OK : PGG_ERR_HIP;
 }

@@ -23,6 +23,7 @@
 
 #include "pgg_act.h"
 #include "pgg_few.h"
+#include "pgg_local.h"
 
 namespace pgg {
 
@@ -44,6 +45,12 @@ struct GluArgs {
   uint32_t topk;
   int32_t bm;               // rows of a table entry
   int32_t n_slots, n_col_tiles;
+  // without tables: group_list and the index themselves, and the preparation for the error word
+  int32_t local;
+  const int64_t* eri;
+  const int64_t* gl;
+  PrepArgs prep;
+  WsView ws;
 };
 
 template <int ACT>
@@ -51,7 +58,15 @@ struct GluOp {
   using Args = GluArgs;
 
   template <int BM>
-  static __device__ __forceinline__ bool tile(const Args& a, int slot, MTile& t) {
+  static __device__ __forceinline__ bool tile(const Args& a, int slot, MTile& t, void* lds) {
+    if constexpr (BM == 32) {
+      if (a.local) {
+        int32_t* words = static_cast<int32_t*>(lds);
+        if (!local_tile(a.gl, a.prep.G, a.M, BM, slot, t, words)) return false;
+        local_rows(a.eri, a.M, a.prep.row_idx_type, t, words + kLocalWords);
+        return true;
+      }
+    }
     if (a.hdr->err != kNoError) return false;
     const int sub = a.bm / BM;   // tiles to a table entry
     const int entry = slot / sub;
@@ -63,8 +78,9 @@ struct GluOp {
     return t.rows > 0;
   }
 
-  static __device__ __forceinline__ int64_t src(const Args& a, const MTile& t, int r) {
-    return static_cast<uint32_t>(a.ori[t.row0 + r]) / a.topk;
+  static __device__ __forceinline__ int64_t src(const Args& a, const MTile& t, int r, const void* lds) {
+    const int32_t p = a.local ? static_cast<const int32_t*>(lds)[kLocalWords + r] : a.ori[t.row0 + r];
+    return static_cast<uint32_t>(p) / a.topk;
   }
 
   static __device__ __forceinline__ int64_t weight(const Args& a, const MTile& t) {
@@ -87,9 +103,11 @@ struct GluOp {
   }
 
   static __device__ __forceinline__ int64_t columns(const Args& a) { return a.F; }
-  static __device__ __forceinline__ int extra(const Args&) { return 0; }
+  static __host__ __device__ __forceinline__ int extra(const Args& a) { return a.local; }
   template <class T>
-  static __device__ __forceinline__ void extra_work(const Args&, int) {}
+  static __device__ __forceinline__ void extra_work(const Args& a, int, void* lds) {
+    prep_block(a.prep, a.eri, a.gl, a.ws, static_cast<long long*>(lds));
+  }
 
   template <class T, int B, class Acc, class Column>
   static __device__ __forceinline__ void adjust(const Args&, const MTile&, int, int, Acc&, Column) {}
@@ -160,7 +178,7 @@ hipError_t launch_16(const Plan& p, GluArgs a, void* padded_x, void* padded_w, h
   a.n_slots = p.max_tiles;
   a.n_col_tiles = static_cast<int32_t>((a.F + 127) / 128);
   if (p.regime == kStream)
-    return direct(p, a) ? launch_few<T, GluOp<ACT>, 32>(a, 0, p.ksplit, s)
+    return direct(p, a) ? launch_few<T, GluOp<ACT>, 32>(a, p.ksplit, s)
                         : launch_reg<T, 32, 256, 1, 4, 2, ACT>(p, a, s);
   GluArgs b = a;   // with the operands that the plan lays out anew
   if (p.pad_a) {
@@ -202,7 +220,7 @@ hipError_t launch_act(const Plan& p, const GluArgs& a, void* px, void* pw, hipSt
 }  // namespace
 
 hipError_t launch_glu(const Plan& p, int32_t act, const void* x, const void* weight, void* h, void* gate_up,
-                      void* ws, hipStream_t s) {
+                      const int64_t* eri, const int64_t* group_list, void* ws, hipStream_t s) {
   const WsView w = ws_view(p, ws);
   GluArgs a;
   a.A = x;
@@ -225,6 +243,11 @@ hipError_t launch_glu(const Plan& p, int32_t act, const void* x, const void* wei
   a.kspan = p.kspan;
   a.topk = static_cast<uint32_t>(p.topk);
   a.bm = p.bm;
+  a.local = p.local;
+  a.eri = eri;
+  a.gl = group_list;
+  a.prep = prep_args(p);
+  a.ws = w;
   void* px = static_cast<char*>(ws) + p.off_pad_a;
   void* pw = static_cast<char*>(ws) + p.off_pad_w;
   return act == PGG_ACT_SILU ? launch_act<PGG_ACT_SILU>(p, a, px, pw, s)

@@ -17,6 +17,7 @@
 #include <algorithm>
 
 #include "pgg_act.h"
+#include "pgg_local.h"
 #include "pgg_pipe.h"
 
 namespace pgg {
@@ -39,6 +40,11 @@ struct GluGradArgs {
   int64_t lda, ldw;         // row strides of A and W
   int32_t bm;               // rows of a table entry
   int32_t n_slots, n_col_tiles;
+  // without tables: group_list itself, and the preparation for the error word
+  int32_t local;
+  const int64_t* gl;
+  PrepArgs prep;
+  WsView ws;
 };
 
 template <int ACT>
@@ -47,7 +53,14 @@ struct GluGradOp {
   static constexpr bool kPaired = false;
 
   template <int BM>
-  static __device__ __forceinline__ bool tile(const Args& a, int slot, MTile& t) {
+  static __device__ __forceinline__ bool tile(const Args& a, int slot, MTile& t, void* lds) {
+    if constexpr (BM == 32) {
+      if (a.local) {
+        const bool found = local_tile(a.gl, a.prep.G, a.M, BM, slot, t, static_cast<int32_t*>(lds));
+        __syncthreads();   // before LDS is used again
+        return found;
+      }
+    }
     if (a.hdr->err != kNoError) return false;
     const int sub = a.bm / BM;   // tiles to a table entry
     const int entry = slot / sub;
@@ -60,7 +73,9 @@ struct GluGradOp {
   }
 
   static __device__ __forceinline__ int64_t src_base(const Args&, const MTile& t) { return t.row0; }
-  static __device__ __forceinline__ int64_t src(const Args&, const MTile& t, int r) { return int64_t(t.row0) + r; }
+  static __device__ __forceinline__ int64_t src(const Args&, const MTile& t, int r, const void*) {
+    return int64_t(t.row0) + r;
+  }
   static __device__ __forceinline__ int64_t weight(const Args& a, const MTile& t) { return t.g * a.F * a.ldw; }
   static __device__ __forceinline__ int64_t first_column(int ct, int bn) { return static_cast<int64_t>(ct) * bn; }
 
@@ -126,10 +141,19 @@ void glu_grad_reg_kernel(GluGradArgs a) {
   static_assert(A_CHUNKS % NT == 0 && B_CHUNKS % NT == 0, "a stage splits evenly");
   __shared__ u32x4_t lds[2][A_CHUNKS + B_CHUNKS];
 
+  if (BM == 32 && a.local && blockIdx.x == gridDim.x - 1) {   // the one workgroup that is no tile's
+    if (blockIdx.y == 0) {
+      long long* scratch = reinterpret_cast<long long*>(&lds[0][0]);
+      reset_header(a.ws.hdr);
+      __syncthreads();
+      groups_phase(a.prep, a.gl, a.ws, scratch, scratch + blockDim.x);
+    }
+    return;
+  }
   int slot, ct;
   if (!tile_place(a, slot, ct)) return;
   MTile tile;
-  if (!Op::template tile<BM>(a, slot, tile)) return;
+  if (!Op::template tile<BM>(a, slot, tile, lds)) return;
   tile.pad = blockIdx.y;
   const int64_t col0 = Op::first_column(ct, BN);
   const int64_t kbeg = static_cast<int64_t>(blockIdx.y) * a.kspan;   // this workgroup's split
@@ -146,7 +170,7 @@ void glu_grad_reg_kernel(GluGradArgs a) {
 #pragma unroll
   for (int s = 0; s < A_PER_T; ++s) {
     const int q = tid + s * NT;
-    arow[s] = static_cast<const E*>(a.A) + Op::src(a, tile, min(q / kChunks, tile.rows - 1)) * a.lda + kbeg + (q % kChunks) * EPC;
+    arow[s] = static_cast<const E*>(a.A) + Op::src(a, tile, min(q / kChunks, tile.rows - 1), nullptr) * a.lda + kbeg + (q % kChunks) * EPC;
   }
 #pragma unroll
   for (int s = 0; s < B_PER_T; ++s) {
@@ -235,7 +259,7 @@ hipError_t launch_reg(const Plan& p, GluGradArgs a, hipStream_t s) {
   constexpr int BN = 128;
   a.n_slots = p.max_tiles * (p.bm / BM);
   a.n_col_tiles = static_cast<int32_t>((a.F + BN - 1) / BN);
-  hipLaunchKernelGGL((glu_grad_reg_kernel<T, GluGradOp<ACT>, BM, BN, WM, 4 / WM, EU>), dim3(tile_blocks(a), p.ksplit), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((glu_grad_reg_kernel<T, GluGradOp<ACT>, BM, BN, WM, 4 / WM, EU>), dim3(tile_blocks(a) + (BM == 32 && a.local ? 1 : 0), p.ksplit), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -311,7 +335,7 @@ hipError_t launch_act(const Plan& p, const GluGradArgs& a, void* pa, void* pw, h
 }  // namespace
 
 hipError_t launch_glu_grad(const Plan& p, int32_t act, const void* grad_y, const void* weight, const void* gate_up,
-                           void* grad, void* h, void* ws, hipStream_t s) {
+                           const int64_t* group_list, void* grad, void* h, void* ws, hipStream_t s) {
   const WsView w = ws_view(p, ws);
   GluGradArgs a;
   a.A = grad_y;
@@ -332,6 +356,10 @@ hipError_t launch_glu_grad(const Plan& p, int32_t act, const void* grad_y, const
   a.part = p.ksplit > 1 ? w.ring : nullptr;
   a.lda = a.ldw = p.N;
   a.bm = p.bm;
+  a.local = p.local;
+  a.gl = group_list;
+  a.prep = prep_args(p);
+  a.ws = w;
   void* pa = static_cast<char*>(ws) + p.off_pad_a;
   void* pw = static_cast<char*>(ws) + p.off_pad_w;
   return act == PGG_ACT_SILU ? launch_act<PGG_ACT_SILU>(p, a, pa, pw, s)

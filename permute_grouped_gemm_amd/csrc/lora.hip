@@ -277,7 +277,7 @@ struct LoraOp {
   using Args = LoraArgs;
 
   template <int BM>
-  static __device__ __forceinline__ bool tile(const Args& a, int slot, MTile& t) {
+  static __device__ __forceinline__ bool tile(const Args& a, int slot, MTile& t, void*) {
     const int64_t row0 = static_cast<int64_t>(slot) * BM;
     t.g = 0;
     t.row0 = static_cast<int32_t>(row0);
@@ -286,7 +286,9 @@ struct LoraOp {
     return t.rows > 0;
   }
 
-  static __device__ __forceinline__ int64_t src(const Args&, const MTile& t, int r) { return int64_t(t.row0) + r; }
+  static __device__ __forceinline__ int64_t src(const Args&, const MTile& t, int r, const void*) {
+    return int64_t(t.row0) + r;
+  }
   static __device__ __forceinline__ int64_t weight(const Args&, const MTile&) { return 0; }
 
   static constexpr bool kPaired = false;
@@ -309,7 +311,7 @@ struct LoraOp {
   // few tokens: workgroups that compute z, and one that checks the ids
   static __host__ __device__ __forceinline__ int extra(const Args& a) { return a.few ? rank_blocks<1>(a.T, a.rank) + 1 : 0; }
   template <class T>
-  static __device__ __forceinline__ void extra_work(const Args& a, int i) {
+  static __device__ __forceinline__ void extra_work(const Args& a, int i, void*) {
     shrink_token<T, 1>(a, i);
   }
 
@@ -501,8 +503,7 @@ hipError_t launch_typed(const LoraPlan& p, LoraArgs a, void* padded_x, void* pad
   const bool direct = T::kPerChunk == 8 && direct_rows(a);
   hipError_t e = hipSuccess;
   // z: beside the product, token by token, or in tiles
-  if (a.few && !direct) e = launch_shrink_token<T, 1>(a, s);
-  else if (!a.few && a.T <= kTokenByToken) e = launch_shrink_token<T, 4>(a, s);
+  if (!a.few && a.T <= kTokenByToken) e = launch_shrink_token<T, 4>(a, s);
   else if (!a.few)
     e = a.rank <= 16 ? launch_shrink<T, 1>(a, s) : a.rank <= 32 ? launch_shrink<T, 2>(a, s) : launch_shrink<T, 4>(a, s);
   if (e != hipSuccess) return e;
@@ -510,8 +511,8 @@ hipError_t launch_typed(const LoraPlan& p, LoraArgs a, void* padded_x, void* pad
     a.n_col_tiles = static_cast<int32_t>((a.C + 255) / 256);
     if (a.few && direct) {
       a.n_slots = 1;
-      e = a.T <= 32 ? launch_few<T, LoraOp, 32>(a, LoraOp::extra(a), p.ksplit, s)
-                    : launch_few<T, LoraOp, 64>(a, LoraOp::extra(a), p.ksplit, s);
+      e = a.T <= 32 ? launch_few<T, LoraOp, 32>(a, p.ksplit, s)
+                    : launch_few<T, LoraOp, 64>(a, p.ksplit, s);
     } else if (a.few) {
       e = launch_reg<T, 32, 256, 1, 4>(a, p, s);
     } else {

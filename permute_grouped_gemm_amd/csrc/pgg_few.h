@@ -41,14 +41,14 @@ void few_kernel(typename Op::Args a, int32_t ksplit) {
   int bid = blockIdx.x;
   const int extra = Op::extra(a);
   if (bid < extra) {
-    Op::template extra_work<T>(a, bid);
+    Op::template extra_work<T>(a, bid, lds);
     return;
   }
   bid -= extra;
   const int ct = bid % a.n_col_tiles;
   const int split = bid / a.n_col_tiles % ksplit;
   MTile tile;
-  if (!Op::template tile<BM>(a, bid / a.n_col_tiles / ksplit, tile)) return;
+  if (!Op::template tile<BM>(a, bid / a.n_col_tiles / ksplit, tile, lds)) return;
   tile.pad = split;
   const int64_t R = a.R, lda = a.lda, ldw = a.ldw;
   const int64_t kbeg = static_cast<int64_t>(split) * a.kspan;
@@ -64,7 +64,7 @@ void few_kernel(typename Op::Args a, int32_t ksplit) {
   const int chunk = (lane & 3) ^ ((ar >> 2) & 3);
   const int64_t row_base = Op::src_base(a, tile);
   const char* pa = reinterpret_cast<const char*>(static_cast<const E*>(a.A) + row_base * lda + kbeg);
-  const uint32_t oa = static_cast<uint32_t>((Op::src(a, tile, min(ar, tile.rows - 1)) - row_base) * lda * 2) + chunk * 16;
+  const uint32_t oa = static_cast<uint32_t>((Op::src(a, tile, min(ar, tile.rows - 1), lds) - row_base) * lda * 2) + chunk * 16;
   // W: load u of run j, 4 rows of k
   const char* pb = reinterpret_cast<const char*>(static_cast<const E*>(a.W) + Op::weight(a, tile) + kbeg * ldw);
   const int n = ((((lane & 15) >> 2) ^ lg) << 5) | (((lane & 3) ^ (wave & 2)) << 3);
@@ -76,6 +76,7 @@ void few_kernel(typename Op::Args a, int32_t ksplit) {
       ob[j][u] = static_cast<uint32_t>(((16 * u + 4 * wave + lg) * ldw + Op::half_column(a, ct, j, n)) * 2);
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(lds));
   const void* zero = &kZero16;
+  __syncthreads();   // the rows have been read from LDS
 
   auto load = [&](int kt, int slot) {
     const uint32_t m0 = lds0 + slot * kStageBytes;
@@ -130,8 +131,9 @@ void few_kernel(typename Op::Args a, int32_t ksplit) {
 }
 
 template <class T, class Op, int BM>
-hipError_t launch_few(const typename Op::Args& a, int32_t extra, int32_t ksplit, hipStream_t s) {
-  const unsigned blocks = static_cast<unsigned>(extra) + static_cast<unsigned>(a.n_slots) * a.n_col_tiles * ksplit;
+hipError_t launch_few(const typename Op::Args& a, int32_t ksplit, hipStream_t s) {
+  const unsigned blocks =
+      static_cast<unsigned>(Op::extra(a)) + static_cast<unsigned>(a.n_slots) * a.n_col_tiles * ksplit;
   hipLaunchKernelGGL((few_kernel<T, Op, BM>), dim3(blocks), dim3(256), 0, s, a, ksplit);
   return hipGetLastError();
 }

@@ -68,6 +68,7 @@ struct Plan {
   bool stream_weights;
   // gated products: operands copied to padded rows of lda / ldw elements first
   bool pad_a, pad_w;
+  bool local;           // and find their tiles themselves, without a preparation launch
   int64_t lda, ldw;
   size_t off_pad_a, off_pad_w;
   // layout (byte offsets into the workspace)
@@ -198,12 +199,14 @@ hipError_t launch_gate_grad(const pgg_moe_gate_desc& d, const void* logits, cons
 // Gated product of the experts: the forward's plan (N = reduction, K = 2F
 // columns) and tables; the gradient's plan has N = reduction D, K = F columns
 // and only the group tables.
+// (Few groups, and where a routing index is searched few rows: pgg_local.h.)
+constexpr int64_t kLocalGroups = 256, kLocalRows = 4096;
 pgg_status make_glu_plan(const pgg_moe_glu_desc* desc, Plan* plan);
 hipError_t launch_glu(const Plan& p, int32_t act, const void* x, const void* weight, void* h, void* gate_up,
-                      void* ws, hipStream_t s);
+                      const int64_t* eri, const int64_t* group_list, void* ws, hipStream_t s);
 pgg_status make_glu_grad_plan(const pgg_moe_glu_grad_desc* desc, Plan* plan);
 hipError_t launch_glu_grad(const Plan& p, int32_t act, const void* grad_y, const void* weight, const void* gate_up,
-                           void* grad, void* h, void* ws, hipStream_t s);
+                           const int64_t* group_list, void* grad, void* h, void* ws, hipStream_t s);
 // rows x len 16-bit elements to rows of `pitch` (a multiple of 8), zeros after len.
 hipError_t launch_pad_rows(const void* src, void* dst, int64_t rows, int64_t len, int64_t pitch, hipStream_t s);
 

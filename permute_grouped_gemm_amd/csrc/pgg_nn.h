@@ -9,9 +9,12 @@
 //                            W_end) and their row strides (lda, ldw), R (the
 //                            reduction), n_slots, n_col_tiles, and kspan
 //                            (reduction elements of one split)
-//   Op::tile<BM>(args, slot, t)  rows [t.row0, t.row0 + t.rows) of group t.g; false:
-//                            no tile.  (The kernels put the split into t.pad.)
-//   Op::src(args, t, r)      row of A that tile row r reads
+//   Op::tile<BM>(args, slot, t, lds)  rows [t.row0, t.row0 + t.rows) of group t.g;
+//                            false: no tile.  (The kernels put the split into
+//                            t.pad.)  It may leave something in LDS for
+//   Op::src(args, t, r, lds) row of A that tile row r reads
+//   Op::extra(args), Op::extra_work<T>(args, i, lds)  workgroups in front of those
+//                            of tiles of few rows, and what they do
 //   Op::weight(args, t)      first element of the tile's W
 //   Op::column<BN>(args, ct, n)  column of W at column n (a multiple of 4) of
 //                            the tile, and how many of W's columns follow in that run
@@ -285,14 +288,21 @@ void nn_reg_kernel(typename Op::Args a) {
 
   int slot, ct;
   if constexpr (BM == 32) {   // few rows: columns fastest, whatever the number of tiles
-    ct = blockIdx.x % a.n_col_tiles;
-    slot = blockIdx.x / a.n_col_tiles;
+    int bid = blockIdx.x;
+    const int extra = Op::extra(a);
+    if (bid < extra) {
+      if (blockIdx.y == 0) Op::template extra_work<T>(a, bid, lds);
+      return;
+    }
+    bid -= extra;
+    ct = bid % a.n_col_tiles;
+    slot = bid / a.n_col_tiles;
     if (slot >= a.n_slots) return;
   } else {
     if (!tile_place(a, slot, ct)) return;
   }
   MTile tile;
-  if (!Op::template tile<BM>(a, slot, tile)) return;
+  if (!Op::template tile<BM>(a, slot, tile, lds)) return;
   tile.pad = blockIdx.y;
   const int rows = tile.rows;
   const int64_t ldw = a.ldw;
@@ -309,7 +319,7 @@ void nn_reg_kernel(typename Op::Args a) {
 #pragma unroll
   for (int s = 0; s < A_PER_T; ++s) {
     const int q = tid + s * NT;
-    arow[s] = static_cast<const E*>(a.A) + Op::src(a, tile, min(q / kChunks, rows - 1)) * a.lda + (q % kChunks) * EPC;
+    arow[s] = static_cast<const E*>(a.A) + Op::src(a, tile, min(q / kChunks, rows - 1), lds) * a.lda + (q % kChunks) * EPC;
   }
   // Columns past the matrix are not stored, so a chunk may hold anything there:
   // it is read whole, from the row's end on into the next row, and a chunk
@@ -344,6 +354,7 @@ void nn_reg_kernel(typename Op::Args a) {
       }
     }
   };
+  if constexpr (BM == 32) __syncthreads();   // the rows have been read from LDS
   auto store_stage = [&](int buf) {
 #pragma unroll
     for (int s = 0; s < A_PER_T; ++s) {
@@ -406,7 +417,8 @@ void nn_reg_kernel(typename Op::Args a) {
 
 template <class T, class Op, int BM, int BN, int WM, int WN, int EU>
 hipError_t launch_nn_reg(const typename Op::Args& a, int ksplit, hipStream_t s) {
-  const unsigned tiles = BM == 32 ? static_cast<unsigned>(a.n_slots) * a.n_col_tiles : tile_blocks(a);
+  const unsigned tiles =
+      BM == 32 ? static_cast<unsigned>(Op::extra(a)) + static_cast<unsigned>(a.n_slots) * a.n_col_tiles : tile_blocks(a);
   hipLaunchKernelGGL((nn_reg_kernel<T, Op, BM, BN, WM, WN, EU>), dim3(tiles, static_cast<unsigned>(ksplit)),
                      dim3(WM * WN * 64), 0, s, a);
   return hipGetLastError();

@@ -176,7 +176,7 @@ void pipe_kernel(typename Op::Args a) {
   int slot, ct;
   if (!tile_place(a, slot, ct)) return;
   MTile tile;
-  if (!Op::template tile<256>(a, slot, tile)) return;
+  if (!Op::template tile<256>(a, slot, tile, lds)) return;
   tile.pad = blockIdx.y;
   // this workgroup's split of the reduction
   const int64_t R = a.R, lda = a.lda, ldw = a.ldw;
@@ -203,7 +203,7 @@ void pipe_kernel(typename Op::Args a) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int r = min(128 * u + 64 * h + 8 * wave + l8, tile.rows - 1);
-      oa[h][u] = static_cast<uint32_t>((Op::src(a, tile, r) - row_base) * lda * 2) + chunk * 16;
+      oa[h][u] = static_cast<uint32_t>((Op::src(a, tile, r, lds) - row_base) * lda * 2) + chunk * 16;
     }
   // Load u of quarter B_j.  NT: 8 columns' rows, as for A.  Otherwise 4 rows of
   // k, 256 bytes each, whose 16-byte chunks sit where quarter_offset puts them.

@@ -564,6 +564,8 @@ pgg_status make_glu_plan(const pgg_moe_glu_desc* d, Plan* p) {
   const int64_t busy = std::min<int64_t>(p->max_tiles, p->M / p->bm + (p->G + 1) / 2 + 1) * p->n_col_tiles;
   split_reduction(p->N, busy, p->regime == kStream ? 512 : cus,
                   p->regime != kStream ? 256 : p->dtype == PGG_F32 ? 32 : 128, &p->ksplit, &p->kspan);
+  // few groups and rows: every workgroup finds its own tile (pgg_local.h)
+  p->local = p->regime == kStream && p->G <= kLocalGroups && p->M <= kLocalRows;
   p->tc = p->max_tiles;
   size_t off = p->off_tiles;
   off = align_up(off + sizeof(MTile) * size_t(p->max_tiles), kRegionAlign);
@@ -625,6 +627,7 @@ pgg_status make_glu_grad_plan(const pgg_moe_glu_grad_desc* d, Plan* p) {
   q.n_col_tiles = static_cast<int32_t>(col_tiles);
   // Where tiles alone do not fill the chip (one 256 x 256 tile, two of 128 x
   // 128 or four of 32 x 128 per compute unit), the reduction is split.
+  q.local = q.bm == 32 && G <= kLocalGroups;   // few groups: every workgroup finds its own tile (pgg_local.h)
   const int64_t busy_cols = q.bm == 256 ? (F + 255) / 256 : col_tiles;
   const int64_t busy = std::min<int64_t>(max_tiles, M / q.bm + (G + 1) / 2 + 1) * busy_cols;
   split_reduction(D, busy, q.bm == 256 ? 256 : q.bm == 128 ? 512 : 1024, q.bm == 32 ? 128 : 256, &q.ksplit, &q.kspan);

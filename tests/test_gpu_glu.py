@@ -49,7 +49,8 @@ def _run(x, w, eri, gl, topk, row_idx_type, act, save=True):
 GLU = [(1, 1, 1, 1, 1), (1, 2, 4, 64, 32), (5, 2, 3, 33, 7), (16, 8, 16, 2048, 128), (17, 3, 5, 1000, 72),
        (64, 2, 4, 256, 64), (100, 4, 6, 520, 200), (257, 2, 3, 129, 65), (400, 2, 2, 328, 136),
        (300, 1, 1, 200, 264), (200, 1, 1, 40, 24), (520, 1, 2, 64, 8), (260, 1, 1, 136, 520),
-       (600, 1, 1, 67, 35), (600, 1, 1, 72, 35), (600, 1, 1, 67, 40), (90, 1, 1, 67, 40)]
+       (600, 1, 1, 67, 35), (600, 1, 1, 72, 35), (600, 1, 1, 67, 40), (90, 1, 1, 67, 40),
+       (8, 2, 256, 40, 8), (8, 2, 257, 40, 8), (512, 8, 100, 16, 8), (513, 8, 100, 24, 7)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
@@ -118,7 +119,8 @@ def test_extreme_gates():
 @pytest.mark.parametrize("batch,topk,G,D,F", [(1, 1, 1, 1, 1), (1, 2, 4, 64, 32), (5, 2, 3, 33, 7), (40, 2, 5, 200, 136),
                                               (333, 2, 7, 203, 141), (300, 1, 1, 264, 200), (257, 2, 2, 520, 264),
                                               (600, 2, 3, 192, 320), (200, 1, 1, 40, 24), (520, 1, 2, 64, 8),
-                                              (600, 1, 1, 67, 35), (1100, 1, 2, 135, 130)])
+                                              (600, 1, 1, 67, 35), (1100, 1, 2, 135, 130), (8, 2, 256, 40, 8),
+                                              (8, 2, 257, 300, 8)])
 def test_glu_grad(batch, topk, G, D, F, dtype):
     _, gl = _routing(batch, topk, G, D + F, 0, 1.0, min(1, G - topk))
     gen = torch.Generator().manual_seed(D)
@@ -197,21 +199,38 @@ def test_operands_at_any_address(batch, topk, G, K, F, dtype):
     ref.assert_within(hh, wh, eh, "h")
 
 
-def test_wrong_routing_sets_the_error_word():
-    x, w, eri, gl = _make(20, 2, 4, 64, 32, "bf16", 6)
+@pytest.mark.parametrize("row_idx_type", [0, 1])
+@pytest.mark.parametrize("batch,G", [(20, 4), (20, 300), (700, 4)])
+def test_wrong_routing_sets_the_error_word(batch, G, row_idx_type):
+    # few rows with few and many groups, and many rows
+    x, w, eri, gl = _make(batch, 2, G, 64, 32, "bf16", 6, row_idx_type)
     args = [t.to(DEV) for t in (x, w)]
-    for bad_eri, bad_gl, code in ((eri, gl + torch.tensor([0, 1, 0, 0]), pgg.DEV_GROUP_SUM),
-                                  (eri, gl - torch.tensor([0, 1000, 0, 0]), pgg.DEV_GROUP_NEGATIVE),
-                                  (eri.clone().index_fill_(0, torch.tensor([5]), 40), gl, pgg.DEV_INDEX_RANGE),
-                                  (eri.clone().index_fill_(0, torch.tensor([5, 6]), 7), gl, pgg.DEV_INDEX_DUP)):
-        ws = torch.empty(pgg.glu_workspace_size(*args, eri.to(DEV), gl.to(DEV), 2), dtype=torch.uint8, device=DEV)
-        pgg.moe_glu(*args, bad_eri.to(DEV), bad_gl.to(DEV), 2, workspace=ws)
+    one = torch.zeros_like(gl)
+    one[1] = 1
+    for bad_eri, bad_gl, code in ((eri, gl + one, pgg.DEV_GROUP_SUM), (eri, gl - 100000 * one, pgg.DEV_GROUP_NEGATIVE),
+                                  (eri, gl + (1 << 40) * one, pgg.DEV_GROUP_SUM),
+                                  (eri.clone().index_fill_(0, torch.tensor([5]), 2 * batch), gl, pgg.DEV_INDEX_RANGE),
+                                  (eri.clone().index_fill_(0, torch.tensor([5]), -1), gl, pgg.DEV_INDEX_RANGE),
+                                  (eri.clone().index_fill_(0, torch.tensor([5, 6]), 7), gl, pgg.DEV_INDEX_DUP),
+                                  (eri, gl, pgg.DEV_OK)):
+        ws = torch.empty(pgg.glu_workspace_size(*args, eri.to(DEV), gl.to(DEV), 2, row_idx_type), dtype=torch.uint8,
+                         device=DEV)
+        pgg.moe_glu(*args, bad_eri.to(DEV), bad_gl.to(DEV), 2, row_idx_type, workspace=ws)
         assert pgg.read_device_error(ws)[0] == code
-    gy, gu = torch.zeros((40, 16), device=DEV), torch.zeros((40, 16), device=DEV)
-    w2 = torch.zeros((4, 8, 16), device=DEV)
+
+
+@pytest.mark.parametrize("M,G", [(40, 4), (40, 300), (700, 4)])
+def test_wrong_counts_set_the_gradients_error_word(M, G):
+    gl = torch.zeros(G, dtype=torch.int64)
+    gl[1], gl[3] = M // 2, M - M // 2
+    gy, gu = torch.zeros((M, 16), device=DEV), torch.zeros((M, 16), device=DEV)
+    w2 = torch.zeros((G, 8, 16), device=DEV)
     ws = torch.empty(pgg.glu_grad_workspace_size(gy, w2, gu, gl.to(DEV)), dtype=torch.uint8, device=DEV)
-    pgg.moe_glu_grad(gy, w2, gu, (gl + 1).to(DEV), workspace=ws)
-    assert pgg.read_device_error(ws) == (pgg.DEV_GROUP_SUM, 44)
+    for at, by, want in ((1, 4, (pgg.DEV_GROUP_SUM, M + 4)), (3, -M, (pgg.DEV_GROUP_NEGATIVE, 3)), (0, 0, (pgg.DEV_OK, 0))):
+        bad = gl.clone()
+        bad[at] += by
+        pgg.moe_glu_grad(gy, w2, gu, bad.to(DEV), workspace=ws)
+        assert pgg.read_device_error(ws) == want
 
 
 def test_glu_captures_into_a_graph():
