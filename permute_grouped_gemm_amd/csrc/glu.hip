@@ -59,7 +59,7 @@ struct GluOp {
 
   template <int BM>
   static __device__ __forceinline__ bool tile(const Args& a, int slot, MTile& t, void* lds) {
-    if constexpr (BM == 32) {
+    if constexpr (BM <= 64) {
       if (a.local) {
         int32_t* words = static_cast<int32_t*>(lds);
         if (!local_tile(a.gl, a.prep.G, a.M, BM, slot, t, words)) return false;
@@ -177,9 +177,10 @@ template <class T, int ACT>
 hipError_t launch_16(const Plan& p, GluArgs a, void* padded_x, void* padded_w, hipStream_t s) {
   a.n_slots = p.max_tiles;
   a.n_col_tiles = static_cast<int32_t>((a.F + 127) / 128);
-  if (p.regime == kStream)
-    return direct(p, a) ? launch_few<T, GluOp<ACT>, 32>(a, p.ksplit, s)
-                        : launch_reg<T, 32, 256, 1, 4, 2, ACT>(p, a, s);
+  if (p.regime == kStream) {
+    if (!direct(p, a)) return launch_reg<T, 32, 256, 1, 4, 2, ACT>(p, a, s);
+    return p.bm == 32 ? launch_few<T, GluOp<ACT>, 32>(a, p.ksplit, s) : launch_few<T, GluOp<ACT>, 64>(a, p.ksplit, s);
+  }
   GluArgs b = a;   // with the operands that the plan lays out anew
   if (p.pad_a) {
     b.A = padded_x;

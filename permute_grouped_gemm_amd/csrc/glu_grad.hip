@@ -54,7 +54,7 @@ struct GluGradOp {
 
   template <int BM>
   static __device__ __forceinline__ bool tile(const Args& a, int slot, MTile& t, void* lds) {
-    if constexpr (BM == 32) {
+    if constexpr (BM <= 64) {
       if (a.local) {
         const bool found = local_tile(a.gl, a.prep.G, a.M, BM, slot, t, static_cast<int32_t*>(lds));
         __syncthreads();   // before LDS is used again
@@ -141,7 +141,7 @@ void glu_grad_reg_kernel(GluGradArgs a) {
   static_assert(A_CHUNKS % NT == 0 && B_CHUNKS % NT == 0, "a stage splits evenly");
   __shared__ u32x4_t lds[2][A_CHUNKS + B_CHUNKS];
 
-  if (BM == 32 && a.local && blockIdx.x == gridDim.x - 1) {   // the one workgroup that is no tile's
+  if (BM <= 64 && a.local && blockIdx.x == gridDim.x - 1) {   // the one workgroup that is no tile's
     if (blockIdx.y == 0) {
       long long* scratch = reinterpret_cast<long long*>(&lds[0][0]);
       reset_header(a.ws.hdr);
@@ -259,7 +259,7 @@ hipError_t launch_reg(const Plan& p, GluGradArgs a, hipStream_t s) {
   constexpr int BN = 128;
   a.n_slots = p.max_tiles * (p.bm / BM);
   a.n_col_tiles = static_cast<int32_t>((a.F + BN - 1) / BN);
-  hipLaunchKernelGGL((glu_grad_reg_kernel<T, GluGradOp<ACT>, BM, BN, WM, 4 / WM, EU>), dim3(tile_blocks(a) + (BM == 32 && a.local ? 1 : 0), p.ksplit), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((glu_grad_reg_kernel<T, GluGradOp<ACT>, BM, BN, WM, 4 / WM, EU>), dim3(tile_blocks(a) + (BM <= 64 && a.local ? 1 : 0), p.ksplit), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -273,6 +273,7 @@ bool direct(const GluGradArgs& a) {
 template <class T, int ACT>
 hipError_t launch_typed(const Plan& p, GluGradArgs a, void* padded_a, void* padded_w, hipStream_t s) {
   if (p.bm == 32) return launch_reg<T, 32, 1, 4, ACT>(p, a, s);
+  if (p.bm == 64) return launch_reg<T, 64, 2, 3, ACT>(p, a, s);
   if constexpr (T::kPerChunk == 8) {
     GluGradArgs b = a;   // with the operands that the plan lays out anew
     if (p.pad_a) {

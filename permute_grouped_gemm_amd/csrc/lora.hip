@@ -260,12 +260,14 @@ __global__ __launch_bounds__(256) void lora_shrink_token_kernel(LoraArgs a) {
 
 // ---------------------------------------------------------------- the shared product
 
-// 8 fp32 values as two bf16 parts.
+// 8 fp32 values as two bf16 parts.  The first part of a finite value is finite:
+// the rest is at most 2^-8 of the value there too.
 __device__ __forceinline__ void split_bf16(const float (&v)[8], u32x4_t& hi, u32x4_t& lo) {
   uint16_t h[8], l[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    h[e] = from_float<TBf16>(v[e]);
+    constexpr float kMost = 0x1.fep127f;   // bf16's largest
+    h[e] = from_float<TBf16>(fabsf(v[e]) < INFINITY ? __builtin_amdgcn_fmed3f(v[e], -kMost, kMost) : v[e]);
     const float rest = v[e] - to_float<TBf16>(h[e]);
     l[e] = rest == rest ? from_float<TBf16>(rest) : 0;   // an infinite value has no rest
   }
@@ -510,9 +512,8 @@ hipError_t launch_typed(const LoraPlan& p, LoraArgs a, void* padded_x, void* pad
   if constexpr (T::kPerChunk == 8) {
     a.n_col_tiles = static_cast<int32_t>((a.C + 255) / 256);
     if (a.few && direct) {
-      a.n_slots = 1;
-      e = a.T <= 32 ? launch_few<T, LoraOp, 32>(a, p.ksplit, s)
-                    : launch_few<T, LoraOp, 64>(a, p.ksplit, s);
+      a.n_slots = static_cast<int32_t>((a.T + 63) / 64);
+      e = a.T <= 32 ? launch_few<T, LoraOp, 32>(a, p.ksplit, s) : launch_few<T, LoraOp, 64>(a, p.ksplit, s);
     } else if (a.few) {
       e = launch_reg<T, 32, 256, 1, 4>(a, p, s);
     } else {

@@ -287,7 +287,7 @@ void nn_reg_kernel(typename Op::Args a) {
   __shared__ u32x4_t lds[2][A_CHUNKS + B_CHUNKS];
 
   int slot, ct;
-  if constexpr (BM == 32) {   // few rows: columns fastest, whatever the number of tiles
+  if constexpr (BM <= 64) {   // few rows: columns fastest, whatever the number of tiles
     int bid = blockIdx.x;
     const int extra = Op::extra(a);
     if (bid < extra) {
@@ -354,7 +354,7 @@ void nn_reg_kernel(typename Op::Args a) {
       }
     }
   };
-  if constexpr (BM == 32) __syncthreads();   // the rows have been read from LDS
+  if constexpr (BM <= 64) __syncthreads();   // the rows have been read from LDS
   auto store_stage = [&](int buf) {
 #pragma unroll
     for (int s = 0; s < A_PER_T; ++s) {
@@ -411,14 +411,14 @@ void nn_reg_kernel(typename Op::Args a) {
     if (kt + 1 < nk) store_stage((kt & 1) ^ 1);
     __syncthreads();
   }
-  store_blocks<T, Op, (BM > 32), FM, FN>(a, tile, Op::first_column(ct, BN) + wn * (Op::kPaired ? WTN / 2 : WTN), wm * WTM, lane,
+  store_blocks<T, Op, (BM > 64), FM, FN>(a, tile, Op::first_column(ct, BN) + wn * (Op::kPaired ? WTN / 2 : WTN), wm * WTM, lane,
                               acc);
 }
 
 template <class T, class Op, int BM, int BN, int WM, int WN, int EU>
 hipError_t launch_nn_reg(const typename Op::Args& a, int ksplit, hipStream_t s) {
   const unsigned tiles =
-      BM == 32 ? static_cast<unsigned>(Op::extra(a)) + static_cast<unsigned>(a.n_slots) * a.n_col_tiles : tile_blocks(a);
+      BM <= 64 ? static_cast<unsigned>(Op::extra(a)) + static_cast<unsigned>(a.n_slots) * a.n_col_tiles : tile_blocks(a);
   hipLaunchKernelGGL((nn_reg_kernel<T, Op, BM, BN, WM, WN, EU>), dim3(tiles, static_cast<unsigned>(ksplit)),
                      dim3(WM * WN * 64), 0, s, a);
   return hipGetLastError();

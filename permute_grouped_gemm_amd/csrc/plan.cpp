@@ -549,15 +549,22 @@ pgg_status make_glu_plan(const pgg_moe_glu_desc* d, Plan* p) {
   // times as many as the plan's; a launch holds fewer than 2^32 lanes
   if (int64_t(p->max_tiles) * p->n_col_tiles >= (int64_t(1) << 21)) return PGG_ERR_UNSUPPORTED;
   p->fused_prep = p->M <= 1024;
-  // Few rows per expert: m-tiles of 32 rows x 256 columns (128 of h), two
+  // Few rows per expert: m-tiles of 32 or 64 rows x 256 columns (128 of h), two
   // workgroups per compute unit; otherwise one of the large tiles, or two of
   // 128 x 128.  Where tiles alone do not fill the chip, the reduction is split.
+  // An expert of more rows than a tile reads its weights again, and the tiles of
+  // 64 rows have to be direct-to-LDS ones.  Measured in us, 32 and 64 rows:
+  //   bf16, 16 experts, N 4096, K 2048: 24 rows per expert 99, 99; 32 142, 101;
+  //     48 156, 107; 60 186, 149
+  //   N 4095, K 2047: 24 126, 150; 32 172, 151; 48 163, 155; 60 239, 247
+  //   f32, N 2048, K 1408: 24 95, 173; 32 121, 175; 48 168, 175; 60 170, 178
   const int64_t cus = p->regime == kLarge ? 256 : 512;
   if (p->M <= 64 * p->G) {
     p->regime = kStream;
-    p->bm = 32;
+    const bool rows16 = p->dtype != PGG_F32 && p->N % 8 == 0 && p->K % 16 == 0;
+    p->bm = !rows16 || p->M <= 24 * p->G ? 32 : 64;
     p->bn = 256;
-    p->max_tiles = static_cast<int32_t>((p->M + 31) / 32 + p->G);
+    p->max_tiles = static_cast<int32_t>((p->M + p->bm - 1) / p->bm + p->G);
     p->n_col_tiles = static_cast<int32_t>((p->K + 255) / 256);
   }
   p->max_tiles = static_cast<int32_t>(std::min<int64_t>(p->max_tiles, p->M));   // each holds a row at least
@@ -614,7 +621,12 @@ pgg_status make_glu_grad_plan(const pgg_moe_glu_grad_desc* d, Plan* p) {
   q.panel_cols = F;
   q.dtype = d->grad_y_dtype;
   q.regime = q.dtype == PGG_F32 ? kF32 : kLarge;
-  q.bm = M <= 64 * G ? 32 : q.dtype == PGG_F32 ? 128 : 256;
+  // m-tiles of 32 rows, 64 (16 bits) or the large ones.  Measured in us, 32 and
+  // 64 rows, 16 experts, F 1408:
+  //   bf16, D 4096: 24 rows per expert 60, 58; 32 58, 63; 48 70, 55; 60 86, 72
+  //   D 4095: 24 77, 72; 32 79, 85; 48 104, 81; 60 112, 94
+  //   f32, D 2048: 32 70, 101; 48 98, 92; 60 101, 115
+  q.bm = M <= (q.dtype == PGG_F32 ? 64 : 40) * G ? 32 : M <= 64 * G ? 64 : q.dtype == PGG_F32 ? 128 : 256;
   q.bn = 128;
   const int64_t max_tiles = std::min<int64_t>(M, (M + q.bm - 1) / q.bm + G);   // each holds a row at least
   const int64_t col_tiles = (F + q.bn - 1) / q.bn;
@@ -626,11 +638,12 @@ pgg_status make_glu_grad_plan(const pgg_moe_glu_grad_desc* d, Plan* p) {
   q.n_panels = 1;
   q.n_col_tiles = static_cast<int32_t>(col_tiles);
   // Where tiles alone do not fill the chip (one 256 x 256 tile, two of 128 x
-  // 128 or four of 32 x 128 per compute unit), the reduction is split.
-  q.local = q.bm == 32 && G <= kLocalGroups;   // few groups: every workgroup finds its own tile (pgg_local.h)
+  // 128, three of 64 x 128 or four of 32 x 128 per compute unit), the reduction is split.
+  q.local = q.bm <= 64 && G <= kLocalGroups;   // few groups: every workgroup finds its own tile (pgg_local.h)
   const int64_t busy_cols = q.bm == 256 ? (F + 255) / 256 : col_tiles;
   const int64_t busy = std::min<int64_t>(max_tiles, M / q.bm + (G + 1) / 2 + 1) * busy_cols;
-  split_reduction(D, busy, q.bm == 256 ? 256 : q.bm == 128 ? 512 : 1024, q.bm == 32 ? 128 : 256, &q.ksplit, &q.kspan);
+  const int64_t fill = q.bm == 256 ? 256 : q.bm == 128 ? 512 : q.bm == 64 ? 768 : 1024;
+  split_reduction(D, busy, fill, q.bm <= 64 ? 128 : 256, &q.ksplit, &q.kspan);
   size_t off = 0;
   q.off_header = off;   off = align_up(off + sizeof(WsHeader), kRegionAlign);
   q.off_offsets = off;  off = align_up(off + sizeof(int64_t) * size_t(G + 1), kRegionAlign);
@@ -671,11 +684,17 @@ pgg_status make_lora_plan(const pgg_lora_desc* d, LoraPlan* p) {
   const bool f32 = q.dtype == PGG_F32;
   auto tiles = [&](int64_t bm, int64_t bn) { return ((q.T + bm - 1) / bm) * ((q.N + bn - 1) / bn); };
   if (tiles(32, 128) >= (int64_t(1) << 23)) return PGG_ERR_UNSUPPORTED;   // launches of fewer than 2^32 lanes
-  // Up to 64 tokens the projection is bound by reading W: one tile of rows, the
-  // reduction split over about 512 workgroups, two per compute unit.  Above
+  // With few tokens the projection is bound by reading W: tiles of 32 or 64 rows,
+  // the reduction split over about 512 workgroups, two per compute unit.  Above
   // that, the 256 x 256 tiles (one workgroup per compute unit) or the 128 x 128
-  // ones (two), split where there are too few of them.
-  q.few = q.T <= 64;
+  // ones (two), split where there are too few of them.  Measured in us, 96, 128,
+  // 192 and 256 tokens, the large tiles and the small ones:
+  //   bf16, 4096 x 4096: 34, 31; 36, 34; 42, 43; 47, 46
+  //   4096 x 192:        24, 15; 24, 16; 27, 17; 29, 21
+  //   4095 x 4095:       38, 34; 42, 42; 45, 47; 50, 57
+  //   3977 x 190:        22, 17; 23, 19; 25, 23; 25, 28
+  //   f32, 2048 x 1408:  38, 24; 38, 29; 40, 36; 41, 39
+  q.few = q.T <= (f32 || (q.K % 8 == 0 && q.N % 8 == 0) ? 256 : 128);
   q.lda = q.K;
   q.ldw = q.N;
   const bool w_pays = q.N % 8 == 0 || q.T >= kPadRowsLora;

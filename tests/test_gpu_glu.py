@@ -50,7 +50,8 @@ GLU = [(1, 1, 1, 1, 1), (1, 2, 4, 64, 32), (5, 2, 3, 33, 7), (16, 8, 16, 2048, 1
        (64, 2, 4, 256, 64), (100, 4, 6, 520, 200), (257, 2, 3, 129, 65), (400, 2, 2, 328, 136),
        (300, 1, 1, 200, 264), (200, 1, 1, 40, 24), (520, 1, 2, 64, 8), (260, 1, 1, 136, 520),
        (600, 1, 1, 67, 35), (600, 1, 1, 72, 35), (600, 1, 1, 67, 40), (90, 1, 1, 67, 40),
-       (8, 2, 256, 40, 8), (8, 2, 257, 40, 8), (512, 8, 100, 16, 8), (513, 8, 100, 24, 7)]
+       (8, 2, 256, 40, 8), (8, 2, 257, 40, 8), (512, 8, 100, 16, 8), (513, 8, 100, 24, 7),
+       (60, 4, 5, 520, 200), (100, 2, 5, 67, 40), (1200, 8, 300, 24, 8), (41, 2, 2, 1024, 136)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
@@ -120,7 +121,8 @@ def test_extreme_gates():
                                               (333, 2, 7, 203, 141), (300, 1, 1, 264, 200), (257, 2, 2, 520, 264),
                                               (600, 2, 3, 192, 320), (200, 1, 1, 40, 24), (520, 1, 2, 64, 8),
                                               (600, 1, 1, 67, 35), (1100, 1, 2, 135, 130), (8, 2, 256, 40, 8),
-                                              (8, 2, 257, 300, 8)])
+                                              (8, 2, 257, 300, 8), (125, 2, 5, 203, 35), (120, 2, 5, 520, 264),
+                                              (1800, 8, 300, 40, 8)])
 def test_glu_grad(batch, topk, G, D, F, dtype):
     _, gl = _routing(batch, topk, G, D + F, 0, 1.0, min(1, G - topk))
     gen = torch.Generator().manual_seed(D)
@@ -181,7 +183,8 @@ def _moved(t):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("batch,topk,G,K,F", [(16, 4, 8, 128, 64), (300, 2, 2, 128, 64), (600, 1, 1, 72, 40)])
+@pytest.mark.parametrize("batch,topk,G,K,F", [(16, 4, 8, 128, 64), (60, 4, 5, 128, 64), (300, 2, 2, 128, 64),
+                                              (600, 1, 1, 72, 40)])
 def test_operands_at_any_address(batch, topk, G, K, F, dtype):
     x, w, eri, gl = _make(batch, topk, G, K, F, dtype, 31)
     wh, eh, wy, ey = ref.glu(x, w, eri, gl, topk, 0, "silu")
@@ -200,7 +203,7 @@ def test_operands_at_any_address(batch, topk, G, K, F, dtype):
 
 
 @pytest.mark.parametrize("row_idx_type", [0, 1])
-@pytest.mark.parametrize("batch,G", [(20, 4), (20, 300), (700, 4)])
+@pytest.mark.parametrize("batch,G", [(20, 4), (80, 4), (20, 300), (700, 4)])
 def test_wrong_routing_sets_the_error_word(batch, G, row_idx_type):
     # few rows with few and many groups, and many rows
     x, w, eri, gl = _make(batch, 2, G, 64, 32, "bf16", 6, row_idx_type)
@@ -219,7 +222,7 @@ def test_wrong_routing_sets_the_error_word(batch, G, row_idx_type):
         assert pgg.read_device_error(ws)[0] == code
 
 
-@pytest.mark.parametrize("M,G", [(40, 4), (40, 300), (700, 4)])
+@pytest.mark.parametrize("M,G", [(40, 4), (200, 4), (40, 300), (700, 4)])
 def test_wrong_counts_set_the_gradients_error_word(M, G):
     gl = torch.zeros(G, dtype=torch.int64)
     gl[1], gl[3] = M // 2, M - M // 2

@@ -39,7 +39,7 @@ def _run(*args):
 SHAPES = [(1, 1, 1, 1, 1), (1, 2048, 264, 4, 8), (2, 67, 33, 3, 5), (16, 520, 300, 20, 16), (33, 256, 129, 2, 17),
           (64, 1000, 70, 70, 3), (65, 129, 257, 5, 33), (130, 72, 136, 1, 64), (300, 264, 520, 7, 12), (257, 99, 101, 3, 40),
           (600, 67, 35, 4, 9), (600, 72, 35, 4, 16), (520, 67, 40, 3, 70), (90, 67, 64, 3, 8), (1100, 128, 64, 6, 16),
-          (2100, 67, 35, 4, 9)]
+          (2100, 67, 35, 4, 9), (100, 264, 520, 5, 12), (128, 67, 35, 9, 16), (129, 67, 35, 9, 16), (256, 520, 136, 30, 33)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
@@ -100,8 +100,21 @@ def test_inner_products_beyond_the_range_of_fp16(dtype):
     ref.assert_within(y, want, bound)
 
 
+@pytest.mark.parametrize("T", [20, 300])
+def test_inner_products_beyond_the_largest_bf16(T):
+    # z = 2^64 * 255 * 2^56 * scale lies between bf16's largest value and fp32's
+    x, w = torch.full((T, 8), 0.0).bfloat16(), torch.zeros((8, 16)).bfloat16()
+    x[:, 0] = 2.0 ** 64
+    a, b = torch.zeros((1, 4, 8)).bfloat16(), torch.full((1, 4, 16), 2.0 ** -100).bfloat16()
+    a[0, 1, 0] = 255 * 2.0 ** 56
+    args = (x, w, a, b, torch.zeros(T, dtype=torch.int64), torch.tensor([1.0037]))
+    want, bound = ref.lora(*args)
+    assert torch.isfinite(want).all()
+    ref.assert_within(_run(*args), want, bound)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("T,K,N", [(8, 256, 128), (300, 128, 264), (600, 72, 40)])
+@pytest.mark.parametrize("T,K,N", [(8, 256, 128), (100, 128, 264), (300, 128, 264), (600, 72, 40)])
 def test_operands_at_any_address(T, K, N, dtype):
     def moved(t):
         out = torch.empty(t.numel() + 8, dtype=t.dtype, device=DEV)[1:1 + t.numel()].view(t.shape)
