@@ -19,7 +19,7 @@
 // Runs of one id make that one pass, 32 different ids 32 passes.
 //
 // z is fp32 and the matrix instructions take 16 bits, so z is split into two
-// bf16 parts (16 significand bits, relative error 2^-17, far below the
+// bf16 parts (relative error 2^-16, far below the
 // rounding of a 16-bit y; bf16 has the range of fp32, so nothing overflows),
 // and an fp16 B_p into two bf16 parts exactly.  fp32 inputs use fp32 matrix
 // instructions.
@@ -92,6 +92,53 @@ __device__ void check_ids(const LoraArgs& a) {
   }
 }
 
+// One wave: z of token t, ranks r to r + RW - 1, with its adapter p.  Lanes run
+// along the reduction, 2 or 4 loads of every row at a time, and their sums are
+// added over a fixed tree.
+template <class T, int RW>
+__device__ __forceinline__ void shrink_ranks(const LoraArgs& a, int64_t t, int32_t p, int r) {
+  using E = typename T::elem;
+  constexpr int EPC = T::kPerChunk, kUnroll = RW == 1 ? 4 : 2;
+  const int lane = threadIdx.x & 63;
+  const E* x = static_cast<const E*>(a.A) + t * a.R;
+  const E* ar[RW];
+#pragma unroll
+  for (int i = 0; i < RW; ++i)
+    ar[i] = static_cast<const E*>(a.a) + (static_cast<int64_t>(p) * a.rank + min(r + i, a.rank - 1)) * a.R;
+  float sum[RW][kUnroll] = {};
+  for (int64_t k = lane * EPC; k < a.R; k += 64 * EPC * kUnroll) {
+    u32x4_t vx[kUnroll], vw[RW][kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t at = k + u * 64 * EPC;
+      vx[u] = load16_part<T>(x + at, a.R - at, a.A_end);
+#pragma unroll
+      for (int i = 0; i < RW; ++i) vw[i][u] = load16_part<T>(ar[i] + at, a.R - at, a.a_end);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      E ex[EPC];
+      __builtin_memcpy(ex, &vx[u], 16);
+#pragma unroll
+      for (int i = 0; i < RW; ++i) {
+        E ew[EPC];
+        __builtin_memcpy(ew, &vw[i][u], 16);
+#pragma unroll
+        for (int e = 0; e < EPC; ++e) sum[i][u] = fmaf(to_float<T>(ex[e]), to_float<T>(ew[e]), sum[i][u]);
+      }
+    }
+  }
+  const float scale = a.scales[p];
+#pragma unroll
+  for (int i = 0; i < RW; ++i) {
+    float total = sum[i][0] + sum[i][1];
+    if constexpr (kUnroll == 4) total += sum[i][2] + sum[i][3];
+#pragma unroll
+    for (int d = 32; d; d >>= 1) total += __shfl_xor(total, d);
+    if (lane == 0 && r + i < a.rank) a.z[t * a.rank + r + i] = scale * total;
+  }
+}
+
 // ---------------------------------------------------------------- z, many tokens
 
 // 32 tokens x 16 NB ranks per workgroup (blockIdx.y: which ranks), the
@@ -102,6 +149,14 @@ __device__ void check_ids(const LoraArgs& a) {
 // one L2 and not by eight (2.2 -> 1.8 million lines from memory at 13824 tokens
 // of 7168, 60 adapters of rank 16 in runs of 300: 69 us, 198 MB of x alone take
 // about 40).  The last workgroup along x checks the ids.
+//
+// A pass over x for every adapter among the 32 tokens; where there are more
+// than kShrinkPasses of them, every token with its own ranks instead.  One
+// pass of rank 16 takes about 60 us at the size above, the tokens one by one 330;
+// 32 passes took 1100.
+template <int NB>
+constexpr int kShrinkPasses = 4 * NB;
+
 template <class T, int NB>
 __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a) {
   using E = typename T::elem;
@@ -127,6 +182,17 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) x[i] = static_cast<const E*>(a.A) + (t0 + min(16 * i + lr, rows - 1)) * R + lg * EPC;
   uint32_t pending = static_cast<uint32_t>(__ballot(id >= 0));
+  int adapters = 0;
+  for (uint32_t left = pending; left && adapters <= kShrinkPasses<NB>; ++adapters)
+    left &= ~static_cast<uint32_t>(__ballot(id == __shfl(id, __builtin_ctz(left))));
+  if (adapters > kShrinkPasses<NB>) {
+    for (int i = wave; i < rows * 4 * NB; i += kWaves) {
+      const int32_t p = __shfl(id, i / (4 * NB));
+      const int r = r0 + i % (4 * NB) * 4;
+      if (p >= 0 && r < a.rank) shrink_ranks<T, 4>(a, t0 + i / (4 * NB), p, r);
+    }
+    return;
+  }
   while (pending) {
     const int32_t p = __shfl(id, __builtin_ctz(pending));
     const uint32_t mine = static_cast<uint32_t>(__ballot(id == p));
@@ -191,9 +257,7 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a) {
 
 // ---------------------------------------------------------------- z, few tokens
 
-// A workgroup takes a token and 4 RW ranks of it, RW to a wave.  Lanes run along
-// the reduction, 2 or 4 loads of every row at a time, and their sums are added
-// over a fixed tree.  RW = 1 makes the most workgroups, for the fewest tokens;
+// A workgroup takes a token and 4 RW ranks of it, RW to a wave.  RW = 1 makes the most workgroups, for the fewest tokens;
 // RW = 4 reads x a quarter as often.  Workgroup rank_blocks<RW> checks the ids.
 template <int RW>
 __host__ __device__ __forceinline__ int rank_blocks(int64_t tokens, int32_t rank) {
@@ -202,55 +266,15 @@ __host__ __device__ __forceinline__ int rank_blocks(int64_t tokens, int32_t rank
 
 template <class T, int RW>
 __device__ __forceinline__ void shrink_token(const LoraArgs& a, int block) {
-  using E = typename T::elem;
-  constexpr int EPC = T::kPerChunk, kUnroll = RW == 1 ? 4 : 2;
   if (block == rank_blocks<RW>(a.T, a.rank)) {
     check_ids(a);
     return;
   }
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int per = (a.rank + 4 * RW - 1) / (4 * RW);
   const int64_t t = block / per;
-  const int r = (block % per * 4 + wave) * RW;
+  const int r = (block % per * 4 + static_cast<int>(threadIdx.x >> 6)) * RW;
   const int32_t p = adapter_of(a, t);
-  if (p < 0 || r >= a.rank) return;
-  const E* x = static_cast<const E*>(a.A) + t * a.R;
-  const E* ar[RW];
-#pragma unroll
-  for (int i = 0; i < RW; ++i)
-    ar[i] = static_cast<const E*>(a.a) + (static_cast<int64_t>(p) * a.rank + min(r + i, a.rank - 1)) * a.R;
-  float sum[RW][kUnroll] = {};
-  for (int64_t k = lane * EPC; k < a.R; k += 64 * EPC * kUnroll) {
-    u32x4_t vx[kUnroll], vw[RW][kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t at = k + u * 64 * EPC;
-      vx[u] = load16_part<T>(x + at, a.R - at, a.A_end);
-#pragma unroll
-      for (int i = 0; i < RW; ++i) vw[i][u] = load16_part<T>(ar[i] + at, a.R - at, a.a_end);
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      E ex[EPC];
-      __builtin_memcpy(ex, &vx[u], 16);
-#pragma unroll
-      for (int i = 0; i < RW; ++i) {
-        E ew[EPC];
-        __builtin_memcpy(ew, &vw[i][u], 16);
-#pragma unroll
-        for (int e = 0; e < EPC; ++e) sum[i][u] = fmaf(to_float<T>(ex[e]), to_float<T>(ew[e]), sum[i][u]);
-      }
-    }
-  }
-  const float scale = a.scales[p];
-#pragma unroll
-  for (int i = 0; i < RW; ++i) {
-    float total = sum[i][0] + sum[i][1];
-    if constexpr (kUnroll == 4) total += sum[i][2] + sum[i][3];
-#pragma unroll
-    for (int d = 32; d; d >>= 1) total += __shfl_xor(total, d);
-    if (lane == 0 && r + i < a.rank) a.z[t * a.rank + r + i] = scale * total;
-  }
+  if (p >= 0 && r < a.rank) shrink_ranks<T, RW>(a, t, p, r);
 }
 
 template <class T, int RW>
@@ -260,14 +284,15 @@ __global__ __launch_bounds__(256) void lora_shrink_token_kernel(LoraArgs a) {
 
 // ---------------------------------------------------------------- the shared product
 
-// 8 fp32 values as two bf16 parts.  The first part of a finite value is finite:
-// the rest is at most 2^-8 of the value there too.
+// 8 fp32 values as two bf16 parts.  The first is the upper half of the value's
+// bits, finite for every finite value (rounding would make infinities of those
+// above the largest bf16), the second the rest, rounded.  (A NaN out of
+// arithmetic has its quiet bit in the upper half.)
 __device__ __forceinline__ void split_bf16(const float (&v)[8], u32x4_t& hi, u32x4_t& lo) {
   uint16_t h[8], l[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    constexpr float kMost = 0x1.fep127f;   // bf16's largest
-    h[e] = from_float<TBf16>(fabsf(v[e]) < INFINITY ? __builtin_amdgcn_fmed3f(v[e], -kMost, kMost) : v[e]);
+    h[e] = static_cast<uint16_t>(__builtin_bit_cast(uint32_t, v[e]) >> 16);
     const float rest = v[e] - to_float<TBf16>(h[e]);
     l[e] = rest == rest ? from_float<TBf16>(rest) : 0;   // an infinite value has no rest
   }
@@ -489,9 +514,15 @@ hipError_t launch_shrink_token(const LoraArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Up to this many tokens z is computed token by token: a token reads its whole
-// adapter, but workgroups are many and their reads contiguous.
-constexpr int64_t kTokenByToken = 1024;
+// Up to this many tokens and ranks z is computed token by token: a token reads
+// its whole adapter, but workgroups are many, their reads contiguous, and the
+// order of the ids does not matter.  Whole calls in us, bf16, K 4096, N 512, 16
+// adapters, token by token and in tiles, runs of 300 ids and mixed ones:
+//   2048 tokens, rank 16: 62 and 64, mixed 60 and 145; rank 64: 107 and 93, 107
+//     and 398; rank 256: 292 and 122, 294 and 463
+//   4096 tokens, rank 16: 82 and 71, mixed 80 and 151
+constexpr int64_t kTokenByToken = 2048, kTokenRanks = 2048 * 64;
+bool token_by_token(const LoraArgs& a) { return a.T <= kTokenByToken && a.T * a.rank <= kTokenRanks; }
 
 // What the direct-to-LDS kernels need: 16-byte rows, and 32-bit byte offsets
 // into 256 rows of x and 64 rows of W.
@@ -505,7 +536,7 @@ hipError_t launch_typed(const LoraPlan& p, LoraArgs a, void* padded_x, void* pad
   const bool direct = T::kPerChunk == 8 && direct_rows(a);
   hipError_t e = hipSuccess;
   // z: beside the product, token by token, or in tiles
-  if (!a.few && a.T <= kTokenByToken) e = launch_shrink_token<T, 4>(a, s);
+  if (!a.few && token_by_token(a)) e = launch_shrink_token<T, 4>(a, s);
   else if (!a.few)
     e = a.rank <= 16 ? launch_shrink<T, 1>(a, s) : a.rank <= 32 ? launch_shrink<T, 2>(a, s) : launch_shrink<T, 4>(a, s);
   if (e != hipSuccess) return e;

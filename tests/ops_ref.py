@@ -166,6 +166,6 @@ def lora(x, weight, a, b, ids, scales):
         ad, bd, s = a[p].cpu().double(), b[p].cpu().double(), float(scales[p])
         z, ez = s * (ad @ xd[t]), abs(s) * gamma(K) * (ad.abs() @ xd[t].abs())
         y[t] += z @ bd
-        # z as two bf16 parts is off by 2^-17 of itself; then a sum of R products
+        # z as two bf16 parts is off by 2^-16 of itself; then a sum of R products
         err[t] += (ez + z.abs() * 2.0 ** -16) @ bd.abs() + gamma(R) * (z.abs() @ bd.abs())
     return y, rounded(y, err + 2.0 ** -23 * y.abs(), dtype)

@@ -39,7 +39,8 @@ def _run(*args):
 SHAPES = [(1, 1, 1, 1, 1), (1, 2048, 264, 4, 8), (2, 67, 33, 3, 5), (16, 520, 300, 20, 16), (33, 256, 129, 2, 17),
           (64, 1000, 70, 70, 3), (65, 129, 257, 5, 33), (130, 72, 136, 1, 64), (300, 264, 520, 7, 12), (257, 99, 101, 3, 40),
           (600, 67, 35, 4, 9), (600, 72, 35, 4, 16), (520, 67, 40, 3, 70), (90, 67, 64, 3, 8), (1100, 128, 64, 6, 16),
-          (2100, 67, 35, 4, 9), (100, 264, 520, 5, 12), (128, 67, 35, 9, 16), (129, 67, 35, 9, 16), (256, 520, 136, 30, 33)]
+          (2100, 67, 35, 4, 9), (100, 264, 520, 5, 12), (128, 67, 35, 9, 16), (129, 67, 35, 9, 16), (256, 520, 136, 30, 33),
+          (2100, 264, 40, 60, 16), (2060, 67, 35, 40, 20), (2055, 130, 72, 50, 40), (300, 72, 40, 3, 500)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
