@@ -483,7 +483,8 @@ pgg_status pgg_moe_gate(const pgg_moe_gate_desc* desc, const void* logits, const
  *   renorm 1: u = softmax of the chosen logits:
  *             grad_logits_{e_j} = u_j * (d_j - sum_m d_m u_m), plus grad_lse p_e for every e
  *
- * logits, lse and expert_ids are pgg_moe_gate's; every element of grad_logits
+ * logits, lse and expert_ids are pgg_moe_gate's (a token's ids are distinct);
+ * every element of grad_logits
  * [tokens, experts] (dtype) is written.  A row of -inf gets zeros.  An id
  * outside [0, experts) selects nothing.  No workspace; one kernel.
  */
@@ -506,7 +507,10 @@ pgg_status pgg_moe_gate_grad(const pgg_moe_gate_desc* desc, const void* logits, 
  *   gate_up  [M, 2F]  dtype, may be NULL: the products, for pgg_moe_glu_grad
  *
  * fp32 accumulation; h comes from the unrounded products and is rounded once.
- * Errors, alignment and workspace rules are pgg_moe_fwd's.
+ * Beside the tables the workspace holds, where tiles alone do not fill the chip,
+ * fp32 partial products (at most 64 x M x 2F floats, and at most about 512 tiles'
+ * worth), and where many rows of x or weight are not 16-byte aligned, copies of
+ * them with padded rows.  Errors, alignment and workspace rules are pgg_moe_fwd's.
  */
 typedef enum { PGG_ACT_SILU = 0, PGG_ACT_GELU_TANH = 1 } pgg_act;
 
@@ -543,9 +547,10 @@ pgg_status pgg_moe_glu(const pgg_moe_glu_desc* desc, const void* x, const void* 
  *
  * Rows are in expanded (expert-grouped) order.  The gradients that remain are
  * pgg_moe_dx and pgg_moe_dw with grad_gate_up, and pgg_moe_dw with h and
- * grad_y.  fp32 accumulation, one rounding.  Workspace: O(M + G) integers;
- * group_list is checked on the device (PGG_DEV_GROUP_NEGATIVE / _SUM; the
- * outputs are then unspecified).
+ * grad_y.  fp32 accumulation, one rounding.  Workspace: O(M + G) integers, and
+ * partial products and padded copies as for pgg_moe_glu; group_list is checked
+ * on the device (PGG_DEV_GROUP_NEGATIVE / _SUM; the outputs are then
+ * unspecified).
  */
 typedef struct {
   int64_t grad_y_rows, grad_y_cols;
@@ -575,11 +580,13 @@ pgg_status pgg_moe_glu_grad(const pgg_moe_glu_grad_desc* desc, const void* grad_
  * sets the workspace error word (PGG_DEV_ADAPTER_RANGE) and leaves y
  * unspecified.  Adapters of smaller rank are padded with zero rows.  A token's
  * row depends on its own x and adapter only, whatever values other adapters
- * hold.  fp32 accumulation; the inner product x * A_p^T stays in fp32; one
- * rounding.  Limit: rank <= PGG_LORA_MAX_RANK.  The workspace holds tokens x
- * rank floats and, with few tokens, fp32 partial results (at most 64 x tokens
- * x N floats, and at most about 512 tiles' worth).  Its rules are
- * pgg_moe_fwd's.
+ * hold.  fp32 accumulation; the inner product x * A_p^T stays in fp32 (16-bit
+ * products take it as two bf16 parts, relative error 2^-16); one rounding.
+ * Limit: rank <= PGG_LORA_MAX_RANK.  The workspace holds tokens x rank floats;
+ * where tiles alone do not fill the chip, fp32 partial results (at most 64 x
+ * tokens x N floats, and at most about 512 tiles' worth); and where many rows of
+ * x or weight are not 16-byte aligned, copies of them with padded rows.  Its
+ * rules are pgg_moe_fwd's.
  */
 #define PGG_LORA_MAX_RANK 1024
 typedef struct {

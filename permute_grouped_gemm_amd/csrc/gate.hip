@@ -24,6 +24,10 @@
 // pick j and hands its d_j to the expert's lane through LDS.
 //
 // Sums and maxima are fp32 and are added in a fixed order.
+//
+// Measured: 13824 tokens, 60 experts, 8 picks, fp32: forward 6.5 us (3.3 MB read,
+// 1.4 written: eight dependent picks, not bytes), gradient 5.1 us (4.9 MB read, 3.3
+// written, 1.6 TB/s); 16 tokens of 16 experts 3.1 us, a launch's own time.
 #include "pgg_device.h"
 
 namespace pgg {

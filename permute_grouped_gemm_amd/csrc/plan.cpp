@@ -554,10 +554,10 @@ pgg_status make_glu_plan(const pgg_moe_glu_desc* d, Plan* p) {
   // 128 x 128.  Where tiles alone do not fill the chip, the reduction is split.
   // An expert of more rows than a tile reads its weights again, and the tiles of
   // 64 rows have to be direct-to-LDS ones.  Measured in us, 32 and 64 rows:
-  //   bf16, 16 experts, N 4096, K 2048: 24 rows per expert 99, 99; 32 142, 101;
+  //   bf16, 16 experts, K 4096, F 2048: 24 rows per expert 99, 99; 32 142, 101;
   //     48 156, 107; 60 186, 149
-  //   N 4095, K 2047: 24 126, 150; 32 172, 151; 48 163, 155; 60 239, 247
-  //   f32, N 2048, K 1408: 24 95, 173; 32 121, 175; 48 168, 175; 60 170, 178
+  //   K 4095, F 2047: 24 126, 150; 32 172, 151; 48 163, 155; 60 239, 247
+  //   f32, K 2048, F 1408: 24 95, 173; 32 121, 175; 48 168, 175; 60 170, 178
   const int64_t cus = p->regime == kLarge ? 256 : 512;
   if (p->M <= 64 * p->G) {
     p->regime = kStream;
