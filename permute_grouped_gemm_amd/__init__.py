@@ -39,6 +39,11 @@ gradients, and
 
 is a projection that all tokens share with a low-rank adapter per token
 beside it.
+
+Every call runs on the current stream of the current device, on which its
+tensors have to be, or on ``stream``.  The caller orders that stream behind the
+work that makes the inputs (``stream.wait_stream``) and later uses of the
+results behind it; what the call allocates is ``stream``'s own memory.
 """
 from __future__ import annotations
 
@@ -311,6 +316,19 @@ def _stream_handle(stream) -> int:
     return int(s.cuda_stream)
 
 
+def _fresh(shape, dtype, dev, stream):
+    """A new tensor for a kernel on ``stream`` (None: the current one), out of
+    that stream's own memory: what the current stream has freed may still be in
+    use by work queued there, which nothing orders before ``stream``.  Results
+    are used and freed by the caller, so the current stream is recorded too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(torch.cuda.current_stream(dev))
+    return t
+
+
 def _check_inputs(*tensors):
     dev = tensors[0].device
     for t in tensors:
@@ -344,9 +362,9 @@ def moe_dx(grad_y: torch.Tensor, weight: torch.Tensor, expanded_row_idx: torch.T
     need = workspace_size_desc(d)
     dev = grad_y.device
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _fresh(need, torch.uint8, dev, stream)
     if out is None:
-        out = torch.empty((int(batch), int(weight.shape[1])), dtype=torch.float32, device=dev)
+        out = _fresh((int(batch), int(weight.shape[1])), torch.float32, dev, stream)
     _check_out(out, batch, weight, dev)
     _check_workspace(workspace, dev)
     st = lib().pgg_moe_dx(ctypes.byref(d), grad_y.data_ptr(), weight.data_ptr(),
@@ -444,10 +462,10 @@ def kernel_time(grad_y, weight, expanded_row_idx, group_list, batch, topk, row_i
     _check_inputs(grad_y, weight, expanded_row_idx, group_list)
     dev = grad_y.device
     if workspace is None:
-        workspace = torch.empty(workspace_size_desc(d), dtype=torch.uint8, device=dev)
+        workspace = _fresh(workspace_size_desc(d), torch.uint8, dev, stream)
     _check_workspace(workspace, dev)
     if out is None:
-        out = torch.empty((int(batch), int(weight.shape[1])), dtype=torch.float32, device=dev)
+        out = _fresh((int(batch), int(weight.shape[1])), torch.float32, dev, stream)
     _check_out(out, batch, weight, dev)
     avg = ctypes.c_double()
     n = ctypes.c_int32()
@@ -508,13 +526,13 @@ def fwd_plan(x, weight, expanded_row_idx, group_list, topk, row_idx_type=0) -> d
     return p.as_dict()
 
 
-def _fwd_buffers(d, x, weight, out, workspace):
+def _fwd_buffers(d, x, weight, out, workspace, stream):
     dev = x.device
     if workspace is None:
-        workspace = torch.empty(fwd_workspace_size_desc(d), dtype=torch.uint8, device=dev)
+        workspace = _fresh(fwd_workspace_size_desc(d), torch.uint8, dev, stream)
     shape = (int(d.batch * d.topk), int(weight.shape[2]))
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=dev)
+        out = _fresh(shape, torch.float32, dev, stream)
     if (out.dtype != torch.float32 or not out.is_contiguous() or tuple(out.shape) != shape
             or out.device != dev):
         raise PggError(ERR_INVALID_ARG, "out must be a contiguous float32 [M, N] tensor on the inputs' GPU")
@@ -532,7 +550,7 @@ def moe_fwd(x: torch.Tensor, weight: torch.Tensor, expanded_row_idx: torch.Tenso
     bfloat16; expanded_row_idx [batch*topk] and group_list [G] are int64."""
     d = _fwd_desc_from_tensors(x, weight, expanded_row_idx, group_list, topk, row_idx_type)
     _check_inputs(x, weight, expanded_row_idx, group_list)
-    out, workspace = _fwd_buffers(d, x, weight, out, workspace)
+    out, workspace = _fwd_buffers(d, x, weight, out, workspace, stream)
     st = lib().pgg_moe_fwd(ctypes.byref(d), x.data_ptr(), weight.data_ptr(),
                            expanded_row_idx.data_ptr(), group_list.data_ptr(), out.data_ptr(),
                            workspace.data_ptr(), workspace.numel() * workspace.element_size(),
@@ -547,7 +565,7 @@ def fwd_kernel_time(x, weight, expanded_row_idx, group_list, topk, row_idx_type=
     back to back after one full call (pgg_moe_fwd_kernel_time)."""
     d = _fwd_desc_from_tensors(x, weight, expanded_row_idx, group_list, topk, row_idx_type)
     _check_inputs(x, weight, expanded_row_idx, group_list)
-    out, workspace = _fwd_buffers(d, x, weight, out, workspace)
+    out, workspace = _fwd_buffers(d, x, weight, out, workspace, stream)
     avg = ctypes.c_double()
     _check(lib().pgg_moe_fwd_kernel_time(ctypes.byref(d), x.data_ptr(), weight.data_ptr(),
                                          expanded_row_idx.data_ptr(), group_list.data_ptr(),
@@ -579,15 +597,15 @@ def dw_workspace_size(x, grad_y, expanded_row_idx, group_list, topk, row_idx_typ
     return n.value
 
 
-def _dw_buffers(d, x, out, workspace):
+def _dw_buffers(d, x, out, workspace, stream):
     dev = x.device
     if workspace is None:
         n = ctypes.c_size_t()
         _check(lib().pgg_moe_dw_workspace_size(ctypes.byref(d), ctypes.byref(n)), "dw_workspace_size")
-        workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
+        workspace = _fresh(n.value, torch.uint8, dev, stream)
     shape = (int(d.weight_groups), int(d.weight_rows), int(d.weight_cols))
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=dev)
+        out = _fresh(shape, torch.float32, dev, stream)
     if (out.dtype != torch.float32 or not out.is_contiguous() or tuple(out.shape) != shape
             or out.device != dev):
         raise PggError(ERR_INVALID_ARG, "out must be a contiguous float32 [G, K, N] tensor on the inputs' GPU")
@@ -604,7 +622,7 @@ def moe_dw(x: torch.Tensor, grad_y: torch.Tensor, expanded_row_idx: torch.Tensor
     grad_y [batch*topk, N] share one of float32 / float16 / bfloat16."""
     d = _dw_desc_from_tensors(x, grad_y, expanded_row_idx, group_list, topk, row_idx_type)
     _check_inputs(x, grad_y, expanded_row_idx, group_list)
-    out, workspace = _dw_buffers(d, x, out, workspace)
+    out, workspace = _dw_buffers(d, x, out, workspace, stream)
     st = lib().pgg_moe_dw(ctypes.byref(d), x.data_ptr(), grad_y.data_ptr(),
                           expanded_row_idx.data_ptr(), group_list.data_ptr(), out.data_ptr(),
                           workspace.data_ptr(), workspace.numel() * workspace.element_size(),
@@ -619,7 +637,7 @@ def dw_kernel_time(x, grad_y, expanded_row_idx, group_list, topk, row_idx_type=0
     after one full call (pgg_moe_dw_kernel_time)."""
     d = _dw_desc_from_tensors(x, grad_y, expanded_row_idx, group_list, topk, row_idx_type)
     _check_inputs(x, grad_y, expanded_row_idx, group_list)
-    out, workspace = _dw_buffers(d, x, out, workspace)
+    out, workspace = _dw_buffers(d, x, out, workspace, stream)
     avg = ctypes.c_double()
     _check(lib().pgg_moe_dw_kernel_time(ctypes.byref(d), x.data_ptr(), grad_y.data_ptr(),
                                         expanded_row_idx.data_ptr(), group_list.data_ptr(),
@@ -666,13 +684,13 @@ def moe_routing(expert_ids: torch.Tensor, experts: int, x: Optional[torch.Tensor
     d = make_routing_desc(batch, topk, experts, K, xd)
     dev = expert_ids.device
     if workspace is None:
-        workspace = torch.empty(routing_workspace_size_desc(d), dtype=torch.uint8, device=dev)
+        workspace = _fresh(routing_workspace_size_desc(d), torch.uint8, dev, stream)
     _check_workspace(workspace, dev)
     M = batch * topk
-    gl = torch.empty(int(experts), dtype=torch.int64, device=dev)
-    eg = torch.empty(M, dtype=torch.int64, device=dev) if gather else None
-    es = torch.empty(M, dtype=torch.int64, device=dev) if scatter else None
-    ex = torch.empty((M, K), dtype=x.dtype, device=dev) if x is not None else None
+    gl = _fresh(int(experts), torch.int64, dev, stream)
+    eg = _fresh(M, torch.int64, dev, stream) if gather else None
+    es = _fresh(M, torch.int64, dev, stream) if scatter else None
+    ex = _fresh((M, K), x.dtype, dev, stream) if x is not None else None
     ptr = lambda t: None if t is None else t.data_ptr()
     st = lib().pgg_moe_routing(ctypes.byref(d), expert_ids.data_ptr(), ptr(x), gl.data_ptr(), ptr(eg),
                                ptr(es), ptr(ex), workspace.data_ptr(),
@@ -706,14 +724,14 @@ def _check_index(t, n, like):
                                         f"on {like.device}")
 
 
-def _unpermute_ws(d, dev, workspace):
+def _unpermute_ws(d, dev, workspace, stream):
     if workspace is not None:
         _check_workspace(workspace, dev)
         return workspace
     n = ctypes.c_size_t()
     _check(lib().pgg_moe_unpermute_workspace_size(ctypes.byref(d), ctypes.byref(n)),
            "unpermute_workspace_size")
-    return torch.empty(n.value, dtype=torch.uint8, device=dev)
+    return _fresh(n.value, torch.uint8, dev, stream)
 
 
 def moe_unpermute(permuted: torch.Tensor, expanded_row_idx: torch.Tensor, batch: int, topk: int,
@@ -731,8 +749,8 @@ def moe_unpermute(permuted: torch.Tensor, expanded_row_idx: torch.Tensor, batch:
         _check_value(probs, (int(batch), int(topk)), permuted, "probs")
     d = make_unpermute_desc(batch, topk, H, row_idx_type, DTYPE_CODE.get(permuted.dtype, -1))
     shape = (int(batch), H) if probs is not None else (int(batch) * int(topk), H)
-    out = torch.empty(shape, dtype=permuted.dtype, device=permuted.device)
-    ws = _unpermute_ws(d, permuted.device, workspace)
+    out = _fresh(shape, permuted.dtype, permuted.device, stream)
+    ws = _unpermute_ws(d, permuted.device, workspace, stream)
     st = lib().pgg_moe_unpermute(ctypes.byref(d), permuted.data_ptr(), expanded_row_idx.data_ptr(),
                                  None if probs is None else probs.data_ptr(), out.data_ptr(),
                                  ws.data_ptr(), _ws_bytes(ws), _stream_handle(stream))
@@ -757,10 +775,9 @@ def moe_unpermute_grad(grad: torch.Tensor, expanded_row_idx: torch.Tensor, batch
             raise PggError(ERR_INVALID_ARG, "permuted is needed with probs")
         _check_value(permuted, (M, H), grad, "permuted")
     d = make_unpermute_desc(batch, topk, H, row_idx_type, DTYPE_CODE.get(grad.dtype, -1))
-    perm_grad = torch.empty((M, H), dtype=grad.dtype, device=grad.device)
-    probs_grad = (torch.empty((int(batch), int(topk)), dtype=grad.dtype, device=grad.device)
-                  if probs is not None else None)
-    ws = _unpermute_ws(d, grad.device, workspace)
+    perm_grad = _fresh((M, H), grad.dtype, grad.device, stream)
+    probs_grad = _fresh((int(batch), int(topk)), grad.dtype, grad.device, stream) if probs is not None else None
+    ws = _unpermute_ws(d, grad.device, workspace, stream)
     ptr = lambda t: None if t is None else t.data_ptr()
     st = lib().pgg_moe_unpermute_grad(ctypes.byref(d), ptr(permuted), grad.data_ptr(),
                                       expanded_row_idx.data_ptr(), ptr(probs), perm_grad.data_ptr(),
@@ -793,15 +810,6 @@ def _on_stream(stream, dev):
     if torch._C._cuda_getDevice() != dev.index:
         raise PggError(ERR_INVALID_ARG, f"the inputs are on {dev}, which is not the current device")
     return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else int(stream.cuda_stream)
-
-
-def _fresh(shape, dtype, dev, stream):
-    """A new tensor that a kernel on ``stream`` uses: its memory is not handed
-    out again before that stream has passed the point where it was freed."""
-    t = torch.empty(shape, dtype=dtype, device=dev)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
 
 
 def _out(t, name, shape, dtype, dev, stream):
