@@ -21,7 +21,8 @@
 // z is fp32 and the matrix instructions take 16 bits, so z is split into two
 // bf16 parts (relative error 2^-16, far below the rounding of a 16-bit y; bf16
 // has the range of fp32, so nothing overflows), and an fp16 B_p into two bf16
-// parts exactly.  fp32 inputs use fp32 matrix instructions.
+// parts exactly; all products of the parts are added.  fp32 inputs use fp32
+// matrix instructions.
 //
 // With few tokens the projection is bound by reading W once and the launches:
 // the reduction is split over workgroups, the first launch also computes z,
@@ -421,7 +422,10 @@ struct LoraOp {
               if constexpr (EPC == 8) {
                 mma_block<TBf16>(d, bh, zh[i]);
                 mma_block<TBf16>(d, bh, zl[i]);
-                if constexpr (__is_same(T, TF16)) mma_block<TBf16>(d, bl, zh[i]);
+                if constexpr (__is_same(T, TF16)) {
+                  mma_block<TBf16>(d, bl, zh[i]);
+                  mma_block<TBf16>(d, bl, zl[i]);   // up to 2^-14: both parts are truncated, not rounded
+                }
               } else {
                 mma<T>(d, bh, zh[i]);
               }
