@@ -159,7 +159,7 @@ __device__ __forceinline__ void finish_row(const GateArgs& a, const typename T::
     if (j < a.k) {
       const float e = expf(l[s] - top);
       a.ids[t * a.k + j] = sel[s];
-      a.probs[t * a.k + j] = (total > 0.0f ? e / total : e) * a.scale;
+      a.probs[t * a.k + j] = (total == 0.0f ? e : e / total) * a.scale;   // NaN stays NaN
     }
   }
 }
@@ -311,7 +311,7 @@ __global__ __launch_bounds__(THREADS) void gate_grad_kernel(GateGradArgs a) {
   }
   if (a.renorm) {
     sum = row_sum<LPR>(sum);
-    inv = sum > 0.0f ? 1.0f / sum : 1.0f;
+    inv = sum == 0.0f ? 1.0f : 1.0f / sum;
   }
   float mean = 0.0f;   // sum_j d_j p_j
 #pragma unroll
