@@ -39,11 +39,18 @@ __device__ __forceinline__ bool local_tile(const int64_t* gl, int64_t G, int64_t
     scratch[wave] = rows;
     scratch[4 + wave] = tiles;
   }
+  // over the waves through the same words: the barrier that reduces a value
+  // would take 256 bytes of LDS of its own, and the 32-row tiles of the gradient
+  // leave none (4 workgroups to a compute unit take all 160 KiB)
+  const bool wave_bad = __ballot(bad) != 0;
+  if (lane == 0) scratch[11 + wave] = wave_bad;
   if (tid == 0) scratch[10] = 0;
-  const bool any_bad = __syncthreads_or(bad);
+  __syncthreads();
+  bool any_bad = false;
   int64_t total = 0;
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
+    any_bad |= scratch[11 + w] != 0;
     total += scratch[w];
     if (w < wave) {
       rows += scratch[w];
