@@ -64,8 +64,12 @@ hipError_t launch_prep_fused(const Plan& p, const int64_t* eri, const int64_t* g
 }
 
 hipError_t launch_prep_groups(const Plan& p, const int64_t* gl, const WsView& w, hipStream_t s) {
-  // few groups: one wave, as above (7 -> 4 us at 64 groups)
-  const unsigned threads = p.M <= 4096 && p.G <= 4096 ? 64u : unsigned(kPrepThreads);
+  // Few rows: no more threads than groups keep busy, as every step of the scan is
+  // a barrier of all of them.  Whole calls of the gradient in us at 1024 rows, D
+  // and F 16, with 64, 256 and 1024 threads: 257 groups 10.8, 9.9, 11.1; 512 13.0,
+  // 10.6, 11.5; 1024 18.9, 12.7, 12.8; 2048 30.3, 18.1, 16.4.  (At 64 groups 64
+  // threads take 4 us and 1024 take 7.)
+  const unsigned threads = p.M > 4096 || p.G > 1024 ? unsigned(kPrepThreads) : p.G > 64 ? 256u : 64u;
   hipLaunchKernelGGL(prep_groups_kernel, dim3(1), dim3(threads), 0, s, prep_args(p), gl, w);
   return hipGetLastError();
 }
