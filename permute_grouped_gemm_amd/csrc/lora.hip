@@ -294,17 +294,22 @@ __global__ __launch_bounds__(256) void lora_shrink_token_kernel(LoraArgs a) {
 // 8 fp32 values as two bf16 parts.  The first is the upper half of the value's
 // bits, finite for every finite value (rounding would make infinities of those
 // above the largest bf16), the second the rest, rounded.  (A NaN out of
-// arithmetic has its quiet bit in the upper half.)
-__device__ __forceinline__ void split_bf16(const float (&v)[8], u32x4_t& hi, u32x4_t& lo) {
-  uint16_t h[8], l[8];
+// arithmetic has its quiet bit in the upper half.)  An infinite value has no
+// rest, and the other operand's rest may be 0 as well: `fin` is the first part
+// with zeros for what is not finite, for products with a rest, where infinity
+// times 0 would make a NaN that the values' product is not.
+__device__ __forceinline__ void split_bf16(const float (&v)[8], u32x4_t& hi, u32x4_t& lo, u32x4_t& fin) {
+  uint16_t h[8], l[8], f[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     h[e] = static_cast<uint16_t>(__builtin_bit_cast(uint32_t, v[e]) >> 16);
     const float rest = v[e] - to_float<TBf16>(h[e]);
-    l[e] = rest == rest ? from_float<TBf16>(rest) : 0;   // an infinite value has no rest
+    l[e] = rest == rest ? from_float<TBf16>(rest) : 0;
+    f[e] = rest == rest ? h[e] : 0;
   }
   __builtin_memcpy(&hi, h, 16);
   __builtin_memcpy(&lo, l, 16);
+  __builtin_memcpy(&fin, f, 16);
 }
 
 struct LoraOp {
@@ -372,7 +377,7 @@ struct LoraOp {
       const float* z0 = a.z + (int64_t(t.row0) + m0 + g * B + lane % B) * a.rank;
       for (int r0 = 0; r0 < a.rank; r0 += kStep) {
         const int r = r0 + EPC * (lane / B);
-        u32x4_t zh[kGroup], zl[kGroup];
+        u32x4_t zh[kGroup], zl[kGroup], zf[kGroup];
 #pragma unroll
         for (int i = 0; i < kGroup; ++i) {
           const float* z = z0 + static_cast<int64_t>(i) * B * a.rank + r;
@@ -383,7 +388,7 @@ struct LoraOp {
 #pragma unroll
             for (int e = 0; e < EPC; ++e) v[e] = id[i] >= 0 && r + e < a.rank ? z[e] : 0.0f;
           }
-          if constexpr (EPC == 8) split_bf16(v, zh[i], zl[i]);
+          if constexpr (EPC == 8) split_bf16(v, zh[i], zl[i], zf[i]);
           else __builtin_memcpy(&zh[i], v, 16);
         }
         for (int32_t last = -1;;) {
@@ -405,12 +410,12 @@ struct LoraOp {
           }
 #pragma unroll
           for (int j = 0; j < NJ; ++j) {
-            u32x4_t bh, bl;
+            u32x4_t bh, bl, bf;
             if constexpr (EPC == 8) {
               float v[EPC];
 #pragma unroll
               for (int e = 0; e < EPC; ++e) v[e] = to_float<T>(raw[j][e]);
-              split_bf16(v, bh, bl);
+              split_bf16(v, bh, bl, bf);
             } else {
               __builtin_memcpy(&bh, raw[j], 16);
             }
@@ -421,9 +426,9 @@ struct LoraOp {
               for (int e = 0; e < B * B / 64; ++e) d[e] = 0.0f;
               if constexpr (EPC == 8) {
                 mma_block<TBf16>(d, bh, zh[i]);
-                mma_block<TBf16>(d, bh, zl[i]);
+                mma_block<TBf16>(d, bf, zl[i]);
                 if constexpr (__is_same(T, TF16)) {
-                  mma_block<TBf16>(d, bl, zh[i]);
+                  mma_block<TBf16>(d, bl, zf[i]);
                   mma_block<TBf16>(d, bl, zl[i]);   // up to 2^-14: both parts are truncated, not rounded
                 }
               } else {

@@ -42,3 +42,38 @@ def test_inner_products_keep_sixteen_bits(T, N, dtype):
     y = pgg.lora_fwd(*[t.to(DEV) for t in (x, w, a, b, ids, scales)])
     want = (zb + w[4:8].double())[ids]
     ref.assert_within(y, want, ref.rounded(want, zb[ids] * (2.0 ** -16 + 2.0 ** -20), dt))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,N", KERNELS)
+def test_infinite_values_give_the_infinities_of_their_product(T, N, dtype):
+    # infinities in B against z of few and of many bits, in A (z infinite) against B
+    # of few and of many bits: y is infinite with the product's sign, as in 64 bits,
+    # and NaN only where the 64-bit form is
+    dt, K = ref.DTYPES[dtype], 72
+    gen = torch.Generator().manual_seed(N)
+    x, w = torch.zeros((T, K)).to(dt), (torch.randn((K, N), generator=gen) * 0.1).to(dt)
+    x[:, 1] = 1.0
+    x[::2, 2] = -1.0                                   # z changes sign
+    a = torch.zeros((5, 2, K)).to(dt)
+    a[:, 0, 1], a[:, 0, 2], a[:, 1, 1] = 1.0, 2.0, 0.5
+    b = (1.0 + torch.rand((5, 2, N), generator=gen)).to(dt)
+    b[0, 0, 1], b[0, 1, 2], b[0, 0, 3] = math.inf, -math.inf, math.nan
+    b[1, 0, 1], b[1, 1, 2] = -math.inf, math.inf       # z of 24 bits
+    b[2, 0, ::3], b[2, 0, 1::3] = 1.0, -2.0
+    b[3, 0, ::3], b[3, 0, 1] = 0.0, -0.0
+    a[2, 0, 1] = a[3, 0, 1] = math.inf                 # z infinite
+    scales = torch.tensor([1.0, 1.2345678, 1.0, 1.0, 0.75])
+    ids = torch.arange(T) // 5 % 6 - 1
+    y = pgg.lora_fwd(*[t.to(DEV) for t in (x, w, a, b, ids, scales)]).cpu().double()
+    want = x.double() @ w.double()
+    for t in range(T):
+        if ids[t] >= 0:
+            z = scales[ids[t]].double() * (a[ids[t]].double() * x[t].double()).sum(dim=1)
+            want[t] += (z[:, None] * b[ids[t]].double()).sum(dim=0)
+    assert torch.equal(y.isnan(), want.isnan())
+    assert torch.equal(y.isinf(), want.isinf())
+    at = want.isinf()
+    assert at.any() and torch.equal(y[at], want[at])
+    # the others: sums of terms below 8 in all, far less than the final rounding's 2^-8
+    ref.assert_within(y[~at], want[~at], 2.0 ** -8 * want[~at].abs() + 8 * 2.0 ** -14)
