@@ -477,7 +477,7 @@ pgg_status pgg_moe_gate(const pgg_moe_gate_desc* desc, const void* logits, const
 /*
  * Gradient of the gate with respect to the logits (the choice is constant):
  * from grad_probs [tokens, topk] float32 and, unless NULL, grad_lse [tokens]
- * float32, with d_j = scale * grad_probs_j and p = exp(logits - lse),
+ * float32, with d_j = scale * grad_probs_j and p = softmax(logits),
  *
  *   renorm 0: grad_logits_e = p_e * (sum_{j: e_j = e} d_j - sum_j d_j p_{e_j}) + grad_lse p_e
  *   renorm 1: u = softmax of the chosen logits:

@@ -32,3 +32,36 @@ def test_an_infinite_logit_makes_its_weights_nan(E, dtype):
         grad = pgg.moe_gate_grad(l.to(DEV), lse, ids, torch.ones((4, 4), device=DEV), renorm=renorm)
         assert grad[0].isfinite().all()
         assert grad.gather(1, ids)[1:].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("E,k", [(8, 2), (60, 8), (130, 8), (300, 4), (1100, 8)])
+def test_gradients_of_rows_far_from_zero(E, k, dtype):
+    # rows of the type's lowest or largest value, and rows with a large offset: the
+    # softmax depends on differences of logits only, and so does its gradient's
+    # error: exp of a rounded difference, E additions, a few products
+    dt = ref.DTYPES[dtype]
+    big = torch.finfo(dt).max
+    l = _logits(8, E, 3 * E, dtype)
+    l[0], l[1] = -big, big
+    l[2] = -big
+    l[2, E // 2] = -big * 0.75                         # one far above the others
+    l[3] = 4096.0 + 4 * (torch.arange(E) % 3)
+    l[4] = -8192.0 - 8 * (torch.arange(E) % 5)
+    l[5, 3:] = -big                                    # three experts left
+    gen = torch.Generator().manual_seed(E)
+    gp, gl = torch.randn((8, k), generator=gen), torch.randn(8, generator=gen)
+    ids, _, lse = pgg.moe_gate(l.to(DEV), k)
+    ld = l.double()
+    p = torch.softmax(ld, dim=1)
+    d = torch.zeros((8, E), dtype=torch.float64).scatter(1, ids.cpu(), gp.double() * 2.5)
+    far = (ld - ld.amax(dim=1, keepdim=True)).abs().clamp_max(128.0)   # beyond, exp is 0 either way
+    for renorm in (False, True):
+        chosen = torch.zeros((8, E), dtype=torch.bool).scatter(1, ids.cpu(), True)
+        w = torch.softmax(ld.masked_fill(~chosen, -math.inf), dim=1) if renorm else p
+        mean = (w * d).sum(dim=1, keepdim=True)
+        size = w * (d.abs() + (w * d.abs()).sum(dim=1, keepdim=True)) + p * gl.double().abs()[:, None]
+        want = w * (d - mean) + p * gl.double()[:, None]
+        got = pgg.moe_gate_grad(l.to(DEV), lse, ids, gp.to(DEV), grad_lse=gl.to(DEV), renorm=renorm, scale=2.5)
+        bound = size * (far.amax(dim=1, keepdim=True) + E + 32) * 2.0 ** -22
+        ref.assert_within(got, want, ref.rounded(want, bound, dt), f"renorm {renorm}")
