@@ -35,7 +35,8 @@ __device__ __forceinline__ void activate_grad(float g, float& value, float& slop
     du = 1.0f;
   } else {
     s = sigmoid(2.0f * kGeluC * (g + kGeluA * g * g * g));
-    du = 2.0f * kGeluC * (1.0f + 3.0f * kGeluA * g * g);
+    // finite, so that it keeps the 0 of s (1 - s), which g is far past by then
+    du = 2.0f * kGeluC * (1.0f + 3.0f * kGeluA * fminf(g * g, 1e30f));
   }
   value = g * s;
   slope = s + g * s * (1.0f - s) * du;
