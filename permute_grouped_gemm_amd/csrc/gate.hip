@@ -268,7 +268,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_long_kernel(GateArgs a) {
 
 // LPR lanes per row, rows of one wave only; E floats of LDS per row, which hold
 // d_j at the picks and kUnpicked elsewhere.
-constexpr uint32_t kUnpicked = 0x7FC0DEADu;   // a NaN that no product makes
+constexpr uint32_t kUnpicked = 0x7FC0DEADu;   // a NaN; those among the d_j are stored as another
 
 // Up to this |lse| its fp32 rounding changes exp(l - lse) by 2^-21 of itself at
 // most.  Beyond, exp(l - lse) is divided by its sum over the row: in a row of the
@@ -341,7 +341,7 @@ __global__ __launch_bounds__(THREADS) void gate_grad_kernel(GateGradArgs a) {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
   for (int s = 0; s < kPickRegs<LPR>; ++s)
-    if (id[s] >= 0) picked[id[s]] = __builtin_bit_cast(uint32_t, d[s]);
+    if (id[s] >= 0) picked[id[s]] = d[s] == d[s] ? __builtin_bit_cast(uint32_t, d[s]) : 0x7FC00000u;
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   if (!live) return;
   E* out = static_cast<E*>(a.grad_logits) + t * a.E;

@@ -65,3 +65,18 @@ def test_gradients_of_rows_far_from_zero(E, k, dtype):
         got = pgg.moe_gate_grad(l.to(DEV), lse, ids, gp.to(DEV), grad_lse=gl.to(DEV), renorm=renorm, scale=2.5)
         bound = size * (far.amax(dim=1, keepdim=True) + E + 32) * 2.0 ** -22
         ref.assert_within(got, want, ref.rounded(want, bound, dt), f"renorm {renorm}")
+
+
+def test_a_nan_of_any_payload_is_a_gradient_like_others():
+    # a product keeps a NaN's payload, so any bits can reach the kernel
+    l = _logits(3, 20, 4)
+    ids, _, lse = pgg.moe_gate(l.to(DEV), 3)
+    for bits in (0x7FC00000, 0x7FC0DEAD, 0x7F80DEAD, 0x7FFFFFFF):
+        gp = torch.ones((3, 3))
+        gp.view(torch.int32)[1, 1] = bits
+        for renorm in (False, True):
+            grad = pgg.moe_gate_grad(l.to(DEV), lse, ids, gp.to(DEV), renorm=renorm)
+            assert grad[[0, 2]].isfinite().all()
+            assert grad[1].gather(0, ids[1]).isnan().all()
+            if not renorm:
+                assert grad[1].isnan().all()
