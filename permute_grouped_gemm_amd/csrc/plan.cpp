@@ -491,8 +491,8 @@ pgg_status check_gate_desc(const pgg_moe_gate_desc* d) {
   if (d->renorm != 0 && d->renorm != 1) return PGG_ERR_INVALID_ARG;
   if (d->dtype < PGG_F32 || d->dtype > PGG_BF16) return PGG_ERR_INVALID_ARG;
   // the picks of a row live in registers, and a launch of up to 64 lanes per
-  // row holds fewer than 2^32 lanes
-  if (d->experts > 8192 || d->topk > PGG_GATE_MAX_TOPK || d->tokens >= (int64_t(1) << 26))
+  // row, in workgroups of 4 rows, holds fewer than 2^32 lanes
+  if (d->experts > 8192 || d->topk > PGG_GATE_MAX_TOPK || d->tokens > (int64_t(1) << 26) - 4)
     return PGG_ERR_UNSUPPORTED;
   return PGG_OK;
 }

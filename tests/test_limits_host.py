@@ -1,0 +1,14 @@
+"""The largest sizes that fit a launch, from the descriptors alone (host only)."""
+import ctypes
+
+import permute_grouped_gemm_amd as pgg
+
+FAKE = 0x100000   # never dereferenced: every call is refused before a launch
+
+
+def test_gate_tokens_fit_a_launch():
+    # 4 rows to a workgroup of 256 lanes, fewer than 2^32 lanes
+    for tokens, status in (((1 << 26) - 4, pgg.ERR_INVALID_ARG), ((1 << 26) - 3, pgg.ERR_UNSUPPORTED)):
+        d = pgg.GateDesc(tokens, 1000, 2, 1.0, 0, 2, 0)
+        assert pgg.lib().pgg_moe_gate(ctypes.byref(d), None, None, FAKE, FAKE, FAKE, None) == status
+        assert pgg.lib().pgg_moe_gate_grad(ctypes.byref(d), None, FAKE, FAKE, FAKE, None, FAKE, None) == status
