@@ -683,7 +683,9 @@ pgg_status make_lora_plan(const pgg_lora_desc* d, LoraPlan* p) {
   q.dtype = d->dtype;
   const bool f32 = q.dtype == PGG_F32;
   auto tiles = [&](int64_t bm, int64_t bn) { return ((q.T + bm - 1) / bm) * ((q.N + bn - 1) / bn); };
-  if (tiles(32, 128) >= (int64_t(1) << 23)) return PGG_ERR_UNSUPPORTED;   // launches of fewer than 2^32 lanes
+  // launches of fewer than 2^32 lanes: 256 per tile at least, and 4096 per 256
+  // tokens for z, with one workgroup of 512 more
+  if (tiles(32, 128) >= (int64_t(1) << 23) || q.T > (int64_t(1) << 28) - 256) return PGG_ERR_UNSUPPORTED;
   // With few tokens the projection is bound by reading W: tiles of 32 or 64 rows,
   // the reduction split over about 512 workgroups, two per compute unit.  Above
   // that, the 256 x 256 tiles (one workgroup per compute unit) or the 128 x 128

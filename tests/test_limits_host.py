@@ -12,3 +12,10 @@ def test_gate_tokens_fit_a_launch():
         d = pgg.GateDesc(tokens, 1000, 2, 1.0, 0, 2, 0)
         assert pgg.lib().pgg_moe_gate(ctypes.byref(d), None, None, FAKE, FAKE, FAKE, None) == status
         assert pgg.lib().pgg_moe_gate_grad(ctypes.byref(d), None, FAKE, FAKE, FAKE, None, FAKE, None) == status
+
+
+def test_adapter_tokens_fit_a_launch():
+    # 8 x 512 lanes to 256 tokens, and one workgroup that checks the ids
+    for tokens, status in (((1 << 28) - 256, pgg.OK), ((1 << 28) - 255, pgg.ERR_UNSUPPORTED)):
+        n, d = ctypes.c_size_t(), pgg.LoraDesc(tokens, 64, 64, 2, 4, 2, 0)
+        assert pgg.lib().pgg_lora_workspace_size(ctypes.byref(d), ctypes.byref(n)) == status
