@@ -545,6 +545,8 @@ pgg_status make_glu_plan(const pgg_moe_glu_desc* d, Plan* p) {
   f.weight_dtype = d->weight_dtype;
   const pgg_status st = make_fwd_plan(&f, p);
   if (st != PGG_OK) return st;
+  // the kernels count the reduction in 32 bits, up to three stages past its end
+  if (d->x_cols > (int64_t(1) << 31) - 256) return PGG_ERR_UNSUPPORTED;
   // tiles of 128 rows and 128 columns where rows are not 16-byte aligned are four
   // times as many as the plan's; a launch holds fewer than 2^32 lanes
   if (int64_t(p->max_tiles) * p->n_col_tiles >= (int64_t(1) << 21)) return PGG_ERR_UNSUPPORTED;

@@ -19,3 +19,10 @@ def test_adapter_tokens_fit_a_launch():
     for tokens, status in (((1 << 28) - 256, pgg.OK), ((1 << 28) - 255, pgg.ERR_UNSUPPORTED)):
         n, d = ctypes.c_size_t(), pgg.LoraDesc(tokens, 64, 64, 2, 4, 2, 0)
         assert pgg.lib().pgg_lora_workspace_size(ctypes.byref(d), ctypes.byref(n)) == status
+
+
+def test_the_gated_products_reduction_stays_in_32_bits():
+    # the tiles count reduction elements in 32 bits, up to three stages of 64 past the end
+    for k, status in (((1 << 31) - 256, pgg.OK), ((1 << 31) - 255, pgg.ERR_UNSUPPORTED)):
+        n, d = ctypes.c_size_t(), pgg.GluDesc(1, k, 1, k, 16, 1, 1, 1, 1, 0, 2, 2, 0)
+        assert pgg.lib().pgg_moe_glu_workspace_size(ctypes.byref(d), ctypes.byref(n)) == status
