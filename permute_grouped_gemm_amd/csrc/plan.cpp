@@ -623,12 +623,13 @@ pgg_status make_glu_grad_plan(const pgg_moe_glu_grad_desc* d, Plan* p) {
   q.panel_cols = F;
   q.dtype = d->grad_y_dtype;
   q.regime = q.dtype == PGG_F32 ? kF32 : kLarge;
-  // m-tiles of 32 rows, 64 (16 bits) or the large ones.  Measured in us, 32 and
-  // 64 rows, 16 experts, F 1408:
-  //   bf16, D 4096: 24 rows per expert 60, 58; 32 58, 63; 48 70, 55; 60 86, 72
-  //   D 4095: 24 77, 72; 32 79, 85; 48 104, 81; 60 112, 94
-  //   f32, D 2048: 32 70, 101; 48 98, 92; 60 101, 115
-  q.bm = M <= (q.dtype == PGG_F32 ? 64 : 40) * G ? 32 : M <= 64 * G ? 64 : q.dtype == PGG_F32 ? 128 : 256;
+  // m-tiles of 32 rows, 64 or the large ones.  Measured in us, whole calls, 32 and
+  // 64 rows, F 1408 and 16 experts where not stated:
+  //   bf16, D 4096: 24 rows per expert 53, 61; 32 57, 65; 36 69, 65; 48 72, 58; 60 77, 62
+  //   D 4095: 24 73, 77; 32 75, 89; 36 101, 91; 48 103, 82; 60 109, 86
+  //   D 7168, F 2048, 60 experts: 32 355, 388; 36 429, 396; 60 467, 428
+  //   f32, D 2048: 32 63, 103; 40 96, 105; 48 98, 92; 60 98, 94
+  q.bm = M <= (q.dtype == PGG_F32 ? 40 : 32) * G ? 32 : M <= 64 * G ? 64 : q.dtype == PGG_F32 ? 128 : 256;
   q.bn = 128;
   const int64_t max_tiles = std::min<int64_t>(M, (M + q.bm - 1) / q.bm + G);   // each holds a row at least
   const int64_t col_tiles = (F + q.bn - 1) / q.bn;
