@@ -312,6 +312,26 @@ __device__ __forceinline__ void split_bf16(const float (&v)[8], u32x4_t& hi, u32
   __builtin_memcpy(&fin, f, 16);
 }
 
+// The same for 8 elements of B, which need no rounding: fp16 leaves at most 3 bits
+// after the first part's, bf16 none.  `fin` and the rest are those of the value
+// clamped to the type's range, finite and with its sign.
+template <class T>
+__device__ __forceinline__ void split_b(const typename T::elem (&b)[8], u32x4_t& hi, u32x4_t& lo, u32x4_t& fin) {
+  constexpr float kMost = __is_same(T, TF16) ? 65504.0f : 0x1.fep127f;
+  auto upper = [](float v) { return static_cast<uint16_t>(__builtin_bit_cast(uint32_t, v) >> 16); };
+  uint16_t h[8], l[8], f[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float v = to_float<T>(b[e]), c = __builtin_amdgcn_fmed3f(v, -kMost, kMost);
+    h[e] = upper(v);
+    f[e] = upper(c);
+    l[e] = upper(c - to_float<TBf16>(f[e]));
+  }
+  __builtin_memcpy(&hi, h, 16);
+  __builtin_memcpy(&lo, l, 16);
+  __builtin_memcpy(&fin, f, 16);
+}
+
 struct LoraOp {
   using Args = LoraArgs;
 
@@ -412,10 +432,7 @@ struct LoraOp {
           for (int j = 0; j < NJ; ++j) {
             u32x4_t bh, bl, bf;
             if constexpr (EPC == 8) {
-              float v[EPC];
-#pragma unroll
-              for (int e = 0; e < EPC; ++e) v[e] = to_float<T>(raw[j][e]);
-              split_bf16(v, bh, bl, bf);
+              split_b<T>(raw[j], bh, bl, bf);
             } else {
               __builtin_memcpy(&bh, raw[j], 16);
             }
