@@ -452,14 +452,15 @@ pgg_status pgg_moe_unpermute_grad(const pgg_moe_unpermute_desc* desc, const void
  *
  * expert_ids holds the experts of the topk largest logit + bias, larger first
  * and equal ones by lower index (the bias balances the choice and enters
- * nothing else).  probs[t, j] = scale * exp(logits[t, e_j] - lse[t]) with
+ * nothing else; it is added to the logit, so one trained against scores after
+ * the softmax or a sigmoid does not carry over).  probs[t, j] = scale * exp(logits[t, e_j] - lse[t]) with
  * renorm == 0; with renorm == 1 scale * the softmax over the chosen logits
  * alone.
- * A logit of -inf excludes an expert: it is chosen only after all others, with
- * weight 0; in a row of -inf the choice is experts 0..topk-1, all weights are
+ * A logit of -inf excludes an expert (the bias being finite): it is chosen only
+ * after all others, with weight 0; in a row of -inf the choice is experts 0..topk-1, all weights are
  * 0 and lse is -inf.  NaN counts as larger than any number, and a NaN or +inf
  * logit makes lse and every weight it enters NaN.
- * Limits: topk <= experts <= 8192 and topk <= PGG_GATE_MAX_TOPK.  No
+ * Limits: topk <= experts <= 8192, topk <= PGG_GATE_MAX_TOPK, tokens <= 2^26 - 4.  No
  * workspace; asynchronous; one kernel.  No output may alias an input.
  */
 #define PGG_GATE_MAX_TOPK 64
@@ -479,7 +480,8 @@ pgg_status pgg_moe_gate(const pgg_moe_gate_desc* desc, const void* logits, const
  * from grad_probs [tokens, topk] float32 and, unless NULL, grad_lse [tokens]
  * float32, with d_j = scale * grad_probs_j and p = softmax(logits),
  *
- *   renorm 0: grad_logits_e = p_e * (sum_{j: e_j = e} d_j - sum_j d_j p_{e_j}) + grad_lse p_e
+ *   renorm 0: grad_logits_e = p_e * (D_e - sum_j d_j p_{e_j}) + grad_lse p_e, where
+ *             D_e = d_j at the pick e_j = e and 0 at the other experts
  *   renorm 1: u = softmax of the chosen logits:
  *             grad_logits_{e_j} = u_j * (d_j - sum_m d_m u_m), plus grad_lse p_e for every e
  *
@@ -499,7 +501,8 @@ pgg_status pgg_moe_gate_grad(const pgg_moe_gate_desc* desc, const void* logits, 
  *   h[i, f]           = act(gate[i, f]) * up[i, f]
  *
  * for the expanded rows i, with p(i) and g(i) as for pgg_moe_fwd, whose
- * descriptor fields and constraints these are; weight_cols = 2F is even.
+ * descriptor fields and constraints these are; weight_cols = 2F is even and
+ * x_cols <= 2^31 - 256.
  *
  *   x [batch, K] dtype, weight [G, K, 2F] dtype, expanded_row_idx [M] int64,
  *   group_list [G] int64                                            inputs
@@ -580,9 +583,10 @@ pgg_status pgg_moe_glu_grad(const pgg_moe_glu_grad_desc* desc, const void* grad_
  * sets the workspace error word (PGG_DEV_ADAPTER_RANGE) and leaves y
  * unspecified.  Adapters of smaller rank are padded with zero rows.  A token's
  * row depends on its own x and adapter only, whatever values other adapters
- * hold.  fp32 accumulation; the inner product x * A_p^T stays in fp32 (16-bit
- * products take it as two bf16 parts, relative error 2^-16); one rounding.
- * Limit: rank <= PGG_LORA_MAX_RANK.  The workspace holds tokens x rank floats;
+ * hold.  fp32 accumulation; the inner product x * A_p^T stays in fp32 (calls of
+ * 16-bit types that do not split the reduction of x * W take it as two bf16 parts,
+ * relative error 2^-16; the others keep its 24 bits); one rounding.
+ * Limits: rank <= PGG_LORA_MAX_RANK, tokens <= 2^28 - 256.  The workspace holds tokens x rank floats;
  * where tiles alone do not fill the chip, fp32 partial results (at most 64 x
  * tokens x N floats, and at most about 512 tiles' worth); and where many rows of
  * x or weight are not 16-byte aligned, copies of them with padded rows.  Its

@@ -22,7 +22,7 @@
 //
 // Measured calls: 16384 rows x 7168 x 4096, bf16, 16 experts, 0.83 ms; 128 rows, 12
 // experts used, the same widths, 127 us; 128 rows, K 256, F 64, fp32, two launches
-// of 8 and 3.5 us.
+// of 7.6 and 2.0 us.
 #include <algorithm>
 
 #include "pgg_act.h"

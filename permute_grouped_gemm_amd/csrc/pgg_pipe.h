@@ -31,11 +31,14 @@
 // one wait for "at most 10" covers them, and no phase drains the queue.
 //
 // Measured, kernel time: gated product of 16384 rows x 7168 x 4096 in 16 experts,
-// bf16, products saved, 0.81 ms (1.19 PFLOP/s); gradient, NT, 110592 rows x 7168 x
-// 2048 in 60 experts, f16, 3.0 ms (1.08); adapters' projection, 13824 x 7168 x 2048,
-// f16, 0.40 ms (1.0: 432 tiles are 1.7 rounds of the chip).  Matrix instructions
-// fill 57-60 % of the cycles at a clock that falls to 1.7 GHz; the same calls on
-// all-zero operands run at 1.7-1.8 PFLOP/s.  What bounds it is the power limit.
+// bf16, products saved, 0.81-0.84 ms (1.15-1.19 PFLOP/s); gradient, NT, 110592 rows x
+// 7168 x 2048 in 60 experts, f16, 3.0 ms (1.08); adapters' projection, 13824 x 7168 x
+// 2048, f16, 0.40 ms (1.0: 432 tiles are 1.7 rounds of the chip).  Matrix
+// instructions fill 52-59 % of the cycles, at a clock that falls to 1.7 GHz; on
+// all-zero operands the same calls run at 1.7-1.8 PFLOP/s, so the power limit takes
+// a part.  It is not all of it: under the same limit a library product of the first
+// size, without activation and with one weight, runs at 1.31, and these kernels read
+// 2.8 GB where 1.0 is needed (the gradient 9.8 for 4.3).
 #pragma once
 
 #include "pgg_nn.h"
