@@ -162,7 +162,7 @@ pgg_status pgg_moe_dx_noalloc(const pgg_moe_dx_desc* desc, const void* grad_y, c
 /*
  * Read the device error word of the last pgg_moe_dx (or pgg_moe_fwd,
  * pgg_moe_dw, pgg_moe_routing, pgg_moe_unpermute[_grad], pgg_moe_glu[_grad],
- * pgg_lora_fwd) that used `workspace`.
+ * pgg_lora_fwd, pgg_moe_fwd_w4, pgg_moe_glu_w4, pgg_moe_combine[_grad]) that used `workspace`.
  * Synchronises `stream`.  Reads the workspace's first 64 bytes (the error
  * word's region), which every workspace of those calls holds.  *code
  * receives a pgg_device_error; *detail its detail value (may be NULL).  When several violations exist, the one with
@@ -604,6 +604,208 @@ pgg_status pgg_lora_workspace_size(const pgg_lora_desc* desc, size_t* bytes);
 pgg_status pgg_lora_fwd(const pgg_lora_desc* desc, const void* x, const void* weight, const void* a, const void* b,
                         const int64_t* adapter_ids, const float* scales, void* y, void* workspace,
                         size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The gate over experts in groups, from sigmoid or softmax scores:
+ *
+ *   s_e   = 1 / (1 + exp(-logits_e)), or softmax(logits)_e
+ *   key_e = s_e + bias_e            (the bias balances the choice and enters nothing else)
+ *
+ * The experts are `groups` runs of experts / groups neighbours.  A group's score
+ * is the sum of its two largest keys (of its one key where it has one expert),
+ * and expert_ids holds the experts with the topk largest keys of the topk_groups
+ * groups with the largest scores, larger first and equal ones by lower index.
+ * probs[t, j] = scale * s_{e_j}, with renorm scale * s_{e_j} / sum_m s_{e_m}.
+ *
+ *   logits      [tokens, experts]  dtype                            input
+ *   bias        [experts]          float32, or NULL                 input
+ *   expert_ids  [tokens, topk]     int64, distinct within a token   output
+ *   probs       [tokens, topk]     float32                          output
+ *
+ * The choice is made on keys of 64 bits, of which 42 bits of mantissa count (39
+ * with more than 1024 experts); the weights are computed in fp32.
+ * A logit of -inf excludes an expert: it adds nothing to its group's score, is
+ * chosen only after the others of the chosen groups, and has weight 0; a group
+ * without any other expert comes after those with one, and in a row of -inf the
+ * choice is experts 0..topk-1 with weights 0.  A key that is NaN counts as larger
+ * than any number, and a NaN logit makes every weight that it enters NaN.
+ * Constraints: groups divides experts, topk_groups <= groups, topk <=
+ * topk_groups * (experts / groups).  Limits: experts <= 8192, topk <=
+ * PGG_GATE_MAX_TOPK, groups <= PGG_GATE_MAX_GROUPS, tokens <= 2^26 - 4.  No
+ * workspace; asynchronous; one kernel.  No output may alias an input.
+ */
+#define PGG_GATE_MAX_GROUPS 64
+typedef enum { PGG_SCORE_SIGMOID = 0, PGG_SCORE_SOFTMAX = 1 } pgg_score;
+
+typedef struct {
+  int64_t tokens, experts, topk;
+  int64_t groups, topk_groups;
+  float scale;
+  int32_t score;           /* pgg_score */
+  int32_t renorm;          /* 0 or 1 */
+  int32_t dtype;           /* pgg_dtype of logits and grad_logits */
+} pgg_moe_gate_grouped_desc;
+
+pgg_status pgg_moe_gate_grouped(const pgg_moe_gate_grouped_desc* desc, const void* logits, const float* bias,
+                                int64_t* expert_ids, float* probs, hipStream_t stream);
+
+/*
+ * Its gradient with respect to the logits (the choice is constant), from
+ * grad_probs [tokens, topk] float32, with d_j = scale * grad_probs_j and w the
+ * weights before the scale:
+ *
+ *   sigmoid: at the picks d_j s_j (1 - s_j), with renorm w_j (1 - s_j) (d_j - sum_m d_m w_m);
+ *            0 at the other experts
+ *   softmax: p_e (D_e - sum_j d_j p_{e_j}) with p the softmax and D_e = d_j at the pick
+ *            e_j = e, 0 elsewhere; with renorm w_j (d_j - sum_m d_m w_m) at the picks, 0 elsewhere
+ *
+ * expert_ids is pgg_moe_gate_grouped's (a token's ids are distinct); every
+ * element of grad_logits [tokens, experts] (dtype) is written.  A row of -inf
+ * gets zeros.  An id outside [0, experts) selects nothing.  No workspace; one
+ * kernel.  The descriptor's constraints are the same.
+ */
+pgg_status pgg_moe_gate_grouped_grad(const pgg_moe_gate_grouped_desc* desc, const void* logits,
+                                     const int64_t* expert_ids, const float* grad_probs, void* grad_logits,
+                                     hipStream_t stream);
+
+/*
+ * Expert weights in 4 bits with a scale, and possibly a zero point, for every
+ * `group_size` successive rows of a column:
+ *
+ *   W[g, k, n] = (codes[g, k, n] - zeros[g, k / group_size, n]) * scales[g, k / group_size, n]
+ *
+ *   codes   [groups, rows, cols]     uint8, 0..15 (the low 4 bits count)
+ *   scales  [groups, S, cols]        dtype, S = ceil(rows / group_size)
+ *   zeros   [groups, S, cols]        uint8, 0..15 (likewise), or NULL: 8
+ *   packed                           the weights as the products read them
+ *
+ * pgg_w4_pack lays them out once; the packed buffer (256-byte aligned, of
+ * pgg_w4_pack_size bytes) is opaque and belongs to the descriptor that made it.
+ * With `gated` the columns are gate columns, then as many up columns, for
+ * pgg_moe_glu_w4; without, they are for pgg_moe_fwd_w4.
+ * group_size is 32, 64 or a multiple of 128; rows need not be a multiple of it.
+ */
+typedef struct {
+  int64_t groups, rows, cols;
+  int64_t group_size;
+  int32_t dtype;           /* pgg_dtype of scales, and of the products' x and results */
+  int32_t zeros;           /* 1: zero points are given, 0: they are 8 */
+  int32_t gated;           /* 0 or 1 */
+  int32_t reserved;        /* must be 0 */
+} pgg_w4_desc;
+
+pgg_status pgg_w4_pack_size(const pgg_w4_desc* desc, size_t* bytes);
+pgg_status pgg_w4_pack(const pgg_w4_desc* desc, const uint8_t* codes, const void* scales, const uint8_t* zeros,
+                       void* packed, hipStream_t stream);
+
+/*
+ * Products of the expanded rows with 4-bit weights:
+ *
+ *   pgg_moe_fwd_w4:  y[i, :] = x[p(i) / topK, :] * W[g(i)]                     [M, cols]
+ *   pgg_moe_glu_w4:  (gate | up)[i, :] = x[p(i) / topK, :] * W[g(i)],
+ *                    h[i, f] = act(gate[i, f]) * up[i, f]                      [M, cols / 2]
+ *
+ * with p(i) and g(i) as for pgg_moe_fwd.  expanded_row_idx may be NULL (idx_len
+ * 0, topk 1): then row i of x is expanded row i, as for an expert's second
+ * matrix.  x and the result are the weights' dtype.  Codes and zero points are
+ * multiplied exactly, as integers, and a group's sum is scaled and added in
+ * fp32; the result is rounded once.  (A group's sum of (code - zero) * x has to
+ * be finite in fp32.)
+ * The workspace holds the tables and, where the reduction is split, fp32
+ * partial results; where the rows of x are many and not 16-byte aligned, a copy
+ * of them with padded rows, and for many rows the rows' sums over 32 columns.
+ * Errors, alignment and workspace rules are pgg_moe_fwd's.
+ */
+typedef struct {
+  pgg_w4_desc weight;
+  int64_t x_rows, x_cols;
+  int64_t idx_len;         /* batch * topk, or 0: no expanded_row_idx */
+  int64_t group_list_len;
+  int64_t batch, topk;
+  int32_t row_idx_type;
+  int32_t act;             /* pgg_act (pgg_moe_glu_w4) */
+} pgg_moe_w4_desc;
+
+pgg_status pgg_moe_w4_workspace_size(const pgg_moe_w4_desc* desc, size_t* bytes);
+pgg_status pgg_moe_fwd_w4(const pgg_moe_w4_desc* desc, const void* x, const void* packed,
+                          const int64_t* expanded_row_idx, const int64_t* group_list, void* y, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream);
+pgg_status pgg_moe_glu_w4(const pgg_moe_w4_desc* desc, const void* x, const void* packed,
+                          const int64_t* expanded_row_idx, const int64_t* group_list, void* h, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The end of a block: the experts' rows summed per token, as pgg_moe_unpermute
+ * does, and what follows that sum:
+ *
+ *   c[t, :]      = sum_j probs[t, j] * permuted[row(t, j), :]
+ *   a[t, :]      = c / sqrt(mean(c^2) + eps) * post_weight      (c without post_weight)
+ *   out[t, :]    = residual_scale * residual[t, :] + gate[t] * a[t, :]   (gate 1 without it)
+ *   normed[t, :] = out / sqrt(mean(out^2) + eps) * next_weight  (the norm in front of the next block)
+ *
+ *   permuted  [M, H]  dtype                      input, M = batch * topk
+ *   expanded_row_idx [M] int64, row(t, j) as for pgg_moe_unpermute   input
+ *   probs     [batch, topk]  float32             input
+ *   residual  [batch, H]  dtype                  input
+ *   post_weight, next_weight [H] dtype, gate [batch] float32: each may be NULL    inputs
+ *   out       [batch, H]  dtype                  output
+ *   normed    [batch, H]  dtype                  output, NULL exactly when next_weight is
+ *
+ * fp32 arithmetic; `normed` comes from the unrounded out; each output is rounded
+ * once.  Sums run in a fixed order.  The routing index is checked on the device
+ * (out of range / not a permutation: the workspace error word; outputs
+ * unspecified).  Limits: hidden <= 16384, M < 2^31 - 1.  Alignment
+ * and workspace rules are pgg_moe_unpermute's.
+ */
+typedef struct {
+  int64_t batch, topk;
+  int64_t hidden;          /* H */
+  float residual_scale, eps;
+  int32_t row_idx_type;
+  int32_t dtype;           /* pgg_dtype of permuted, residual, the weights and the outputs */
+} pgg_moe_combine_desc;
+
+pgg_status pgg_moe_combine_workspace_size(const pgg_moe_combine_desc* desc, size_t* bytes);
+pgg_status pgg_moe_combine(const pgg_moe_combine_desc* desc, const void* permuted, const int64_t* expanded_row_idx,
+                           const float* probs, const void* residual, const void* post_weight, const float* gate,
+                           const void* next_weight, void* out, void* normed, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Its gradient, from grad_out [batch, H] and, exactly when next_weight is given,
+ * grad_normed [batch, H] (dtype); the inputs are the forward's, and what lies
+ * between is computed again:
+ *
+ *   grad_permuted    [M, H]         dtype      every row written
+ *   grad_probs       [batch, topk]  float32
+ *   grad_residual    [batch, H]     dtype
+ *   grad_gate        [batch]        float32    NULL exactly when gate is
+ *   grad_post_weight [H]            float32    NULL exactly when post_weight is
+ *   grad_next_weight [H]            float32    NULL exactly when next_weight is
+ *
+ * Everything is added in a fixed order: repeated calls give the same bits.
+ */
+typedef struct {
+  const void* grad_out;
+  const void* grad_normed;
+  const void* permuted;
+  const int64_t* expanded_row_idx;
+  const float* probs;
+  const void* residual;
+  const void* post_weight;
+  const float* gate;
+  const void* next_weight;
+  void* grad_permuted;
+  float* grad_probs;
+  void* grad_residual;
+  float* grad_gate;
+  float* grad_post_weight;
+  float* grad_next_weight;
+} pgg_moe_combine_grad_args;
+
+pgg_status pgg_moe_combine_grad_workspace_size(const pgg_moe_combine_desc* desc, size_t* bytes);
+pgg_status pgg_moe_combine_grad(const pgg_moe_combine_desc* desc, const pgg_moe_combine_grad_args* args,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 const char* pgg_status_string(pgg_status status);
 const char* pgg_device_error_string(int32_t code);

@@ -40,6 +40,17 @@ gradients, and
 is a projection that all tokens share with a low-rank adapter per token
 beside it.
 
+    expert_ids, probs = moe_gate_grouped(logits, topk, score="sigmoid", groups=8, topk_groups=4, bias=bias)
+    weight = w4_pack(codes, scales, group_size, zeros=zeros, gated=True)
+    h = moe_glu_w4(x, weight, expanded_row_idx, group_list, topk)
+    y = moe_fwd_w4(h, weight_out, None, group_list)
+    out, normed = moe_combine(y, eri_scatter, probs, residual, row_idx_type=1, post_weight=w1, next_weight=w2)
+
+are the router over experts in groups, the experts' products with 4-bit weights
+(serving), and unpermute fused with the norm, the residual stream and the next
+block's norm behind it; moe_gate_grouped_grad and moe_combine_grad are the
+gradients.
+
 Every call runs on the current stream of the current device, on which its
 tensors have to be, or on ``stream``.  The caller orders that stream behind the
 work that makes the inputs (``stream.wait_stream``) and later uses of the
@@ -60,6 +71,8 @@ __all__ = [
     "moe_dw", "dw_workspace_size", "dw_kernel_time", "moe_routing", "moe_unpermute",
     "moe_unpermute_grad", "moe_gate", "moe_gate_grad", "moe_glu", "glu_workspace_size", "moe_glu_grad",
     "glu_grad_workspace_size", "lora_fwd", "lora_workspace_size",
+    "moe_gate_grouped", "moe_gate_grouped_grad", "W4Weight", "w4_pack", "w4_workspace_size", "moe_fwd_w4",
+    "moe_glu_w4", "moe_combine", "combine_workspace_size", "moe_combine_grad", "combine_grad_workspace_size",
     "KernelTimer", "PggError", "lib", "LIB_PATH", "HEADER_PATH",
 ]
 
@@ -72,6 +85,7 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE_TOO_SMALL, ERR_HIP, ERR_MISA
  DEV_ADAPTER_RANGE) = range(7)
 DTYPE_CODE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 ACT_CODE = {"silu": 0, "gelu_tanh": 1}
+SCORE_CODE = {"sigmoid": 0, "softmax": 1}
 
 
 class Desc(ctypes.Structure):
@@ -146,6 +160,45 @@ class LoraDesc(ctypes.Structure):
         ("adapters", ctypes.c_int64), ("rank", ctypes.c_int64), ("dtype", ctypes.c_int32),
         ("reserved", ctypes.c_int32),
     ]
+
+
+class GateGroupedDesc(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int64), ("experts", ctypes.c_int64), ("topk", ctypes.c_int64),
+        ("groups", ctypes.c_int64), ("topk_groups", ctypes.c_int64), ("scale", ctypes.c_float),
+        ("score", ctypes.c_int32), ("renorm", ctypes.c_int32), ("dtype", ctypes.c_int32),
+    ]
+
+
+class W4Desc(ctypes.Structure):
+    _fields_ = [
+        ("groups", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+        ("group_size", ctypes.c_int64), ("dtype", ctypes.c_int32), ("zeros", ctypes.c_int32),
+        ("gated", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
+
+
+class MoeW4Desc(ctypes.Structure):
+    _fields_ = [
+        ("weight", W4Desc), ("x_rows", ctypes.c_int64), ("x_cols", ctypes.c_int64), ("idx_len", ctypes.c_int64),
+        ("group_list_len", ctypes.c_int64), ("batch", ctypes.c_int64), ("topk", ctypes.c_int64),
+        ("row_idx_type", ctypes.c_int32), ("act", ctypes.c_int32),
+    ]
+
+
+class CombineDesc(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64), ("topk", ctypes.c_int64), ("hidden", ctypes.c_int64),
+        ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float), ("row_idx_type", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class CombineGradArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "grad_out", "grad_normed", "permuted", "expanded_row_idx", "probs", "residual", "post_weight", "gate",
+        "next_weight", "grad_permuted", "grad_probs", "grad_residual", "grad_gate", "grad_post_weight",
+        "grad_next_weight")]
 
 
 class Plan(ctypes.Structure):
@@ -226,6 +279,19 @@ def lib():
         PA = ctypes.POINTER(LoraDesc)
         L.pgg_lora_workspace_size.argtypes = [PA, ctypes.POINTER(sz)]
         L.pgg_lora_fwd.argtypes = [PA, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        PGG = ctypes.POINTER(GateGroupedDesc)
+        L.pgg_moe_gate_grouped.argtypes = [PGG, vp, vp, vp, vp, vp]
+        L.pgg_moe_gate_grouped_grad.argtypes = [PGG, vp, vp, vp, vp, vp]
+        PW, PM, PC = ctypes.POINTER(W4Desc), ctypes.POINTER(MoeW4Desc), ctypes.POINTER(CombineDesc)
+        L.pgg_w4_pack_size.argtypes = [PW, ctypes.POINTER(sz)]
+        L.pgg_w4_pack.argtypes = [PW, vp, vp, vp, vp, vp]
+        L.pgg_moe_w4_workspace_size.argtypes = [PM, ctypes.POINTER(sz)]
+        L.pgg_moe_fwd_w4.argtypes = [PM, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.pgg_moe_glu_w4.argtypes = [PM, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.pgg_moe_combine_workspace_size.argtypes = [PC, ctypes.POINTER(sz)]
+        L.pgg_moe_combine_grad_workspace_size.argtypes = [PC, ctypes.POINTER(sz)]
+        L.pgg_moe_combine.argtypes = [PC, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.pgg_moe_combine_grad.argtypes = [PC, ctypes.POINTER(CombineGradArgs), vp, sz, vp]
         L.pgg_timing_begin.argtypes = [i32]
         L.pgg_timing_end.argtypes = [ctypes.POINTER(KernelTime), i32, ctypes.POINTER(i32)]
         L.pgg_status_string.argtypes = [ctypes.c_int]
@@ -242,6 +308,10 @@ def lib():
                   "pgg_moe_unpermute_grad", "pgg_moe_gate", "pgg_moe_gate_grad",
                   "pgg_moe_glu_workspace_size", "pgg_moe_glu", "pgg_moe_glu_grad_workspace_size",
                   "pgg_moe_glu_grad", "pgg_lora_workspace_size", "pgg_lora_fwd",
+                  "pgg_moe_gate_grouped", "pgg_moe_gate_grouped_grad", "pgg_w4_pack_size", "pgg_w4_pack",
+                  "pgg_moe_w4_workspace_size", "pgg_moe_fwd_w4", "pgg_moe_glu_w4",
+                  "pgg_moe_combine_workspace_size", "pgg_moe_combine_grad_workspace_size", "pgg_moe_combine",
+                  "pgg_moe_combine_grad",
                   "pgg_timing_begin", "pgg_timing_end"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
@@ -1015,6 +1085,265 @@ def lora_fwd(x: torch.Tensor, weight: torch.Tensor, a: torch.Tensor, b: torch.Te
                               adapter_ids.data_ptr(), scales.data_ptr(), out.data_ptr(), ws.data_ptr(),
                               _ws_bytes(ws), _on_stream(stream, dev)), "pgg_lora_fwd")
     return out
+
+
+# ---------------------------------------------------------------- gate over groups, 4-bit weights, combination
+
+def _grouped_desc(logits, k, score, groups, topk_groups, renorm, scale) -> GateGroupedDesc:
+    code = _value_type(logits, "logits", 2)
+    if score not in SCORE_CODE:
+        raise PggError(ERR_INVALID_ARG, f"score must be one of {sorted(SCORE_CODE)}")
+    T, E = logits.shape
+    kept = int(groups) if topk_groups is None else int(topk_groups)
+    return GateGroupedDesc(T, E, int(k), int(groups), kept, float(scale), SCORE_CODE[score], int(bool(renorm)), code)
+
+
+def moe_gate_grouped(logits: torch.Tensor, topk: int, *, score: str = "sigmoid", groups: int = 1,
+                     topk_groups: Optional[int] = None, bias: Optional[torch.Tensor] = None, renorm: bool = True,
+                     scale: float = 1.0, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The router's gate over experts in groups: (expert_ids [T, topk] int64,
+    probs [T, topk] float32) from logits [T, E] (asynchronous).
+
+    Scores are the sigmoid or the softmax of the logits; ``bias`` [E] float32 is
+    added to the score for the choice only.  The E experts are ``groups`` runs of
+    neighbours; a group's score is the sum of its two largest keys (score +
+    bias), and the experts are those of the topk largest keys of the
+    ``topk_groups`` best groups (default: all), larger first and equal ones by
+    lower index.  probs = scale * score, with ``renorm`` divided by the chosen
+    scores' sum.  A logit of -inf excludes an expert: it comes after the others of
+    the chosen groups and gets weight 0.  Limits: E <= 8192, topk <= 64, groups <= 64."""
+    d = _grouped_desc(logits, topk, score, groups, topk_groups, renorm, scale)
+    T, E, k = d.tokens, d.experts, d.topk
+    dev = logits.device
+    if bias is not None:
+        _expect(bias, "bias", (E,), torch.float32, dev)
+    if T <= 0 or not 0 < k <= E:
+        raise PggError(ERR_INVALID_ARG, "moe_gate_grouped needs tokens and 0 < topk <= experts")
+    ids = _fresh((T, k), torch.int64, dev, stream)
+    probs = _fresh((T, k), torch.float32, dev, stream)
+    _check(lib().pgg_moe_gate_grouped(ctypes.byref(d), logits.data_ptr(), _ptr(bias), ids.data_ptr(),
+                                      probs.data_ptr(), _on_stream(stream, dev)), "pgg_moe_gate_grouped")
+    return ids, probs
+
+
+def moe_gate_grouped_grad(logits: torch.Tensor, expert_ids: torch.Tensor, grad_probs: torch.Tensor, *,
+                          score: str = "sigmoid", renorm: bool = True, scale: float = 1.0,
+                          out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of moe_gate_grouped: grad_logits [T, E] in logits' dtype from
+    grad_probs [T, topk] float32.  ``expert_ids`` is moe_gate_grouped's, ``score``,
+    ``renorm`` and ``scale`` its arguments; the groups and the bias enter the
+    choice only."""
+    if expert_ids.dim() != 2:
+        raise PggError(ERR_INVALID_ARG, "expert_ids must be an int64 [tokens, topk] tensor")
+    d = _grouped_desc(logits, expert_ids.shape[1], score, 1, 1, renorm, scale)
+    dev, shape = logits.device, (d.tokens, d.topk)
+    _expect(expert_ids, "expert_ids", shape, torch.int64, dev)
+    _expect(grad_probs, "grad_probs", shape, torch.float32, dev)
+    out = _out(out, "out", (d.tokens, d.experts), logits.dtype, dev, stream)
+    _check(lib().pgg_moe_gate_grouped_grad(ctypes.byref(d), logits.data_ptr(), expert_ids.data_ptr(),
+                                           grad_probs.data_ptr(), out.data_ptr(), _on_stream(stream, dev)),
+           "pgg_moe_gate_grouped_grad")
+    return out
+
+
+class W4Weight:
+    """Expert weights in 4 bits as w4_pack lays them out: ``data`` (uint8, opaque)
+    and what it holds: ``shape`` (G, K, N), ``group_size``, ``dtype``, ``gated``."""
+
+    def __init__(self, data: torch.Tensor, desc: W4Desc, dtype: torch.dtype):
+        self.data, self.desc, self.dtype = data, desc, dtype
+
+    @property
+    def shape(self) -> Tuple[int, int, int]:
+        return self.desc.groups, self.desc.rows, self.desc.cols
+
+    @property
+    def group_size(self) -> int:
+        return self.desc.group_size
+
+    @property
+    def gated(self) -> bool:
+        return bool(self.desc.gated)
+
+
+def w4_pack(codes: torch.Tensor, scales: torch.Tensor, group_size: int, *, zeros: Optional[torch.Tensor] = None,
+            gated: bool = False, stream=None) -> W4Weight:
+    """Lays out expert weights W = (codes - zeros) * scales for moe_fwd_w4 or, with
+    ``gated`` (gate columns, then up columns), moe_glu_w4 (asynchronous).
+
+    codes [G, K, N] uint8 of 0..15; scales [G, ceil(K / group_size), N] float32,
+    float16 or bfloat16, the type that x and the results will have; zeros like
+    scales, uint8 of 0..15 (default: 8 everywhere).  group_size is 32, 64 or a
+    multiple of 128.  Done once, when the weights are loaded."""
+    if codes.dim() != 3 or codes.dtype != torch.uint8 or not codes.is_cuda or not codes.is_contiguous():
+        raise PggError(ERR_INVALID_ARG, "codes must be a contiguous uint8 [G, K, N] GPU tensor")
+    code = _value_type(scales, "scales", 3)
+    G, K, N = codes.shape
+    dev = codes.device
+    d = W4Desc(G, K, N, int(group_size), code, int(zeros is not None), int(bool(gated)), 0)
+    size = _size_of(lib().pgg_w4_pack_size, d, "w4_pack")
+    shape = (G, -(-K // int(group_size)), N)
+    _expect(scales, "scales", shape, scales.dtype, dev)
+    if zeros is not None:
+        _expect(zeros, "zeros", shape, torch.uint8, dev)
+    data = _fresh((size,), torch.uint8, dev, stream)
+    _check(lib().pgg_w4_pack(ctypes.byref(d), codes.data_ptr(), scales.data_ptr(), _ptr(zeros), data.data_ptr(),
+                             _on_stream(stream, dev)), "pgg_w4_pack")
+    return W4Weight(data, d, scales.dtype)
+
+
+def _w4_desc(x, weight, eri, group_list, topk, row_idx_type, act) -> MoeW4Desc:
+    if not isinstance(weight, W4Weight):
+        raise PggError(ERR_INVALID_ARG, "weight must be w4_pack's")
+    _value_type(x, "x", 2)
+    dev, (G, K, _) = x.device, weight.shape
+    if x.dtype != weight.dtype or x.shape[1] != K or weight.data.device != dev:
+        raise PggError(ERR_INVALID_ARG, f"x must be a {weight.dtype} [batch, {K}] tensor on {weight.data.device}")
+    M = x.shape[0] * int(topk)
+    _expect(group_list, "group_list", (G,), torch.int64, dev)
+    if eri is not None:
+        _expect(eri, "expanded_row_idx", (M,), torch.int64, dev)
+    return MoeW4Desc(weight.desc, x.shape[0], x.shape[1], 0 if eri is None else M, G, x.shape[0], int(topk),
+                     int(row_idx_type), _act_code(act))
+
+
+def w4_workspace_size(x, weight, expanded_row_idx, group_list, topk=1, row_idx_type=0) -> int:
+    d = _w4_desc(x, weight, expanded_row_idx, group_list, topk, row_idx_type, "silu")
+    return _size_of(lib().pgg_moe_w4_workspace_size, d, "w4_workspace_size")
+
+
+def _run_w4(call, name, x, weight, eri, group_list, topk, row_idx_type, act, cols, out, workspace, stream):
+    d = _w4_desc(x, weight, eri, group_list, topk, row_idx_type, act)
+    dev = x.device
+    ws = _scratch(workspace, lambda: _size_of(lib().pgg_moe_w4_workspace_size, d, "w4_workspace_size"), dev, stream)
+    out = _out(out, "out", (d.batch * d.topk, cols), x.dtype, dev, stream)
+    _check(call(ctypes.byref(d), x.data_ptr(), weight.data.data_ptr(), _ptr(eri), group_list.data_ptr(),
+                out.data_ptr(), ws.data_ptr(), _ws_bytes(ws), _on_stream(stream, dev)), name)
+    return out
+
+
+def moe_fwd_w4(x: torch.Tensor, weight: W4Weight, expanded_row_idx: Optional[torch.Tensor], group_list: torch.Tensor,
+               topk: int = 1, row_idx_type: int = 0, *, out: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """moe_fwd with 4-bit weights: y [batch*topk, N] in x's dtype (asynchronous).
+
+    x [batch, K] in the weights' dtype; expanded_row_idx [batch*topk] and
+    group_list [G] int64 as for moe_fwd, or expanded_row_idx None (topk 1) where
+    the rows of x are in expert order already, as for an expert's second matrix."""
+    if not isinstance(weight, W4Weight) or weight.gated:
+        raise PggError(ERR_INVALID_ARG, "moe_fwd_w4 takes weights packed without gated")
+    return _run_w4(lib().pgg_moe_fwd_w4, "pgg_moe_fwd_w4", x, weight, expanded_row_idx, group_list, topk,
+                   row_idx_type, "silu", weight.shape[2], out, workspace, stream)
+
+
+def moe_glu_w4(x: torch.Tensor, weight: W4Weight, expanded_row_idx: Optional[torch.Tensor], group_list: torch.Tensor,
+               topk: int = 1, row_idx_type: int = 0, *, act: str = "silu", out: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """moe_glu with 4-bit weights, packed with ``gated``: h [batch*topk, N/2] =
+    act(gate) * up in x's dtype (asynchronous).  Arguments as for moe_fwd_w4."""
+    if not isinstance(weight, W4Weight) or not weight.gated:
+        raise PggError(ERR_INVALID_ARG, "moe_glu_w4 takes weights packed with gated")
+    return _run_w4(lib().pgg_moe_glu_w4, "pgg_moe_glu_w4", x, weight, expanded_row_idx, group_list, topk,
+                   row_idx_type, act, weight.shape[2] // 2, out, workspace, stream)
+
+
+def _combine_desc(permuted, probs, row_idx_type, residual_scale, eps) -> CombineDesc:
+    code = _value_type(permuted, "permuted", 2)
+    if probs.dim() != 2:
+        raise PggError(ERR_INVALID_ARG, "probs must be a float32 [batch, topk] tensor")
+    batch, topk = probs.shape
+    _expect(permuted, "permuted", (batch * topk, permuted.shape[1]), permuted.dtype, permuted.device)
+    _expect(probs, "probs", (batch, topk), torch.float32, permuted.device)
+    return CombineDesc(batch, topk, permuted.shape[1], float(residual_scale), float(eps), int(row_idx_type), code)
+
+
+def combine_workspace_size(permuted, probs, *, row_idx_type=0) -> int:
+    return _size_of(lib().pgg_moe_combine_workspace_size, _combine_desc(permuted, probs, row_idx_type, 1.0, 1e-6),
+                    "combine_workspace_size")
+
+
+def combine_grad_workspace_size(permuted, probs, *, row_idx_type=0) -> int:
+    return _size_of(lib().pgg_moe_combine_grad_workspace_size,
+                    _combine_desc(permuted, probs, row_idx_type, 1.0, 1e-6), "combine_grad_workspace_size")
+
+
+def _check_combine(d, permuted, eri, residual, post_weight, gate, next_weight):
+    dev, dtype, H = permuted.device, permuted.dtype, d.hidden
+    _expect(eri, "expanded_row_idx", (d.batch * d.topk,), torch.int64, dev)
+    _expect(residual, "residual", (d.batch, H), dtype, dev)
+    for t, name in ((post_weight, "post_weight"), (next_weight, "next_weight")):
+        if t is not None:
+            _expect(t, name, (H,), dtype, dev)
+    if gate is not None:
+        _expect(gate, "gate", (d.batch,), torch.float32, dev)
+
+
+def moe_combine(permuted: torch.Tensor, expanded_row_idx: torch.Tensor, probs: torch.Tensor, residual: torch.Tensor, *,
+                row_idx_type: int = 0, post_weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                residual_scale: float = 1.0, next_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                out: Optional[torch.Tensor] = None, normed: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None, stream=None):
+    """The end of a block: unpermute with probs, then the norm of the sum, the
+    residual stream and the norm in front of the next block (asynchronous):
+
+        c = sum over slots of probs * the token's expert rows
+        a = c / sqrt(mean(c^2) + eps) * post_weight         (c without post_weight)
+        out = residual_scale * residual + gate * a          (gate 1 without it)
+        normed = out / sqrt(mean(out^2) + eps) * next_weight
+
+    permuted [batch*topk, H], residual [batch, H], post_weight and next_weight [H]
+    share one of float32 / float16 / bfloat16; probs [batch, topk] and gate
+    [batch] are float32; expanded_row_idx [batch*topk] int64 as for
+    moe_unpermute (row_idx_type 1 needs one launch less).  Returns out, with
+    next_weight (out, normed).  H <= 16384."""
+    d = _combine_desc(permuted, probs, row_idx_type, residual_scale, eps)
+    _check_combine(d, permuted, expanded_row_idx, residual, post_weight, gate, next_weight)
+    dev, shape = permuted.device, (d.batch, d.hidden)
+    ws = _scratch(workspace, lambda: _size_of(lib().pgg_moe_combine_workspace_size, d, "combine_workspace_size"), dev,
+                  stream)
+    if normed is not None and next_weight is None:
+        raise PggError(ERR_INVALID_ARG, "normed needs next_weight")
+    out = _out(out, "out", shape, permuted.dtype, dev, stream)
+    if next_weight is not None:
+        normed = _out(normed, "normed", shape, permuted.dtype, dev, stream)
+    _check(lib().pgg_moe_combine(ctypes.byref(d), permuted.data_ptr(), expanded_row_idx.data_ptr(), probs.data_ptr(),
+                                 residual.data_ptr(), _ptr(post_weight), _ptr(gate), _ptr(next_weight),
+                                 out.data_ptr(), _ptr(normed), ws.data_ptr(), _ws_bytes(ws),
+                                 _on_stream(stream, dev)), "pgg_moe_combine")
+    return out if normed is None else (out, normed)
+
+
+def moe_combine_grad(grad_out: torch.Tensor, permuted: torch.Tensor, expanded_row_idx: torch.Tensor,
+                     probs: torch.Tensor, residual: torch.Tensor, *, grad_normed: Optional[torch.Tensor] = None,
+                     row_idx_type: int = 0, post_weight: Optional[torch.Tensor] = None,
+                     gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
+                     next_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of moe_combine from grad_out and, exactly with next_weight,
+    grad_normed [batch, H]: (grad_permuted [batch*topk, H], grad_probs [batch,
+    topk] float32, grad_residual [batch, H], grad_gate [batch] float32,
+    grad_post_weight [H] float32, grad_next_weight [H] float32), None where the
+    input is.  The other arguments are moe_combine's; nothing else is kept from it."""
+    d = _combine_desc(permuted, probs, row_idx_type, residual_scale, eps)
+    _check_combine(d, permuted, expanded_row_idx, residual, post_weight, gate, next_weight)
+    dev, dtype, H = permuted.device, permuted.dtype, d.hidden
+    _expect(grad_out, "grad_out", (d.batch, H), dtype, dev)
+    if (grad_normed is None) != (next_weight is None):
+        raise PggError(ERR_INVALID_ARG, "grad_normed and next_weight come together")
+    if grad_normed is not None:
+        _expect(grad_normed, "grad_normed", (d.batch, H), dtype, dev)
+    ws = _scratch(workspace, lambda: _size_of(lib().pgg_moe_combine_grad_workspace_size, d,
+                                              "combine_grad_workspace_size"), dev, stream)
+    fresh = lambda shape, dt: _fresh(shape, dt, dev, stream)  # noqa: E731
+    grads = (fresh((d.batch * d.topk, H), dtype), fresh((d.batch, d.topk), torch.float32), fresh((d.batch, H), dtype),
+             None if gate is None else fresh((d.batch,), torch.float32),
+             None if post_weight is None else fresh((H,), torch.float32),
+             None if next_weight is None else fresh((H,), torch.float32))
+    args = CombineGradArgs(*(_ptr(t) for t in (grad_out, grad_normed, permuted, expanded_row_idx, probs, residual,
+                                               post_weight, gate, next_weight) + grads))
+    _check(lib().pgg_moe_combine_grad(ctypes.byref(d), ctypes.byref(args), ws.data_ptr(), _ws_bytes(ws),
+                                      _on_stream(stream, dev)), "pgg_moe_combine_grad")
+    return grads
 
 
 class KernelTimer:

@@ -1,7 +1,8 @@
 // C ABI of the fused MoE d_x backward, of the layer's forward, of its weight
 // gradient, of on-device routing, of unpermute and its gradient, of the
-// router's gate, of the gated products and of the low-rank adapters (declared
-// in include/pgg.h).
+// router's gates, of the gated products, of the low-rank adapters, of the 4-bit
+// products and of the combination with the residual stream (declared in
+// include/pgg.h).
 //
 // The execute call validates the descriptor on the host, lays out the
 // workspace, and enqueues on the caller's stream:
@@ -663,6 +664,180 @@ pgg_status pgg_lora_fwd(const pgg_lora_desc* desc, const void* x, const void* we
   TimedLaunch t("lora", stream);
   return launch_lora(p, x, weight, a, b, adapter_ids, scales, y, workspace, stream) == hipSuccess
              ? PGG_OK : PGG_ERR_HIP;
+}
+
+pgg_status pgg_moe_gate_grouped(const pgg_moe_gate_grouped_desc* desc, const void* logits, const float* bias,
+                                int64_t* expert_ids, float* probs, hipStream_t stream) {
+  const pgg_status st = check_gate_grouped_desc(desc);
+  if (st != PGG_OK) return st;
+  if (!logits || !expert_ids || !probs) return PGG_ERR_INVALID_ARG;
+  if (!is_aligned(logits, elem_size(desc->dtype)) || !is_aligned(bias, 4) || !is_aligned(expert_ids, 8) ||
+      !is_aligned(probs, 4))
+    return PGG_ERR_MISALIGNED;
+  TimedLaunch t("gate_grouped", stream);
+  return launch_gate_grouped(*desc, logits, bias, expert_ids, probs, stream) == hipSuccess ? PGG_OK : PGG_ERR_HIP;
+}
+
+pgg_status pgg_moe_gate_grouped_grad(const pgg_moe_gate_grouped_desc* desc, const void* logits,
+                                     const int64_t* expert_ids, const float* grad_probs, void* grad_logits,
+                                     hipStream_t stream) {
+  const pgg_status st = check_gate_grouped_desc(desc);
+  if (st != PGG_OK) return st;
+  if (!logits || !expert_ids || !grad_probs || !grad_logits) return PGG_ERR_INVALID_ARG;
+  const size_t es = elem_size(desc->dtype);
+  if (!is_aligned(logits, es) || !is_aligned(grad_logits, es) || !is_aligned(expert_ids, 8) ||
+      !is_aligned(grad_probs, 4))
+    return PGG_ERR_MISALIGNED;
+  TimedLaunch t("gate_grouped_grad", stream);
+  return launch_gate_grouped_grad(*desc, logits, expert_ids, grad_probs, grad_logits, stream) == hipSuccess
+             ? PGG_OK : PGG_ERR_HIP;
+}
+
+pgg_status pgg_w4_pack_size(const pgg_w4_desc* desc, size_t* bytes) {
+  if (!bytes) return PGG_ERR_INVALID_ARG;
+  W4Layout l;
+  const pgg_status st = make_w4_layout(desc, &l);
+  if (st != PGG_OK) return st;
+  *bytes = l.total;
+  return PGG_OK;
+}
+
+pgg_status pgg_w4_pack(const pgg_w4_desc* desc, const uint8_t* codes, const void* scales, const uint8_t* zeros,
+                       void* packed, hipStream_t stream) {
+  W4Layout l;
+  const pgg_status st = make_w4_layout(desc, &l);
+  if (st != PGG_OK) return st;
+  if (!codes || !scales || !packed || (zeros != nullptr) != (l.zeros != 0)) return PGG_ERR_INVALID_ARG;
+  if (!is_aligned(scales, elem_size(l.dtype)) || !is_aligned(packed, kWorkspaceAlign)) return PGG_ERR_MISALIGNED;
+  TimedLaunch t("w4_pack", stream);
+  return launch_w4_pack(l, codes, scales, zeros, packed, stream) == hipSuccess ? PGG_OK : PGG_ERR_HIP;
+}
+
+pgg_status pgg_moe_w4_workspace_size(const pgg_moe_w4_desc* desc, size_t* bytes) {
+  if (!desc || !bytes) return PGG_ERR_INVALID_ARG;
+  W4Plan p;
+  const pgg_status st = make_w4_plan(desc, desc->weight.gated != 0, &p);
+  if (st != PGG_OK) return st;
+  *bytes = p.base.total;
+  return PGG_OK;
+}
+
+static pgg_status run_w4(const pgg_moe_w4_desc* desc, bool gated, const void* x, const void* packed,
+                         const int64_t* eri, const int64_t* group_list, void* out, void* workspace,
+                         size_t workspace_bytes, hipStream_t stream) {
+  W4Plan p;
+  const pgg_status st = make_w4_plan(desc, gated, &p);
+  if (st != PGG_OK) return st;
+  if (!x || !packed || !group_list || !out || !workspace || (eri != nullptr) != (desc->idx_len != 0))
+    return PGG_ERR_INVALID_ARG;
+  if (workspace_bytes < p.base.total) return PGG_ERR_WORKSPACE_TOO_SMALL;
+  const size_t es = elem_size(p.base.dtype);
+  if (!is_aligned(workspace, kWorkspaceAlign) || !is_aligned(packed, kWorkspaceAlign) || !is_aligned(eri, 8) ||
+      !is_aligned(group_list, 8) || !is_aligned(x, es) || !is_aligned(out, es))
+    return PGG_ERR_MISALIGNED;
+  const WsView w = ws_view(p.base, workspace);
+  hipError_t e = hipSuccess;
+  if (p.base.local) {
+    // the tiles find their rows themselves
+  } else if (!eri) {
+    TimedLaunch t("prep_groups", stream);
+    e = launch_prep_groups(p.base, group_list, w, stream);
+  } else if (p.base.fused_prep) {
+    TimedLaunch t("prep_fused", stream);
+    e = launch_prep_fused(p.base, eri, group_list, w, stream);
+  } else {
+    {
+      TimedLaunch t("prep_tables", stream);
+      e = launch_prep_tables(p.base, eri, group_list, w, stream);
+    }
+    if (e == hipSuccess) {
+      TimedLaunch t("prep_check", stream);
+      e = launch_prep_check(p.base, eri, w, stream);
+    }
+  }
+  if (e == hipSuccess) {
+    TimedLaunch t("w4", stream);
+    e = launch_w4(p, desc->act, x, packed, eri, group_list, out, workspace, stream);
+  }
+  return e == hipSuccess ? PGG_OK : PGG_ERR_HIP;
+}
+
+pgg_status pgg_moe_fwd_w4(const pgg_moe_w4_desc* desc, const void* x, const void* packed,
+                          const int64_t* expanded_row_idx, const int64_t* group_list, void* y, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream) {
+  return run_w4(desc, false, x, packed, expanded_row_idx, group_list, y, workspace, workspace_bytes, stream);
+}
+
+pgg_status pgg_moe_glu_w4(const pgg_moe_w4_desc* desc, const void* x, const void* packed,
+                          const int64_t* expanded_row_idx, const int64_t* group_list, void* h, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream) {
+  return run_w4(desc, true, x, packed, expanded_row_idx, group_list, h, workspace, workspace_bytes, stream);
+}
+
+pgg_status pgg_moe_combine_workspace_size(const pgg_moe_combine_desc* desc, size_t* bytes) {
+  if (!bytes) return PGG_ERR_INVALID_ARG;
+  CombinePlan p;
+  const pgg_status st = make_combine_plan(desc, &p);
+  if (st != PGG_OK) return st;
+  *bytes = p.total_fwd;
+  return PGG_OK;
+}
+
+pgg_status pgg_moe_combine_grad_workspace_size(const pgg_moe_combine_desc* desc, size_t* bytes) {
+  if (!bytes) return PGG_ERR_INVALID_ARG;
+  CombinePlan p;
+  const pgg_status st = make_combine_plan(desc, &p);
+  if (st != PGG_OK) return st;
+  *bytes = p.total_grad;
+  return PGG_OK;
+}
+
+pgg_status pgg_moe_combine(const pgg_moe_combine_desc* desc, const void* permuted, const int64_t* expanded_row_idx,
+                           const float* probs, const void* residual, const void* post_weight, const float* gate,
+                           const void* next_weight, void* out, void* normed, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream) {
+  CombinePlan p;
+  const pgg_status st = make_combine_plan(desc, &p);
+  if (st != PGG_OK) return st;
+  if (!permuted || !expanded_row_idx || !probs || !residual || !out || !workspace ||
+      (normed != nullptr) != (next_weight != nullptr))
+    return PGG_ERR_INVALID_ARG;
+  if (workspace_bytes < p.total_fwd) return PGG_ERR_WORKSPACE_TOO_SMALL;
+  const size_t es = elem_size(p.dtype);
+  if (!is_aligned(workspace, kWorkspaceAlign) || !is_aligned(expanded_row_idx, 8) || !is_aligned(probs, 4) ||
+      !is_aligned(gate, 4) || !is_aligned(permuted, es) || !is_aligned(residual, es) || !is_aligned(post_weight, es) ||
+      !is_aligned(next_weight, es) || !is_aligned(out, es) || !is_aligned(normed, es))
+    return PGG_ERR_MISALIGNED;
+  TimedLaunch t("combine", stream);
+  return launch_combine(p, permuted, expanded_row_idx, probs, residual, post_weight, gate, next_weight, out, normed,
+                        workspace, stream) == hipSuccess ? PGG_OK : PGG_ERR_HIP;
+}
+
+pgg_status pgg_moe_combine_grad(const pgg_moe_combine_desc* desc, const pgg_moe_combine_grad_args* args,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  CombinePlan p;
+  const pgg_status st = make_combine_plan(desc, &p);
+  if (st != PGG_OK) return st;
+  if (!args || !workspace) return PGG_ERR_INVALID_ARG;
+  const pgg_moe_combine_grad_args& g = *args;
+  if (!g.grad_out || !g.permuted || !g.expanded_row_idx || !g.probs || !g.residual || !g.grad_permuted ||
+      !g.grad_probs || !g.grad_residual)
+    return PGG_ERR_INVALID_ARG;
+  if ((g.grad_normed != nullptr) != (g.next_weight != nullptr) ||
+      (g.grad_next_weight != nullptr) != (g.next_weight != nullptr) || (g.grad_gate != nullptr) != (g.gate != nullptr) ||
+      (g.grad_post_weight != nullptr) != (g.post_weight != nullptr))
+    return PGG_ERR_INVALID_ARG;
+  if (workspace_bytes < p.total_grad) return PGG_ERR_WORKSPACE_TOO_SMALL;
+  const void* values[] = {g.grad_out, g.grad_normed, g.permuted, g.residual, g.post_weight, g.next_weight,
+                          g.grad_permuted, g.grad_residual};
+  for (const void* v : values)
+    if (!is_aligned(v, elem_size(p.dtype))) return PGG_ERR_MISALIGNED;
+  const void* floats[] = {g.probs, g.gate, g.grad_probs, g.grad_gate, g.grad_post_weight, g.grad_next_weight};
+  for (const void* v : floats)
+    if (!is_aligned(v, 4)) return PGG_ERR_MISALIGNED;
+  if (!is_aligned(workspace, kWorkspaceAlign) || !is_aligned(g.expanded_row_idx, 8)) return PGG_ERR_MISALIGNED;
+  TimedLaunch t("combine_grad", stream);
+  return launch_combine_grad(p, g, workspace, stream) == hipSuccess ? PGG_OK : PGG_ERR_HIP;
 }
 
 pgg_status pgg_moe_dx_read_device_error(const void* workspace, hipStream_t stream, int32_t* code,

@@ -226,6 +226,57 @@ pgg_status make_lora_plan(const pgg_lora_desc* desc, LoraPlan* plan);
 hipError_t launch_lora(const LoraPlan& p, const void* x, const void* weight, const void* a, const void* b,
                        const int64_t* ids, const float* scales, void* y, void* ws, hipStream_t s);
 
+// The gate over experts in groups and its gradient (one launch each, no workspace).
+pgg_status check_gate_grouped_desc(const pgg_moe_gate_grouped_desc* desc);
+hipError_t launch_gate_grouped(const pgg_moe_gate_grouped_desc& d, const void* logits, const float* bias, int64_t* ids,
+                               float* probs, hipStream_t s);
+hipError_t launch_gate_grouped_grad(const pgg_moe_gate_grouped_desc& d, const void* logits, const int64_t* ids,
+                                    const float* grad_probs, void* grad_logits, hipStream_t s);
+
+// Packed 4-bit weights, and the products with them.
+struct W4Layout {
+  int64_t G, K, N, group_size;
+  int64_t tiles;           // G x KB x CB
+  int32_t KB, CB;          // tiles of 128 k; column blocks of 64 (gated: 32 gate and 32 up columns)
+  int32_t sub;             // scale groups of a tile: 1, 2 or 4
+  int32_t dtype, zeros, gated;
+  size_t off_scales, off_zeros, total;
+};
+pgg_status make_w4_layout(const pgg_w4_desc* desc, W4Layout* layout);
+hipError_t launch_w4_pack(const W4Layout& l, const uint8_t* codes, const void* scales, const uint8_t* zeros,
+                          void* packed, hipStream_t s);
+
+struct W4Plan {
+  Plan base;               // sizes, tables and workspace layout (N: reduction, K: columns)
+  W4Layout layout;
+  int32_t waves;           // of a workgroup, which split its part of the reduction
+  int32_t ksplit, kb_span; // splits over workgroups, and tiles of 128 k of one
+  int32_t sub;
+};
+pgg_status make_w4_plan(const pgg_moe_w4_desc* desc, bool gated, W4Plan* plan);
+hipError_t launch_w4(const W4Plan& p, int32_t act, const void* x, const void* packed, const int64_t* eri,
+                     const int64_t* group_list, void* out, void* ws, hipStream_t s);
+
+// Unpermute with the norms and the residual stream behind it, and its gradient.
+struct CombinePlan {
+  int64_t M, batch, topk, H;
+  float alpha, eps;
+  int32_t dtype, row_idx_type;
+  int32_t row_long;          // rows of more than 8192 elements
+  int64_t grad_blocks;       // workgroups of the gradient
+  // a token's workgroup: pieces of 8 elements to a thread are 1 (gradient 2) or, of long rows, 4
+  int32_t threads(bool grad) const {
+    const int64_t n = 8 * (row_long ? 4 : grad ? 2 : 1);
+    return static_cast<int32_t>(((H + n - 1) / n + 63) / 64 * 64);
+  }
+  size_t off_header, off_inv, off_ori, off_part, total_fwd, total_grad;
+};
+pgg_status make_combine_plan(const pgg_moe_combine_desc* desc, CombinePlan* plan);
+hipError_t launch_combine(const CombinePlan& p, const void* permuted, const int64_t* eri, const float* probs,
+                          const void* residual, const void* post, const float* gate, const void* next, void* out,
+                          void* normed, void* ws, hipStream_t s);
+hipError_t launch_combine_grad(const CombinePlan& p, const pgg_moe_combine_grad_args& g, void* ws, hipStream_t s);
+
 // Forward grouped matmul with the permute gathered into the A operand:
 // y[i, :] = x[ori[i] / topK, :] · W[g(i)] for every m-tile of the plan.
 hipError_t launch_forward(const Plan& p, const void* x, const void* weight, float* y, bool aligned,

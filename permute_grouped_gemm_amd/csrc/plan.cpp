@@ -730,4 +730,149 @@ pgg_status make_lora_plan(const pgg_lora_desc* d, LoraPlan* p) {
   return PGG_OK;
 }
 
+pgg_status check_gate_grouped_desc(const pgg_moe_gate_grouped_desc* d) {
+  if (!d) return PGG_ERR_INVALID_ARG;
+  if (d->tokens <= 0 || d->experts <= 0 || d->topk <= 0 || d->groups <= 0 || d->topk_groups <= 0)
+    return PGG_ERR_INVALID_ARG;
+  if (d->groups > d->experts || d->experts % d->groups != 0 || d->topk_groups > d->groups) return PGG_ERR_INVALID_ARG;
+  const int64_t each = d->experts / d->groups;
+  if ((d->topk + each - 1) / each > d->topk_groups) return PGG_ERR_INVALID_ARG;
+  if (d->score != PGG_SCORE_SIGMOID && d->score != PGG_SCORE_SOFTMAX) return PGG_ERR_INVALID_ARG;
+  if (d->renorm != 0 && d->renorm != 1) return PGG_ERR_INVALID_ARG;
+  if (d->dtype < PGG_F32 || d->dtype > PGG_BF16) return PGG_ERR_INVALID_ARG;
+  // as for the gate; the groups' scores live in LDS, one bit of a word each in the long form
+  if (d->experts > 8192 || d->topk > PGG_GATE_MAX_TOPK || d->groups > PGG_GATE_MAX_GROUPS ||
+      d->tokens > (int64_t(1) << 26) - 4)
+    return PGG_ERR_UNSUPPORTED;
+  return PGG_OK;
+}
+
+pgg_status make_w4_layout(const pgg_w4_desc* d, W4Layout* l) {
+  if (!d || !l || d->reserved != 0) return PGG_ERR_INVALID_ARG;
+  if (d->groups <= 0 || d->rows <= 0 || d->cols <= 0 || d->group_size <= 0) return PGG_ERR_INVALID_ARG;
+  if (d->group_size != 32 && d->group_size != 64 && d->group_size % 128 != 0) return PGG_ERR_INVALID_ARG;
+  if ((d->zeros != 0 && d->zeros != 1) || (d->gated != 0 && d->gated != 1)) return PGG_ERR_INVALID_ARG;
+  if (d->gated && d->cols % 2 != 0) return PGG_ERR_INVALID_ARG;
+  if (d->dtype < PGG_F32 || d->dtype > PGG_BF16) return PGG_ERR_INVALID_ARG;
+  if (d->groups >= (int64_t(1) << 30) || d->rows > (int64_t(1) << 31) - 1024 || d->cols > (int64_t(1) << 31) - 1024)
+    return PGG_ERR_UNSUPPORTED;
+  W4Layout q{};
+  q.G = d->groups;
+  q.K = d->rows;
+  q.N = d->cols;
+  q.group_size = d->group_size;
+  q.KB = static_cast<int32_t>((q.K + 127) / 128);
+  q.CB = static_cast<int32_t>(d->gated ? (q.N / 2 + 31) / 32 : (q.N + 63) / 64);
+  q.sub = d->group_size == 32 ? 4 : d->group_size == 64 ? 2 : 1;
+  q.dtype = d->dtype;
+  q.zeros = d->zeros;
+  q.gated = d->gated;
+  const int64_t plane = int64_t(q.KB) * q.CB;
+  // 31-bit byte offsets within a matrix (codes, and fp32 scales of groups of 32)
+  if (plane >= (int64_t(1) << 19) || plane * q.G >= (int64_t(1) << 40)) return PGG_ERR_UNSUPPORTED;
+  q.tiles = plane * q.G;
+  q.off_scales = size_t(q.tiles) * 4096;
+  q.off_zeros = align_up(q.off_scales + size_t(q.tiles) * q.sub * 64 * (q.dtype == PGG_F32 ? 4 : 2), 256);
+  q.total = align_up(q.off_zeros + (q.zeros ? size_t(q.tiles) * q.sub * 64 : 0), 256);
+  *l = q;
+  return PGG_OK;
+}
+
+pgg_status make_w4_plan(const pgg_moe_w4_desc* d, bool gated, W4Plan* p) {
+  if (!d || !p) return PGG_ERR_INVALID_ARG;
+  W4Plan w{};
+  const pgg_status st = make_w4_layout(&d->weight, &w.layout);
+  if (st != PGG_OK) return st;
+  const W4Layout& l = w.layout;
+  if (gated != (l.gated != 0)) return PGG_ERR_INVALID_ARG;
+  if (d->act != PGG_ACT_SILU && d->act != PGG_ACT_GELU_TANH) return PGG_ERR_INVALID_ARG;
+  if (d->topk <= 0 || d->batch <= 0 || d->x_rows != d->batch || d->x_cols != l.K) return PGG_ERR_INVALID_ARG;
+  if (d->row_idx_type != 0 && d->row_idx_type != 1) return PGG_ERR_INVALID_ARG;
+  if (d->group_list_len != l.G || d->topk > INT64_MAX / d->batch) return PGG_ERR_INVALID_ARG;
+  const int64_t M = d->batch * d->topk;
+  const bool indexed = d->idx_len != 0;
+  if (indexed ? d->idx_len != M : d->topk != 1) return PGG_ERR_INVALID_ARG;
+  if (M >= (int64_t(1) << 31) - 1) return PGG_ERR_UNSUPPORTED;
+  Plan& q = w.base;
+  q.M = M; q.N = l.K; q.G = l.G; q.K = l.N; q.batch = d->batch; q.topk = d->topk;
+  q.row_idx_type = d->row_idx_type;
+  q.dtype = l.dtype;
+  q.n_panels = 1;
+  q.max_chunks = 1;
+  q.regime = kStream;
+  q.bm = l.dtype == PGG_F32 || M <= 16 * l.G ? 16 : 32;
+  const int64_t max_tiles = std::min<int64_t>(M, (M + q.bm - 1) / q.bm + l.G);   // each holds a row at least
+  if (max_tiles * l.CB >= (int64_t(1) << 22)) return PGG_ERR_UNSUPPORTED;   // launches of fewer than 2^32 lanes
+  q.max_tiles = static_cast<int32_t>(max_tiles);
+  q.tc = q.max_tiles;
+  // few groups: every workgroup finds its own tile (and, with a routing index, few rows)
+  q.local = l.G <= kLocalGroups && (!indexed || M <= kLocalRows);
+  q.fused_prep = M <= 1024;
+  const int64_t busy = std::min<int64_t>(max_tiles, M / q.bm + (l.G + 1) / 2 + 1) * l.CB;
+  w.sub = l.sub;
+  w.waves = busy >= 512 ? 4 : 8;
+  w.ksplit = 1;
+  w.kb_span = l.KB;
+  if (busy < 128 && l.KB >= 32) {
+    const int64_t split = std::min<int64_t>(std::min<int64_t>(256 / busy, l.KB / 16), 16);
+    w.kb_span = static_cast<int32_t>((l.KB + split - 1) / split);
+    w.ksplit = (l.KB + w.kb_span - 1) / w.kb_span;
+  }
+  q.ksplit = w.ksplit;
+  size_t off = 0;
+  q.off_header = off;   off = align_up(off + sizeof(WsHeader), kRegionAlign);
+  q.off_offsets = off;  off = align_up(off + sizeof(int64_t) * size_t(l.G + 1), kRegionAlign);
+  q.off_tiles = off;    off = align_up(off + sizeof(MTile) * size_t(q.max_tiles), kRegionAlign);
+  q.off_chunks = off;   off = align_up(off + sizeof(int32_t) * 2, kRegionAlign);
+  q.off_inv = off;      off = align_up(off + (indexed ? sizeof(int32_t) * size_t(M) : 0), kRegionAlign);
+  q.off_ori = off;      off = align_up(off + (indexed ? sizeof(int32_t) * size_t(M) : 0), kRegionAlign);
+  q.table_bytes = q.off_ring = off;
+  if (w.ksplit > 1) off = align_up(off + size_t(w.ksplit) * size_t(M) * 64 * size_t(l.CB) * sizeof(float), kRegionAlign);
+  // x is read in chunks of 16 bytes: rows that end inside one are copied to longer ones
+  const int64_t chunk = l.dtype == PGG_F32 ? 4 : 8;
+  q.lda = l.K;
+  q.off_pad_a = off;
+  q.pad_a = l.K % chunk != 0;
+  if (q.pad_a) {
+    q.lda = pad_pitch(l.K);
+    off = align_up(off + size_t(q.batch) * size_t(q.lda) * (l.dtype == PGG_F32 ? 4 : 2), kRegionAlign);
+  }
+  q.total = off;
+  *p = w;
+  return PGG_OK;
+}
+
+pgg_status make_combine_plan(const pgg_moe_combine_desc* d, CombinePlan* p) {
+  if (!d || !p) return PGG_ERR_INVALID_ARG;
+  if (d->batch <= 0 || d->topk <= 0 || d->hidden <= 0) return PGG_ERR_INVALID_ARG;
+  if (d->row_idx_type != 0 && d->row_idx_type != 1) return PGG_ERR_INVALID_ARG;
+  if (d->dtype < PGG_F32 || d->dtype > PGG_BF16) return PGG_ERR_INVALID_ARG;
+  if (!(d->eps >= 0.0f) || d->topk > INT64_MAX / d->batch) return PGG_ERR_INVALID_ARG;
+  const int64_t M = d->batch * d->topk;
+  // a workgroup of 512 threads takes four pieces of 8 elements to a thread; a
+  // launch holds fewer than 2^32 lanes
+  if (M >= (int64_t(1) << 31) - 1 || d->hidden > 16384) return PGG_ERR_UNSUPPORTED;
+  CombinePlan q{};
+  q.M = M;
+  q.batch = d->batch;
+  q.topk = d->topk;
+  q.H = d->hidden;
+  q.alpha = d->residual_scale;
+  q.eps = d->eps;
+  q.dtype = d->dtype;
+  q.row_idx_type = d->row_idx_type;
+  q.row_long = q.H > 8192;
+  if ((q.batch + 1024) * q.threads(false) >= (int64_t(1) << 32)) return PGG_ERR_UNSUPPORTED;
+  // the gradient's workgroups, one or more to a compute unit, go through the tokens
+  q.grad_blocks = std::min<int64_t>(q.batch, 256 * (512 / q.threads(true)));
+  size_t off = 0;
+  q.off_header = off; off = align_up(off + sizeof(WsHeader), kRegionAlign);
+  q.off_inv = off;    off = align_up(off + sizeof(int32_t) * size_t(M), kRegionAlign);
+  q.off_ori = off;    off = align_up(off + sizeof(int32_t) * size_t(M), kRegionAlign);
+  q.off_part = q.total_fwd = off;
+  q.total_grad = align_up(off + 2 * size_t(q.grad_blocks) * size_t(q.H) * sizeof(float), kRegionAlign);
+  *p = q;
+  return PGG_OK;
+}
+
 }  // namespace pgg
