@@ -19,7 +19,7 @@ SOURCES = ["plan.cpp", "api.cpp", "prep.hip", "gemm.hip", "gemm_large.hip", "gem
            "fwd.hip", "fwd_large.hip", "dw.hip",
            "dw_large.hip", "routing.hip",
            "unpermute.hip", "noalloc.hip", "gate.hip", "glu.hip", "glu_grad.hip", "lora.hip", "pad.hip",
-           "gate_grouped.hip", "w4.hip", "combine.hip"]
+           "gate_grouped.hip", "w4.hip", "w4_tile.hip", "combine.hip"]
 ARCH = os.environ.get("PGG_ARCH", "gfx950")
 
 FLAGS = [

@@ -40,7 +40,7 @@ constexpr float kNegInf = -__builtin_inff();
 constexpr int kMaxGroups = PGG_GATE_MAX_GROUPS;
 
 // Keys outside the scores' range, all finite so that their low bits can hold an index
-constexpr double kNanKey = 0x1p1022, kMostKey = 0x1p1000, kExcluded = -0x1p1000, kMissing = -0x1p1023;
+constexpr double kMostKey = 0x1p1000, kExcluded = -0x1p1000, kMissing = -0x1p1023;
 
 struct GroupedArgs {
   const void* logits;   // [T, E]
@@ -81,32 +81,49 @@ __device__ __forceinline__ uint32_t rotate16(uint32_t v) {
   return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x120 + N, 0xF, 0xF, false));
 }
 
-// The value of the lane N places on within the row of lanes; N >= 16: of lane ^ N.
+// The values that a lane and its partner N places on hold (N < 16: rotation
+// within 16 lanes, the first being the lane's own; otherwise the lane N bits away,
+// the lower lane's first).
 template <int N>
-__device__ __forceinline__ uint32_t neighbour(uint32_t v) {
-  if constexpr (N < 16) return rotate16<N>(v);
-  else return static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), N));
+__device__ __forceinline__ void partners(uint32_t v, uint32_t& a, uint32_t& b) {
+  if constexpr (N < 16) {
+    a = v;
+    b = rotate16<N>(v);
+  } else if constexpr (N == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    a = r[0];
+    b = r[1];
+  } else {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    a = r[0];
+    b = r[1];
+  }
 }
-template <int N>
-__device__ __forceinline__ float neighbour(float v) {
-  return __builtin_bit_cast(float, neighbour<N>(__builtin_bit_cast(uint32_t, v)));
+template <int N, class Op>
+__device__ __forceinline__ float step(float v, Op op) {
+  uint32_t a, b;
+  partners<N>(__builtin_bit_cast(uint32_t, v), a, b);
+  return op(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
 }
-template <int N>
-__device__ __forceinline__ double neighbour(double v) {
+template <int N, class Op>
+__device__ __forceinline__ double step(double v, Op op) {
   const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint64_t lo = neighbour<N>(static_cast<uint32_t>(u)), hi = neighbour<N>(static_cast<uint32_t>(u >> 32));
-  return __builtin_bit_cast(double, hi << 32 | lo);
+  uint32_t a[2], b[2];
+  partners<N>(static_cast<uint32_t>(u), a[0], b[0]);
+  partners<N>(static_cast<uint32_t>(u >> 32), a[1], b[1]);
+  return op(__builtin_bit_cast(double, static_cast<uint64_t>(a[1]) << 32 | a[0]),
+            __builtin_bit_cast(double, static_cast<uint64_t>(b[1]) << 32 | b[0]));
 }
 
 // Reduction over the LPR lanes of a row; every lane gets the result.
 template <int LPR, class V, class Op>
 __device__ __forceinline__ V reduce(V v, Op op) {
-  v = op(v, neighbour<8>(v));
-  v = op(v, neighbour<4>(v));
-  v = op(v, neighbour<2>(v));
-  v = op(v, neighbour<1>(v));
-  if constexpr (LPR >= 32) v = op(v, neighbour<16>(v));
-  if constexpr (LPR >= 64) v = op(v, neighbour<32>(v));
+  v = step<8>(v, op);
+  v = step<4>(v, op);
+  v = step<2>(v, op);
+  v = step<1>(v, op);
+  if constexpr (LPR >= 32) v = step<16>(v, op);
+  if constexpr (LPR >= 64) v = step<32>(v, op);
   return v;
 }
 template <int LPR>
@@ -147,23 +164,48 @@ __device__ __forceinline__ double reciprocal(double v) {
   return __builtin_fma(__builtin_fma(-v, r, 1.0), r, r);
 }
 
-// The score as a double.  norm: 1 / sum exp(l - top) (softmax).
-__device__ __forceinline__ double score(float l, bool softmax, float top, double norm) {
-  const double x = l;
-  if (softmax) return exp(x - static_cast<double>(top)) * norm;
-  const double q = exp(-fabs(x));
-  return (x >= 0.0 ? 1.0 : q) * reciprocal(1.0 + q);   // NaN stays NaN
+// exp(v) for v <= 0, to 2^-46 of itself, more than a key keeps: v = n ln 2 + r with
+// |r| <= ln 2 / 2, the Taylor polynomial of degree 11 at r (the first term left out
+// is 2^-47), times 2^n.  Below -800 as at -800, which is 0; NaN likewise.
+__device__ __forceinline__ double exp_negative(double v) {
+  v = max64(v, -800.0);
+  const double n = __builtin_rint(v * 1.4426950408889634);
+  const double r = __builtin_fma(n, -0.6931471805599453, v);
+  double p = 1.0 / 39916800.0;
+  p = __builtin_fma(p, r, 1.0 / 3628800.0);
+  p = __builtin_fma(p, r, 1.0 / 362880.0);
+  p = __builtin_fma(p, r, 1.0 / 40320.0);
+  p = __builtin_fma(p, r, 1.0 / 5040.0);
+  p = __builtin_fma(p, r, 1.0 / 720.0);
+  p = __builtin_fma(p, r, 1.0 / 120.0);
+  p = __builtin_fma(p, r, 1.0 / 24.0);
+  p = __builtin_fma(p, r, 1.0 / 6.0);
+  p = __builtin_fma(p, r, 0.5);
+  p = __builtin_fma(p, r, 1.0);
+  p = __builtin_fma(p, r, 1.0);
+  return __builtin_amdgcn_ldexp(p, static_cast<int>(n));
 }
 
-// Key and index in one double; BITS of it are the index's.
+__device__ __forceinline__ double sigmoid_score(float l) {
+  const double x = l, q = exp_negative(-fabs(x));
+  return (x >= 0.0 ? 1.0 : q) * reciprocal(1.0 + q);
+}
+
+// Key and index in one double; BITS of it are the index's.  A NaN comes out as the
+// largest key, and so does a logit above `limit` or a NaN: softmax makes a NaN of +inf.
 template <int BITS>
-__device__ __forceinline__ double pack_key(double key, bool excluded, int e) {
-  constexpr uint64_t mask = (uint64_t(1) << BITS) - 1;
-  double v = key != key ? kNanKey : key > kMostKey ? kMostKey : key;
-  if (excluded || v < kExcluded) v = kExcluded;
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint64_t low = static_cast<int64_t>(u) < 0 ? e : mask - e;   // a lower index is larger
-  return __builtin_bit_cast(double, (u & ~mask) | low);
+__device__ __forceinline__ double pack_key(double key, float l, float limit, int e) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, max64(min64(key, kMostKey), kExcluded));
+  constexpr uint32_t mask = (1u << BITS) - 1;
+  constexpr uint32_t most = __builtin_bit_cast(uint64_t, kMostKey) >> 32, least = most | 0x80000000u;
+  // (the low words of both are only index)
+  uint32_t hi = static_cast<uint32_t>(u >> 32), lo = static_cast<uint32_t>(u);
+  const bool banned = l == kNegInf, first = !(l <= limit);
+  hi = banned ? least : first ? most : hi;
+  lo = banned || first ? 0u : lo;
+  const uint32_t low = static_cast<uint32_t>(e ^ ~(static_cast<int32_t>(hi) >> 31));   // a lower index is larger
+  lo = (lo & ~mask) | (low & mask);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
 template <int BITS>
 __device__ __forceinline__ int32_t packed_index(double v) {
@@ -232,23 +274,24 @@ __device__ __forceinline__ float sigmoid_exact(float l) {
   return (l >= 0.0f ? 1.0f : q) / (1.0f + q);
 }
 
-// Weights before the scale, of picks with the logits l (-inf: no pick or an
+// Weights before the scale, of k picks with the logits l (-inf: no pick or an
 // excluded one, weight 0).  top / total: the row's pivot and sum of exp (softmax
 // without renorm).
 template <int LPR>
-__device__ __forceinline__ void weights(bool softmax, bool renorm, float top, float total,
+__device__ __forceinline__ void weights(int k, bool softmax, bool renorm, float top, float total,
                                         const float (&l)[kPickRegs<LPR>], float (&w)[kPickRegs<LPR>]) {
   constexpr int R = kPickRegs<LPR>;
   if (!renorm) {
 #pragma unroll
-    for (int s = 0; s < R; ++s) {
-      if (softmax) {
-        const float e = expf(l[s] - top);
-        w[s] = total == 0.0f ? e : e / total;
-      } else {
-        w[s] = sigmoid_exact(l[s]);
+    for (int s = 0; s < R; ++s)
+      if (s * LPR < k) {
+        if (softmax) {
+          const float e = expf(l[s] - top);
+          w[s] = total == 0.0f ? e : e / total;
+        } else {
+          w[s] = sigmoid_exact(l[s]);
+        }
       }
-    }
     return;
   }
   float m = l[0];
@@ -260,14 +303,16 @@ __device__ __forceinline__ void weights(bool softmax, bool renorm, float top, fl
   if (!softmax) top = top > 0.0f ? 0.0f : top;
   float sum = 0.0f;
 #pragma unroll
-  for (int s = 0; s < R; ++s) {
-    if (softmax) w[s] = expf(l[s] - top);
-    else w[s] = l[s] >= 0.0f ? 1.0f / (1.0f + expf(-l[s])) : expf(l[s] - top) / (1.0f + expf(l[s]));
-    sum += w[s];
-  }
+  for (int s = 0; s < R; ++s)
+    if (s * LPR < k) {
+      if (softmax) w[s] = expf(l[s] - top);
+      else w[s] = l[s] >= 0.0f ? 1.0f / (1.0f + expf(-l[s])) : expf(l[s] - top) / (1.0f + expf(l[s]));
+      sum += w[s];
+    }
   sum = row_sum<LPR>(sum);
 #pragma unroll
-  for (int s = 0; s < R; ++s) w[s] = sum == 0.0f ? w[s] : w[s] / sum;
+  for (int s = 0; s < R; ++s)
+    if (s * LPR < k) w[s] = sum == 0.0f ? w[s] : w[s] / sum;
 }
 
 template <class T, int LPR>
@@ -277,7 +322,7 @@ __device__ __forceinline__ void store_picks(const GroupedArgs& a, const typename
   float l[R], w[R];
 #pragma unroll
   for (int s = 0; s < R; ++s) l[s] = s * LPR + lane < a.k ? to_float<T>(row[sel[s]]) : kNegInf;
-  weights<LPR>(a.softmax, a.renorm, top, total, l, w);
+  weights<LPR>(a.k, a.softmax, a.renorm, top, total, l, w);
 #pragma unroll
   for (int s = 0; s < R; ++s) {
     const int j = s * LPR + lane;
@@ -308,7 +353,8 @@ __global__ __launch_bounds__(kThreads) void grouped_gate_kernel(GroupedArgs a) {
 #pragma unroll
   for (int i = 0; i < EPL; i += 4) load4<T>(row, e0 + i, a.E, *reinterpret_cast<float(*)[4]>(&l[i]));
   float top = 0.0f;
-  double total = 1.0, norm = 1.0;
+  double total = 1.0, key[EPL];
+  const float limit = a.softmax ? 3.402823466e38f : -kNegInf;
   if (a.softmax) {
     float m = l[0];
 #pragma unroll
@@ -316,17 +362,34 @@ __global__ __launch_bounds__(kThreads) void grouped_gate_kernel(GroupedArgs a) {
     top = pivot(row_max<LPR>(m));
     double sum = 0.0;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) sum += exp(static_cast<double>(l[i]) - static_cast<double>(top));
+    for (int i = 0; i < EPL; ++i) {
+      key[i] = exp_negative(static_cast<double>(l[i]) - static_cast<double>(top));
+      sum += key[i];
+    }
     total = row_sum<LPR>(sum);
-    norm = total == 0.0 ? 0.0 : reciprocal(total);
-  }
-  double key[EPL];
+    const double norm = reciprocal(max64(total, 1.0));   // at least 1 but for a row of -inf
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = e0 + i;
-    double v = score(l[i], a.softmax, top, norm);
-    if (a.bias && e < a.E) v += static_cast<double>(a.bias[e]);
-    key[i] = e < a.E ? pack_key<BITS>(v, l[i] == kNegInf, e) : kMissing;
+    for (int i = 0; i < EPL; ++i) key[i] *= norm;
+    if (top != top || top == -kNegInf) total = __builtin_nan("");   // a NaN or +inf logit: exp_negative takes neither
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = sigmoid_score(l[i]);
+  }
+  if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < EPL; i += 4) {
+      float b[4];
+      load4<TF32>(a.bias, e0 + i, a.E, b);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) key[i + q] += static_cast<double>(b[q]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) key[i] = pack_key<BITS>(key[i], l[i], limit, e0 + i);
+  if (e0 + EPL > a.E) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (e0 + i >= a.E) key[i] = kMissing;
   }
   const int each = a.E / a.groups;
   const bool whole = each % EPL == 0;   // a lane's experts are of one group
@@ -362,6 +425,7 @@ __global__ __launch_bounds__(kThreads) void grouped_gate_kernel(GroupedArgs a) {
     for (int g = lane; g < a.groups; g += LPR) {
       const double mine = s_score[r][g];
       int before = 0;
+#pragma unroll 4
       for (int o = 0; o < a.groups; ++o) {
         const double other = s_score[r][o];
         before += other > mine || (other == mine && o < g);
@@ -409,22 +473,24 @@ __global__ __launch_bounds__(64) void grouped_gate_long_kernel(GroupedArgs a) {
   const int64_t t = blockIdx.x;
   const E* __restrict__ row = static_cast<const E*>(a.logits) + t * a.E;
   float top = 0.0f;
-  double total = 1.0, norm = 1.0;
+  double total = 1.0;
+  const float limit = a.softmax ? 3.402823466e38f : -kNegInf;
   if (a.softmax) {
     float m = kNegInf;
     for (int e = lane; e < a.E; e += LPR) m = max_nan(to_float<T>(row[e]), m);
     top = pivot(row_max<LPR>(m));
     double sum = 0.0;
     for (int e = lane; e < a.E; e += LPR)
-      sum += exp(static_cast<double>(to_float<T>(row[e])) - static_cast<double>(top));
+      sum += exp_negative(static_cast<double>(to_float<T>(row[e])) - static_cast<double>(top));
     total = row_sum<LPR>(sum);
-    norm = total == 0.0 ? 0.0 : reciprocal(total);
   }
+  const double norm = reciprocal(max64(total, 1.0));
+  if (top != top || top == -kNegInf) total = __builtin_nan("");
   for (int e = lane; e < a.E; e += LPR) {
     const float l = to_float<T>(row[e]);
-    double v = score(l, a.softmax, top, norm);
+    double v = a.softmax ? exp_negative(static_cast<double>(l) - static_cast<double>(top)) * norm : sigmoid_score(l);
     if (a.bias) v += static_cast<double>(a.bias[e]);
-    scratch[e] = pack_key<BITS>(v, l == kNegInf, e);
+    scratch[e] = pack_key<BITS>(v, l, limit, e);
   }
   wave_fence();
   if (a.groups > 1) {
@@ -514,18 +580,18 @@ __global__ __launch_bounds__(THREADS) void grouped_gate_grad_kernel(GroupedGradA
     }
     total = row_sum<LPR>(sum);
   }
-  weights<LPR>(a.softmax, a.renorm, top, total, l, w);
+  weights<LPR>(a.k, a.softmax, a.renorm, top, total, l, w);
   float mean = 0.0f;   // sum_j d_j w_j
   if (dense || a.renorm) {
 #pragma unroll
     for (int s = 0; s < R; ++s)
-      if (id[s] >= 0) mean += d[s] * w[s];
+      if (s * LPR < a.k && id[s] >= 0) mean += d[s] * w[s];
     mean = row_sum<LPR>(mean);
   }
   wave_fence();
 #pragma unroll
   for (int s = 0; s < R; ++s)
-    if (id[s] >= 0) {
+    if (s * LPR < a.k && id[s] >= 0) {
       float v = d[s];
       if (!dense) {
         v = w[s] * (v - mean);
@@ -568,12 +634,23 @@ hipError_t launch_rows(const GroupedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Few tokens: more lanes to a row, so that the work and the code of a wave are
+// shorter.  Groups of experts that end inside a lane's run of EPL take a way
+// through LDS and a second sort, so shorter runs that end with them are taken
+// instead.  Measured in us (a launch in a row of launches, bf16, 8 groups, 8
+// picks), 64 lanes of 4, 32 of 8 and 16 of 16:
+//   256 experts: 1024 tokens 5.5, 5.9, 7.9; 2048 6.3, 5.9, 7.9; 4096 8.3, 7.0, 8.1
+//   160 experts (20 to a group): 1024 5.2, 8.0, 12.2; 4096 7.7, 9.1, 12.3; 13824 18.5, 19.0, 20.1
+//   512 experts, 64 lanes of 8 and 32 of 16: 2048 7.6, 8.2; 4096 10.9, 10.0; 13824 28.0, 23.3
+//   128 experts, 32 lanes of 4 and 16 of 8: 4096 5.9, 6.2; 13824 11.4, 10.8
 template <class T>
 hipError_t launch_typed(const GroupedArgs& a, hipStream_t s) {
+  const int each = a.E / a.groups;
+  auto split = [&](int run) { return a.groups > 1 && each % run != 0 && each % (run / 2) == 0; };
   if (a.E <= 64) return launch_rows<T, 16, 4>(a, s);
-  if (a.E <= 128) return launch_rows<T, 16, 8>(a, s);
-  if (a.E <= 256) return launch_rows<T, 16, 16>(a, s);
-  if (a.E <= 512) return launch_rows<T, 32, 16>(a, s);
+  if (a.E <= 128) return a.T <= 4096 || split(8) ? launch_rows<T, 32, 4>(a, s) : launch_rows<T, 16, 8>(a, s);
+  if (a.E <= 256) return a.T <= 1024 || split(8) ? launch_rows<T, 64, 4>(a, s) : launch_rows<T, 32, 8>(a, s);
+  if (a.E <= 512) return a.T <= 2048 || split(16) ? launch_rows<T, 64, 8>(a, s) : launch_rows<T, 32, 16>(a, s);
   if (a.E <= 1024) return launch_rows<T, 64, 16>(a, s);
   hipLaunchKernelGGL((grouped_gate_long_kernel<T>), rows_grid(a.T, 1), dim3(64), sizeof(double) * a.E, s, a);
   return hipGetLastError();
@@ -587,11 +664,13 @@ hipError_t launch_grad_rows(const GroupedGradArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// 16 KiB of LDS at most per workgroup, but one row always fits (32 KiB)
+// LDS: 32 KiB at most per workgroup, 16 with many rows, but one row always fits.
+// Few rows: more lanes to a row.  Measured in us as above, 16, 32 and 64 lanes:
+//   256 experts: 2048 tokens 5.3, 4.0, 3.7; 4096 5.4, 4.3, 4.4; 13824 7.4, 6.7, 8.6
+//   512 experts: 4096 -, 5.4, 5.1; 13824 -, 8.9, 10.4;  64 experts: 2048 3.9, 3.5, -; 13824 5.4, 5.4, -
 template <class T>
 hipError_t launch_grad_typed(const GroupedGradArgs& a, hipStream_t s) {
-  if (a.E <= 64) return launch_grad_rows<T, 16, 256>(a, s);
-  if (a.E <= 128) return launch_grad_rows<T, 32, 256>(a, s);
+  if (a.E <= 128 || (a.E <= 512 && a.T > 4096)) return launch_grad_rows<T, 32, 256>(a, s);
   if (a.E <= 1024) return launch_grad_rows<T, 64, 256>(a, s);
   return launch_grad_rows<T, 64, 64>(a, s);
 }

@@ -133,6 +133,12 @@ __device__ __forceinline__ void dma16(const void* src, uint32_t m0) {
                :: "s"(m0), "v"(src) : "memory", "m0");
 }
 
+// The same of 4 bytes per lane.
+__device__ __forceinline__ void dma4(const void* src, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+               :: "s"(m0), "v"(src) : "memory", "m0");
+}
+
 // The same load with the non-temporal hint: for data read exactly once (a
 // weight stream), so its lines do not displace operands that are reused.
 __device__ __forceinline__ void dma16_nt(const void* src, uint32_t m0) {

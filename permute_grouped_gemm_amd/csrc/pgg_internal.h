@@ -252,6 +252,8 @@ struct W4Plan {
   int32_t waves;           // of a workgroup, which split its part of the reduction
   int32_t ksplit, kb_span; // splits over workgroups, and tiles of 128 k of one
   int32_t sub;
+  bool tiles;              // many rows per expert: tiles of 64 rows x 256 columns
+  size_t off_sums;         // and the sums of x over the scale groups for them
 };
 pgg_status make_w4_plan(const pgg_moe_w4_desc* desc, bool gated, W4Plan* plan);
 hipError_t launch_w4(const W4Plan& p, int32_t act, const void* x, const void* packed, const int64_t* eri,

@@ -24,6 +24,12 @@
 
 namespace pgg {
 
+struct PrepArgs {
+  int64_t M, G, topk;
+  int32_t bm, tc, max_tiles, max_chunks;
+  int32_t row_idx_type;
+};
+
 namespace {
 
 constexpr int kPrepThreads = 1024;
@@ -34,12 +40,6 @@ __device__ __forceinline__ void set_error(WsHeader* h, int code, long long detai
                            (static_cast<unsigned long long>(detail) & kDetailMask);
   atomicMin(&h->err, key);
 }
-
-struct PrepArgs {
-  int64_t M, G, topk;
-  int32_t bm, tc, max_tiles, max_chunks;
-  int32_t row_idx_type;
-};
 
 // Block-wide: header reset (thread 0; caller syncs before errors may be set).
 __device__ void reset_header(WsHeader* h) {

@@ -39,8 +39,6 @@ namespace pgg {
 constexpr int kW4K = 128, kW4Cols = 64;          // a packed tile
 constexpr int kW4TileBytes = kW4K * kW4Cols / 2;
 
-namespace {
-
 struct W4Args {
   const void* x;
   const uint8_t* codes;
@@ -55,7 +53,7 @@ struct W4Args {
   int64_t M, K, cols;       // K: of x, a multiple of 8 (fp32: 4); cols: output columns (gated: F)
   int64_t lda;
   int32_t KB, CB, kb_span, ksplit;
-  int32_t n_slots;
+  int32_t n_slots, n_col_tiles;
   uint32_t topk;
   int32_t gated, act;
   // without tables
@@ -65,6 +63,11 @@ struct W4Args {
   PrepArgs prep;
   WsView ws;
 };
+
+// Many rows per expert (w4_tile.hip).
+hipError_t launch_w4_tile(const W4Plan& p, const W4Args& a, hipStream_t s);
+
+namespace {
 
 // Column of the product (gated: gate columns, then up) in tile column block cb.
 __host__ __device__ __forceinline__ int64_t w4_column(int64_t cb, int i, int j, bool gated, int64_t F) {
@@ -418,16 +421,45 @@ __device__ __forceinline__ bool w4_find(const W4Args& a, int slot, int bm, MTile
   return true;
 }
 
-// The error word's preparation, by one workgroup: header, group tables and, where
-// there is one, the routing index.
-__device__ __forceinline__ void w4_prepare(const W4Args& a, long long* scratch) {
-  if (a.eri) {
-    prep_block(a.prep, a.eri, a.gl, a.ws, scratch);
-    return;
+// The error word of a call without tables, by one workgroup: the counts by its
+// first wave, the index with a bit per row.
+__device__ __forceinline__ void w4_check(const W4Args& a, uint32_t* bits) {
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    a.ws.hdr->err = kNoError;
+    a.ws.hdr->n_tiles = 0;
   }
-  reset_header(a.ws.hdr);
+  if (a.eri)
+    for (int64_t i = tid; i < (a.M + 31) / 32; i += blockDim.x) bits[i] = 0;
   __syncthreads();
-  groups_phase(a.prep, a.gl, a.ws, scratch, scratch + blockDim.x);
+  if (tid < 64) {
+    int64_t total = 0;
+    int first_bad = kLocalGroups;
+    for (int g = tid; g < a.prep.G; g += 64) {
+      const int64_t c = a.gl[g];
+      if (c < 0) first_bad = min(first_bad, g);
+      else total += min<int64_t>(c, a.M + 1);
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      total += __shfl_xor(total, d);
+      first_bad = min(first_bad, __shfl_xor(first_bad, d));
+    }
+    if (tid == 0) {
+      if (first_bad < kLocalGroups) set_error(a.ws.hdr, PGG_DEV_GROUP_NEGATIVE, first_bad);
+      else if (total != a.M) set_error(a.ws.hdr, PGG_DEV_GROUP_SUM, total);
+    }
+  }
+  if (a.eri)
+    for (int64_t p = tid; p < a.M; p += blockDim.x) {
+      const int64_t v = a.eri[p];
+      if (v < 0 || v >= a.M) {
+        set_error(a.ws.hdr, PGG_DEV_INDEX_RANGE, p);
+      } else {
+        const uint32_t bit = 1u << (v & 31);
+        if (atomicOr(&bits[v >> 5], bit) & bit) set_error(a.ws.hdr, PGG_DEV_INDEX_DUP, v);
+      }
+    }
 }
 
 }  // namespace

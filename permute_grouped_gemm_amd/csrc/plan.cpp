@@ -800,21 +800,27 @@ pgg_status make_w4_plan(const pgg_moe_w4_desc* d, bool gated, W4Plan* p) {
   q.n_panels = 1;
   q.max_chunks = 1;
   q.regime = kStream;
-  q.bm = l.dtype == PGG_F32 || M <= 16 * l.G ? 16 : 32;
+  w.tiles = l.dtype != PGG_F32 && M > 32 * l.G && !(indexed && d->batch <= 32);
+  if (const char* e = getenv("W4_TILES")) w.tiles = l.dtype != PGG_F32 && atoi(e);
+  q.bm = w.tiles ? 64 : l.dtype == PGG_F32 || M <= 12 * l.G || (indexed && d->batch <= 16) ? 16 : 32;
+  if (const char* e = getenv("W4_BM")) if (!w.tiles && l.dtype != PGG_F32) q.bm = atoi(e);
   const int64_t max_tiles = std::min<int64_t>(M, (M + q.bm - 1) / q.bm + l.G);   // each holds a row at least
+  const int64_t col_tiles = w.tiles ? (l.CB + 3) / 4 : l.CB;
   if (max_tiles * l.CB >= (int64_t(1) << 22)) return PGG_ERR_UNSUPPORTED;   // launches of fewer than 2^32 lanes
   q.max_tiles = static_cast<int32_t>(max_tiles);
   q.tc = q.max_tiles;
   // few groups: every workgroup finds its own tile (and, with a routing index, few rows)
-  q.local = l.G <= kLocalGroups && (!indexed || M <= kLocalRows);
+  q.local = !w.tiles && l.G <= kLocalGroups && (!indexed || M <= kLocalRows);
   q.fused_prep = M <= 1024;
-  const int64_t busy = std::min<int64_t>(max_tiles, M / q.bm + (l.G + 1) / 2 + 1) * l.CB;
+  const int64_t busy = std::min<int64_t>(max_tiles, M / q.bm + (l.G + 1) / 2 + 1) * col_tiles;
   w.sub = l.sub;
   w.waves = busy >= 512 ? 4 : 8;
+  if (const char* e = getenv("W4_WAVES")) w.waves = atoi(e);
   w.ksplit = 1;
   w.kb_span = l.KB;
-  if (busy < 128 && l.KB >= 32) {
-    const int64_t split = std::min<int64_t>(std::min<int64_t>(256 / busy, l.KB / 16), 16);
+  const int64_t fill = w.tiles ? 512 : 256, least = w.tiles ? 8 : 16;   // workgroups; tiles of 128 k of a split
+  if (busy <= fill / 2 && l.KB >= 2 * least) {
+    const int64_t split = std::min<int64_t>(std::min<int64_t>(fill / busy, l.KB / least), 16);
     w.kb_span = static_cast<int32_t>((l.KB + split - 1) / split);
     w.ksplit = (l.KB + w.kb_span - 1) / w.kb_span;
   }
@@ -837,6 +843,8 @@ pgg_status make_w4_plan(const pgg_moe_w4_desc* d, bool gated, W4Plan* p) {
     q.lda = pad_pitch(l.K);
     off = align_up(off + size_t(q.batch) * size_t(q.lda) * (l.dtype == PGG_F32 ? 4 : 2), kRegionAlign);
   }
+  w.off_sums = off;
+  if (w.tiles) off = align_up(off + sizeof(float) * size_t(q.batch) * size_t(l.KB) * l.sub, kRegionAlign);
   q.total = off;
   *p = w;
   return PGG_OK;

@@ -75,25 +75,28 @@ struct W4Stage {
   }
 };
 
-// Tiles of 128 k that are loaded ahead: as many as fit the registers of two waves per SIMD.
+// Tiles of 128 k that are loaded ahead, and waves to a SIMD: more tiles cost waves.
+// Measured, 128 rows x 7168 x 4096, 12 experts, bf16: 2 tiles and 3 waves 38.6 us,
+// 3 and 2 43.5, 4 and 2 43.5.
+constexpr int kW4Ahead = 2;
 template <class T, int RB>
-constexpr int kW4Ahead = __is_same(T, TF32) || RB == 2 ? 2 : 3;
+constexpr int kW4Waves = __is_same(T, TF32) || RB == 2 ? 2 : 3;
 
 constexpr int kW4MaxWaves = 8;
 
 template <class T, int RB, int SUB>
-__global__ __launch_bounds__(kW4MaxWaves * 64) __attribute__((amdgpu_waves_per_eu(2)))
+__global__ __launch_bounds__(kW4MaxWaves * 64) __attribute__((amdgpu_waves_per_eu(kW4Waves<T, RB>)))
 void w4_rows_kernel(W4Args a) {
   using E = typename T::elem;
-  constexpr int BM = 16 * RB, D = kW4Ahead<T, RB>, kPitch = kW4Cols + 4;
+  constexpr int BM = 16 * RB, D = kW4Ahead, kPitch = kW4Cols + 4;
   __shared__ float lds[kW4MaxWaves * BM * kPitch];
   __shared__ int32_t s_rows[BM];
-  static_assert(sizeof(lds) >= 2 * sizeof(long long) * kW4MaxWaves * 64, "the preparation's scratch");
+  static_assert(sizeof(lds) * 8 >= kLocalRows, "a bit per row for the check of the index");
 
   int bid = blockIdx.x;
   if (a.local) {
     if (bid == 0) {
-      w4_prepare(a, reinterpret_cast<long long*>(lds));
+      w4_check(a, reinterpret_cast<uint32_t*>(lds));
       return;
     }
     --bid;
@@ -237,7 +240,8 @@ hipError_t launch_sub(const W4Plan& p, const W4Args& a, hipStream_t s) {
 template <class T>
 hipError_t launch_typed(const W4Plan& p, const W4Args& a, hipStream_t s) {
   hipError_t e;
-  if constexpr (__is_same(T, TF32)) e = launch_sub<T, 1>(p, a, s);
+  if (p.tiles) e = launch_w4_tile(p, a, s);
+  else if constexpr (__is_same(T, TF32)) e = launch_sub<T, 1>(p, a, s);
   else e = p.base.bm == 16 ? launch_sub<T, 1>(p, a, s) : launch_sub<T, 2>(p, a, s);
   if (e != hipSuccess || a.ksplit == 1) return e;
   hipLaunchKernelGGL((w4_finish_kernel<T>), dim3(std::min(blocks_for(a.M * 16 * a.CB), 2048u)), dim3(256), 0, s, a);
@@ -297,7 +301,9 @@ hipError_t launch_w4(const W4Plan& p, int32_t act, const void* x, const void* pa
   a.CB = l.CB;
   a.kb_span = p.kb_span;
   a.ksplit = p.ksplit;
+  a.sums = reinterpret_cast<const float*>(static_cast<const char*>(ws) + p.off_sums);
   a.n_slots = p.base.max_tiles;
+  a.n_col_tiles = (l.CB + 3) / 4;
   a.topk = static_cast<uint32_t>(p.base.topk);
   a.gated = l.gated;
   a.act = act;
