@@ -399,6 +399,11 @@ def _fresh(shape, dtype, dev, stream):
     return t
 
 
+def _fresh_like(t, stream):
+    """_fresh of a contiguous tensor's shape and dtype (for the current stream a shorter way)."""
+    return torch.empty_like(t) if stream is None else _fresh(t.shape, t.dtype, t.device, stream)
+
+
 def _check_inputs(*tensors):
     dev = tensors[0].device
     for t in tensors:
@@ -859,8 +864,9 @@ def moe_unpermute_grad(grad: torch.Tensor, expanded_row_idx: torch.Tensor, batch
 # ---------------------------------------------------------------- gate, gated products, adapters
 
 def _expect(t, name, shape, dtype, dev):
-    """t: a contiguous GPU tensor of this shape and dtype on dev."""
-    if t.dtype != dtype or t.device != dev or not t.is_cuda or t.shape != shape or not t.is_contiguous():
+    """t: a contiguous GPU tensor of this shape and dtype on dev (get_device() of a
+    CPU tensor is -1; every call makes several of these checks)."""
+    if t.dtype is not dtype or t.get_device() != dev.index or t.shape != shape or not t.is_contiguous():
         raise PggError(ERR_INVALID_ARG, f"{name} must be a contiguous {dtype} {list(shape)} tensor on {dev}")
 
 
@@ -1139,7 +1145,10 @@ def moe_gate_grouped_grad(logits: torch.Tensor, expert_ids: torch.Tensor, grad_p
     dev, shape = logits.device, (d.tokens, d.topk)
     _expect(expert_ids, "expert_ids", shape, torch.int64, dev)
     _expect(grad_probs, "grad_probs", shape, torch.float32, dev)
-    out = _out(out, "out", (d.tokens, d.experts), logits.dtype, dev, stream)
+    if out is None:
+        out = _fresh_like(logits, stream)
+    else:
+        _expect(out, "out", (d.tokens, d.experts), logits.dtype, dev)
     _check(lib().pgg_moe_gate_grouped_grad(ctypes.byref(d), logits.data_ptr(), expert_ids.data_ptr(),
                                            grad_probs.data_ptr(), out.data_ptr(), _on_stream(stream, dev)),
            "pgg_moe_gate_grouped_grad")
@@ -1303,9 +1312,11 @@ def moe_combine(permuted: torch.Tensor, expanded_row_idx: torch.Tensor, probs: t
                   stream)
     if normed is not None and next_weight is None:
         raise PggError(ERR_INVALID_ARG, "normed needs next_weight")
-    out = _out(out, "out", shape, permuted.dtype, dev, stream)
-    if next_weight is not None:
-        normed = _out(normed, "normed", shape, permuted.dtype, dev, stream)
+    out = _fresh_like(residual, stream) if out is None else _out(out, "out", shape, permuted.dtype, dev, stream)
+    if next_weight is not None and normed is None:
+        normed = _fresh_like(residual, stream)
+    elif normed is not None:
+        _expect(normed, "normed", shape, permuted.dtype, dev)
     _check(lib().pgg_moe_combine(ctypes.byref(d), permuted.data_ptr(), expanded_row_idx.data_ptr(), probs.data_ptr(),
                                  residual.data_ptr(), _ptr(post_weight), _ptr(gate), _ptr(next_weight),
                                  out.data_ptr(), _ptr(normed), ws.data_ptr(), _ws_bytes(ws),
@@ -1334,11 +1345,10 @@ def moe_combine_grad(grad_out: torch.Tensor, permuted: torch.Tensor, expanded_ro
         _expect(grad_normed, "grad_normed", (d.batch, H), dtype, dev)
     ws = _scratch(workspace, lambda: _size_of(lib().pgg_moe_combine_grad_workspace_size, d,
                                               "combine_grad_workspace_size"), dev, stream)
-    fresh = lambda shape, dt: _fresh(shape, dt, dev, stream)  # noqa: E731
-    grads = (fresh((d.batch * d.topk, H), dtype), fresh((d.batch, d.topk), torch.float32), fresh((d.batch, H), dtype),
-             None if gate is None else fresh((d.batch,), torch.float32),
-             None if post_weight is None else fresh((H,), torch.float32),
-             None if next_weight is None else fresh((H,), torch.float32))
+    fresh = lambda shape: _fresh(shape, torch.float32, dev, stream)  # noqa: E731
+    grads = (_fresh_like(permuted, stream), _fresh_like(probs, stream), _fresh_like(residual, stream),
+             None if gate is None else _fresh_like(gate, stream), None if post_weight is None else fresh((H,)),
+             None if next_weight is None else fresh((H,)))
     args = CombineGradArgs(*(_ptr(t) for t in (grad_out, grad_normed, permuted, expanded_row_idx, probs, residual,
                                                post_weight, gate, next_weight) + grads))
     _check(lib().pgg_moe_combine_grad(ctypes.byref(d), ctypes.byref(args), ws.data_ptr(), _ws_bytes(ws),

@@ -249,7 +249,7 @@ hipError_t launch_w4_pack(const W4Layout& l, const uint8_t* codes, const void* s
 struct W4Plan {
   Plan base;               // sizes, tables and workspace layout (N: reduction, K: columns)
   W4Layout layout;
-  int32_t waves;           // of a workgroup, which split its part of the reduction
+  int32_t beside, waves;   // column blocks of a workgroup, and waves that split each one's reduction
   int32_t ksplit, kb_span; // splits over workgroups, and tiles of 128 k of one
   int32_t sub;
   bool tiles;              // many rows per expert: tiles of 64 rows x 256 columns

@@ -54,6 +54,7 @@ struct W4Args {
   int64_t lda;
   int32_t KB, CB, kb_span, ksplit;
   int32_t n_slots, n_col_tiles;
+  int32_t beside;           // column blocks of a workgroup
   uint32_t topk;
   int32_t gated, act;
   // without tables

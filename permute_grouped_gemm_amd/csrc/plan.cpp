@@ -800,10 +800,15 @@ pgg_status make_w4_plan(const pgg_moe_w4_desc* d, bool gated, W4Plan* p) {
   q.n_panels = 1;
   q.max_chunks = 1;
   q.regime = kStream;
+  // Rows of a tile.  An expert with more rows than a tile reads its weights again,
+  // and one of 16-bit x with many multiplies faster in the 64 x 256 tiles; a token
+  // goes to an expert once, so with an index no expert has more rows than there are
+  // tokens.  Measured in us, 16 experts, tiles of 16, 32 and 64 rows:
+  //   bf16, 7168 x 4096: 8 rows per expert 53, 60, 70; 16 62, 66, 69; 24 106, 73, 70;
+  //     32 110, 82, 84; 48 161, 142, 85; 64 202, 150, 87; 1024 3258, 2268, 945
+  //   f16, 1403 x 2039, groups of 64: 8 15, 23, 33; 32 28, 23, 35; 64 48, 39, 40; 128 86, 66, 41
   w.tiles = l.dtype != PGG_F32 && M > 32 * l.G && !(indexed && d->batch <= 32);
-  if (const char* e = getenv("W4_TILES")) w.tiles = l.dtype != PGG_F32 && atoi(e);
   q.bm = w.tiles ? 64 : l.dtype == PGG_F32 || M <= 12 * l.G || (indexed && d->batch <= 16) ? 16 : 32;
-  if (const char* e = getenv("W4_BM")) if (!w.tiles && l.dtype != PGG_F32) q.bm = atoi(e);
   const int64_t max_tiles = std::min<int64_t>(M, (M + q.bm - 1) / q.bm + l.G);   // each holds a row at least
   const int64_t col_tiles = w.tiles ? (l.CB + 3) / 4 : l.CB;
   if (max_tiles * l.CB >= (int64_t(1) << 22)) return PGG_ERR_UNSUPPORTED;   // launches of fewer than 2^32 lanes
@@ -814,16 +819,27 @@ pgg_status make_w4_plan(const pgg_moe_w4_desc* d, bool gated, W4Plan* p) {
   q.fused_prep = M <= 1024;
   const int64_t busy = std::min<int64_t>(max_tiles, M / q.bm + (l.G + 1) / 2 + 1) * col_tiles;
   w.sub = l.sub;
-  w.waves = busy >= 512 ? 4 : 8;
-  if (const char* e = getenv("W4_WAVES")) w.waves = atoi(e);
-  w.ksplit = 1;
-  w.kb_span = l.KB;
-  const int64_t fill = w.tiles ? 512 : 256, least = w.tiles ? 8 : 16;   // workgroups; tiles of 128 k of a split
-  if (busy <= fill / 2 && l.KB >= 2 * least) {
-    const int64_t split = std::min<int64_t>(std::min<int64_t>(fill / busy, l.KB / least), 16);
-    w.kb_span = static_cast<int32_t>((l.KB + split - 1) / split);
-    w.ksplit = (l.KB + w.kb_span - 1) / w.kb_span;
+  // Tiles of few rows: about three waves to a SIMD.  With many column blocks one
+  // wave takes the whole reduction, and four blocks side by side share their rows
+  // of x in L1; with few the reduction is split over waves, and with very few over
+  // workgroups.  Measured in us, waves per block x blocks side by side:
+  //   4096 blocks, 7168 deep, 16 rows: 4x1 212, 2x2 201, 1x4 197; 2048: 109, 102, 99
+  //   1024 blocks: 8 rows 48.6, 45.6, -; 16 rows 58.2, 53.2, -; 768: 37.3, 42.8, 53.0
+  //   2048 blocks, 1408 deep, 12 rows: 37.6, 29.4, 26.7;  176, 2048 deep: 11.6, 16.9, 27.0, 8x1 11.1
+  //   over workgroups (8x1, 4x1 with 4 splits): 32 blocks, 7168 deep 13.5, 11.2; 112 14.4, 13.6;
+  //     22 blocks, 2048 deep 9.2, 11.7
+  w.waves = busy >= 2048 ? 1 : busy >= 1280 ? 2 : busy >= 256 ? 4 : 8;
+  w.beside = busy >= 2048 ? 4 : busy >= 1280 ? 2 : 1;
+  int64_t split = 1;
+  if (w.tiles) {   // two workgroups to a compute unit
+    if (busy <= 256) split = std::min<int64_t>(std::min<int64_t>(512 / busy, l.KB / 8), 16);
+  } else if (busy <= 128 && l.KB >= 28) {
+    split = std::min<int64_t>(l.KB / 14, 4);
+    w.waves = 4;
   }
+  split = std::max<int64_t>(split, 1);
+  w.kb_span = static_cast<int32_t>((l.KB + split - 1) / split);
+  w.ksplit = (l.KB + w.kb_span - 1) / w.kb_span;
   q.ksplit = w.ksplit;
   size_t off = 0;
   q.off_header = off;   off = align_up(off + sizeof(WsHeader), kRegionAlign);

@@ -1,13 +1,17 @@
 // Experts' products with 4-bit weights, few rows per expert: bound by reading
 // the used experts' weights once.
 //
-// A workgroup takes BM rows x 64 columns; its waves split the reduction, each
-// walking its own tiles of 128 k on its own, without a barrier: 4 KiB of codes a
-// tile go straight into registers, D tiles ahead, and x into the same registers'
-// neighbours (its rows are read by every column block, from L2).  The waves' sums
-// meet in LDS at the end.  Where that makes too few workgroups, the reduction is
-// split over workgroups too, and a second kernel adds the partial results in
-// order.
+// A wave takes BM rows x 64 columns and a part of the reduction, and walks its
+// tiles of 128 k on its own, without a barrier: 4 KiB of codes a tile go straight
+// into registers, two tiles ahead, and so does x (its rows are read by every
+// column block, from L1 and L2).  A workgroup's waves share column blocks and parts
+// as the plan says; the sums of one block meet in LDS at the end.  Where that makes
+// too few workgroups, the reduction is split over workgroups too, and a second
+// kernel adds the partial results in order.
+//
+// Measured: 128 rows, 12 experts of 7168 x 4096 in groups of 128, bf16, 182 MB in
+// 37 us, 4.9 TB/s (a large copy on this card: 4.9); one row for each of 64 experts
+// of that size 152 us, 6.4 TB/s of codes and scales.
 #include <algorithm>
 
 #include "pgg_w4.h"
@@ -16,69 +20,68 @@ namespace pgg {
 
 namespace {
 
-template <class T, int RB, int SUB>
-struct W4Stage {
-  W4Weights<T, SUB> w;
+// What a wave holds of x for one tile.
+template <class T, int RB>
+struct W4Rows {
   u32x4_t x[RB][4][W4Type<T>::kVec];
 
-  // kb >= kb1: nothing that counts, but as many loads
-  __device__ __forceinline__ void load(const W4Args& a, const W4Planes& planes, int kb, int kb1,
-                                       const typename T::elem* const (&px)[RB], int lane) {
-    w.load(planes, static_cast<uint32_t>(kb) * a.CB, kb < kb1, lane);
+  // kb past the last: the last again
+  __device__ __forceinline__ void load(const W4Args& a, int kb, const typename T::elem* const (&px)[RB], int lane) {
     const int64_t k0 = static_cast<int64_t>(min(kb, a.KB - 1)) * kW4K;
 #pragma unroll
     for (int i = 0; i < RB; ++i)
 #pragma unroll
       for (int s = 0; s < 4; ++s) w4_load_x<T>(x[i][s], px[i] + k0 + 32 * s, a.K - k0 - 32 * s - 8 * (lane >> 4));
   }
-
-  __device__ __forceinline__ void multiply(f32x4_t (&acc)[RB][4]) const {
-    using Mma = typename W4Type<T>::Mma;
-    constexpr int P = W4Type<T>::kParts;
-#pragma unroll
-    for (int u = 0; u < SUB; ++u) {
-      f32x4_t part[RB][4], sum[RB];
-#pragma unroll
-      for (int i = 0; i < RB; ++i) {
-        sum[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) part[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-      }
-#pragma unroll
-      for (int s = u * 4 / SUB; s < (u + 1) * 4 / SUB; ++s) {
-        __builtin_amdgcn_sched_barrier(0);   // the operands of one step at a time
-        u32x4_t f[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f[j] = w4_expand<Mma>(w.code[j][s]);
-#pragma unroll
-        for (int i = 0; i < RB; ++i) {
-          u32x4_t p[P];
-          w4_parts<T, false>(x[i][s], p);
-#pragma unroll
-          for (int q = 0; q < P; ++q) {
-            mma_block<Mma>(sum[i], p[q], ones<Mma>());
-#pragma unroll
-            for (int j = 0; j < 4; ++j) mma_block<Mma>(part[i][j], p[q], f[j]);
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < RB; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float scale = w.scale[u].get(j), zero = w.zero_of(u, j);
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-            acc[i][j][v] = __builtin_fmaf(scale, __builtin_fmaf(-zero, sum[i][v], part[i][j][v]), acc[i][j][v]);
-        }
-    }
-  }
 };
 
-// Tiles of 128 k that are loaded ahead, and waves to a SIMD: more tiles cost waves.
-// Measured, 128 rows x 7168 x 4096, 12 experts, bf16: 2 tiles and 3 waves 38.6 us,
-// 3 and 2 43.5, 4 and 2 43.5.
-constexpr int kW4Ahead = 2;
+template <class T, int RB, int SUB>
+__device__ __forceinline__ void w4_multiply(const W4Weights<T, SUB>& w, const W4Rows<T, RB>& rows, f32x4_t (&acc)[RB][4]) {
+  using Mma = typename W4Type<T>::Mma;
+  constexpr int P = W4Type<T>::kParts;
+#pragma unroll
+  for (int u = 0; u < SUB; ++u) {
+    f32x4_t part[RB][4], sum[RB];
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      sum[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) part[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+#pragma unroll
+    for (int s = u * 4 / SUB; s < (u + 1) * 4 / SUB; ++s) {
+      __builtin_amdgcn_sched_barrier(0);   // the operands of one step at a time
+      u32x4_t f[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = w4_expand<Mma>(w.code[j][s]);
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+        u32x4_t p[P];
+        w4_parts<T, false>(rows.x[i][s], p);
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+          mma_block<Mma>(sum[i], p[q], ones<Mma>());
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mma_block<Mma>(part[i][j], p[q], f[j]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float scale = w.scale[u].get(j), zero = w.zero_of(u, j);
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          acc[i][j][v] = __builtin_fmaf(scale, __builtin_fmaf(-zero, sum[i][v], part[i][j][v]), acc[i][j][v]);
+      }
+  }
+}
+
+// Tiles of 128 k that are loaded ahead, and waves to a SIMD.  More tiles cost
+// registers and so waves: 3 tiles, of codes alone or of both, took 40 to 44 us
+// where 2 take 37 (128 rows x 7168 x 4096, 12 experts, bf16).
+constexpr int kAhead = 2;
 template <class T, int RB>
 constexpr int kW4Waves = __is_same(T, TF32) || RB == 2 ? 2 : 3;
 
@@ -88,7 +91,7 @@ template <class T, int RB, int SUB>
 __global__ __launch_bounds__(kW4MaxWaves * 64) __attribute__((amdgpu_waves_per_eu(kW4Waves<T, RB>)))
 void w4_rows_kernel(W4Args a) {
   using E = typename T::elem;
-  constexpr int BM = 16 * RB, D = kW4Ahead, kPitch = kW4Cols + 4;
+  constexpr int BM = 16 * RB, kPitch = kW4Cols + 4;
   __shared__ float lds[kW4MaxWaves * BM * kPitch];
   __shared__ int32_t s_rows[BM];
   static_assert(sizeof(lds) * 8 >= kLocalRows, "a bit per row for the check of the index");
@@ -101,21 +104,25 @@ void w4_rows_kernel(W4Args a) {
     }
     --bid;
   }
-  const int cb = bid % a.CB;
-  const int split = bid / a.CB % a.ksplit;
+  const int ct = bid % a.n_col_tiles;
+  const int split = bid / a.n_col_tiles % a.ksplit;
   MTile tile;
-  if (!w4_find(a, bid / a.CB / a.ksplit, BM, tile, s_rows)) return;
+  if (!w4_find(a, bid / a.n_col_tiles / a.ksplit, BM, tile, s_rows)) return;
 
-  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // waves: `beside` with column blocks side by side, and these times `waves`
+  // parts of the reduction
+  const int lane = threadIdx.x & 63, beside = a.beside, waves = (blockDim.x >> 6) / beside;
+  const int id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = id / beside;
+  const int cb = ct * beside + id % beside;
+  const bool there = cb < a.CB;   // the last workgroup of a row may have waves too many
   const E* px[RB];
 #pragma unroll
   for (int i = 0; i < RB; ++i)
     px[i] = static_cast<const E*>(a.x) + s_rows[16 * i + (lane & 15)] * a.lda + 8 * (lane >> 4);
   const W4Planes planes =
-      w4_planes<T, SUB>(a, static_cast<int64_t>(__builtin_amdgcn_readfirstlane(tile.g)) * a.KB * a.CB + cb);
+      w4_planes<T, SUB>(a, static_cast<int64_t>(__builtin_amdgcn_readfirstlane(tile.g)) * a.KB * a.CB + (there ? cb : 0));
   // this wave's tiles of the workgroup's [first, first + count)
-  const int first = split * a.kb_span, count = min(a.kb_span, a.KB - first);
+  const int first = split * a.kb_span, count = there ? min(a.kb_span, a.KB - first) : 0;
   const int kb0 = first + count * wave / waves, kb1 = first + count * (wave + 1) / waves;
 
   f32x4_t acc[RB][4];
@@ -124,16 +131,22 @@ void w4_rows_kernel(W4Args a) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  W4Stage<T, RB, SUB> st[D];
+  W4Weights<T, SUB> w[kAhead];
+  W4Rows<T, RB> rows[kAhead];
+  auto load = [&](int kb, int to) {
+    rows[to].load(a, kb, px, lane);
+    __builtin_amdgcn_sched_barrier(0);
+    w[to].load(planes, static_cast<uint32_t>(kb) * a.CB, kb < kb1, lane);
+    __builtin_amdgcn_sched_barrier(0);
+  };
 #pragma unroll
-  for (int d = 0; d < D; ++d) st[d].load(a, planes, kb0 + d, kb1, px, lane);
-  for (int kb = kb0; kb < kb1; kb += D) {
+  for (int d = 0; d < kAhead; ++d) load(kb0 + d, d);
+  for (int kb = kb0; kb < kb1; kb += kAhead) {
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
-      if (kb + d < kb1) st[d].multiply(acc);
+    for (int d = 0; d < kAhead; ++d) {
+      if (kb + d < kb1) w4_multiply<T, RB, SUB>(w[d], rows[d], acc);
       __builtin_amdgcn_sched_barrier(0);
-      st[d].load(a, planes, kb + d + D, kb1, px, lane);
-      __builtin_amdgcn_sched_barrier(0);
+      load(kb + d + kAhead, d);
     }
   }
   if (w4_not_finite(acc)) w4_again<T, RB, SUB>(a, planes, kb0, kb1, px, lane, acc);
@@ -144,19 +157,22 @@ void w4_rows_kernel(W4Args a) {
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const f32x4_t q = {acc[i][0][v], acc[i][1][v], acc[i][2][v], acc[i][3][v]};
-      *reinterpret_cast<f32x4_t*>(lds + (wave * BM + 16 * i + 4 * (lane >> 4) + v) * kPitch + 4 * (lane & 15)) = q;
+      *reinterpret_cast<f32x4_t*>(lds + (id * BM + 16 * i + 4 * (lane >> 4) + v) * kPitch + 4 * (lane & 15)) = q;
     }
   __syncthreads();
-  for (int p = threadIdx.x; p < tile.rows * 16; p += blockDim.x) {
-    const int r = p >> 4, c = p & 15;
-    f32x4_t v = *reinterpret_cast<const f32x4_t*>(lds + r * kPitch + 4 * c);
-    for (int w = 1; w < waves; ++w) v += *reinterpret_cast<const f32x4_t*>(lds + (w * BM + r) * kPitch + 4 * c);
+  for (int p = threadIdx.x; p < tile.rows * 16 * beside; p += blockDim.x) {
+    const int c = p & 15, b = (p >> 4) % beside, r = (p >> 4) / beside;
+    const int block = ct * beside + b;
+    if (block >= a.CB) continue;
+    f32x4_t v = *reinterpret_cast<const f32x4_t*>(lds + (b * BM + r) * kPitch + 4 * c);
+    for (int w = 1; w < waves; ++w)
+      v += *reinterpret_cast<const f32x4_t*>(lds + ((w * beside + b) * BM + r) * kPitch + 4 * c);
     const int64_t row = tile.row0 + r;
     if (a.part) {
-      float* to = a.part + (static_cast<int64_t>(split) * a.M + row) * (64ll * a.CB) + 64ll * cb + 4 * c;
+      float* to = a.part + (static_cast<int64_t>(split) * a.M + row) * (64ll * a.CB) + 64ll * block + 4 * c;
       *reinterpret_cast<f32x4_t*>(to) = v;
     } else {
-      w4_store<T>(a, row, cb, c, v);
+      w4_store<T>(a, row, block, c, v);
     }
   }
 }
@@ -226,8 +242,8 @@ unsigned blocks_for(int64_t n) { return static_cast<unsigned>(std::min<int64_t>(
 
 template <class T, int RB, int SUB>
 hipError_t launch_rows(const W4Plan& p, const W4Args& a, hipStream_t s) {
-  const unsigned blocks = (a.local ? 1u : 0u) + static_cast<unsigned>(a.n_slots) * a.CB * a.ksplit;
-  hipLaunchKernelGGL((w4_rows_kernel<T, RB, SUB>), dim3(blocks), dim3(64u * p.waves), 0, s, a);
+  const unsigned blocks = (a.local ? 1u : 0u) + static_cast<unsigned>(a.n_slots) * a.n_col_tiles * a.ksplit;
+  hipLaunchKernelGGL((w4_rows_kernel<T, RB, SUB>), dim3(blocks), dim3(64u * p.waves * a.beside), 0, s, a);
   return hipGetLastError();
 }
 
@@ -303,7 +319,8 @@ hipError_t launch_w4(const W4Plan& p, int32_t act, const void* x, const void* pa
   a.ksplit = p.ksplit;
   a.sums = reinterpret_cast<const float*>(static_cast<const char*>(ws) + p.off_sums);
   a.n_slots = p.base.max_tiles;
-  a.n_col_tiles = (l.CB + 3) / 4;
+  a.beside = p.tiles ? 4 : p.beside;
+  a.n_col_tiles = (l.CB + a.beside - 1) / a.beside;
   a.topk = static_cast<uint32_t>(p.base.topk);
   a.gated = l.gated;
   a.act = act;
