@@ -24,8 +24,8 @@
 // grid and keeps its part of the weights' gradients in registers (of long rows in
 // memory); a second kernel adds the workgroups' parts.
 //
-// The routing index is read as it is where it holds rows (row_idx_type 1) and
-// inverted by a launch before otherwise.  It is checked beside the work: in one
+// The routing index is read as it is where it holds rows (row_idx_type 1);
+// otherwise it is searched where it is short, and inverted by a launch before.  It is checked beside the work: in one
 // spare workgroup with a bit per row where M is small, else by workgroups of the
 // same launch against the tables that the launch before has filled.  Rows
 // outside [0, M) read and write row 0.
@@ -61,6 +61,7 @@ struct CombineArgs {
   float alpha, eps, inv_h;
   int32_t check;        // workgroups in front that check the index
   int32_t bits;         // 1: one, with a bit per row
+  int32_t scan;         // 1: a token's rows are looked for in eri
   PrepArgs prep;
   WsView ws;
 };
@@ -214,10 +215,11 @@ struct Slots {
   int32_t row;
   float prob;
 
-  __device__ __forceinline__ void load(const CombineArgs& a, int64_t p, int n) {
-    const int lane = threadIdx.x & 63;
-    const int64_t at = p + min(lane, n - 1);
-    const int64_t r = a.inv ? static_cast<int64_t>(a.inv[at]) : a.eri[at];
+  // found: the token's rows as find_rows leaves them, j the slot of position p
+  __device__ __forceinline__ void load(const CombineArgs& a, int64_t p, int n, const int32_t* found, int64_t j) {
+    const int lane = threadIdx.x & 63, q = min(lane, n - 1);
+    const int64_t at = p + q;
+    const int64_t r = a.scan ? found[j + q] : a.inv ? a.inv[at] : a.eri[at];
     row = static_cast<uint64_t>(r) < static_cast<uint64_t>(a.M) ? static_cast<int32_t>(r) : 0;
     prob = a.probs[at];
   }
@@ -226,6 +228,21 @@ struct Slots {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int32_t, prob), q));
   }
 };
+
+// Rows of token t's slots where the index holds positions and is short: every
+// workgroup looks through all of it.  Ends with a barrier.
+constexpr int kScanSlots = 64;
+__device__ __forceinline__ void find_rows(const CombineArgs& a, int64_t t, int32_t* found) {
+  if (threadIdx.x < kScanSlots) found[threadIdx.x] = 0;
+  __syncthreads();
+  const int64_t p0 = t * a.topk;
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < a.M; i += blockDim.x) {
+    const int64_t j = a.eri[i] - p0;
+    if (j >= 0 && j < a.topk) found[j] = static_cast<int32_t>(i);
+  }
+  __syncthreads();
+}
 
 // The rows of n <= HELD slots (after the last, the last again).
 template <class T, int NCH, bool EVEN, bool STREAM, int HELD>
@@ -278,7 +295,9 @@ __global__ __launch_bounds__(kMaxThreads<NCH>) void combine_kernel(CombineArgs a
   int left[NCH];
   pieces(a.H, h, left);
   Slots slots;
-  slots.load(a, t * a.topk, static_cast<int>(min<int64_t>(HELD, a.topk)));
+  __shared__ int32_t s_found[kScanSlots];
+  if (a.scan) find_rows(a, t, s_found);
+  slots.load(a, t * a.topk, static_cast<int>(min<int64_t>(HELD, a.topk)), s_found, 0);
   Eight<T> res[NCH], post[NCH], next[NCH], y[HELD][NCH];
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
@@ -294,7 +313,7 @@ __global__ __launch_bounds__(kMaxThreads<NCH>) void combine_kernel(CombineArgs a
     for (int k = 0; k < 8; ++k) c[i][k] = 0.0f;
   for (int64_t j0 = 0; j0 < a.topk; j0 += HELD) {
     const int n = static_cast<int>(min<int64_t>(HELD, a.topk - j0));
-    if (j0) slots.load(a, t * a.topk + j0, n);
+    if (j0) slots.load(a, t * a.topk + j0, n, s_found, j0);
     load_slots<T, NCH, EVEN, true, HELD>(a, slots, left, h, y);
     add_slots<T, NCH, HELD>(slots, n, y, c);
   }
@@ -351,6 +370,7 @@ __global__ __launch_bounds__(kMaxThreads<NCH>) void combine_grad_kernel(CombineA
     check_index(a, blockIdx.x, s.bits);
     return;
   }
+  __shared__ int32_t s_found[kScanSlots];
   const int64_t first = static_cast<int64_t>(blockIdx.x) - a.check, step = static_cast<int64_t>(gridDim.x) - a.check;
   uint32_t h[NCH];
   int left[NCH];
@@ -382,7 +402,8 @@ __global__ __launch_bounds__(kMaxThreads<NCH>) void combine_grad_kernel(CombineA
   };
   for (int64_t t = first; t < a.batch; t += step) {
     Slots slots;
-    slots.load(a, t * a.topk, static_cast<int>(min<int64_t>(HELD, a.topk)));
+    if (a.scan) find_rows(a, t, s_found);
+    slots.load(a, t * a.topk, static_cast<int>(min<int64_t>(HELD, a.topk)), s_found, 0);
     Eight<T> res_reg[NCH], go_reg[NCH], gn_reg[NCH], y[HELD][NCH];
     if constexpr (!kLong) {
       // the weights are widened where they are used: as loop invariants they would take 16 registers, not 8
@@ -408,7 +429,7 @@ __global__ __launch_bounds__(kMaxThreads<NCH>) void combine_grad_kernel(CombineA
       for (int k = 0; k < 8; ++k) c[i][k] = 0.0f;
     for (int64_t j0 = 0; j0 < a.topk; j0 += HELD) {
       const int n = static_cast<int>(min<int64_t>(HELD, a.topk - j0));
-      if (!ONCE && j0) slots.load(a, t * a.topk + j0, n);
+      if (!ONCE && j0) slots.load(a, t * a.topk + j0, n, s_found, j0);
       load_slots<T, NCH, EVEN, false, HELD>(a, slots, left, h, y);
       add_slots<T, NCH, HELD>(slots, n, y, c);
       if (ONCE) break;
@@ -518,7 +539,7 @@ __global__ __launch_bounds__(kMaxThreads<NCH>) void combine_grad_kernel(CombineA
     for (int64_t j0 = 0; j0 < a.topk; j0 += HELD) {
       const int n = static_cast<int>(min<int64_t>(HELD, a.topk - j0));
       if constexpr (!ONCE) {   // the rows did not stay
-        slots.load(a, t * a.topk + j0, n);
+        slots.load(a, t * a.topk + j0, n, s_found, j0);
         load_slots<T, NCH, EVEN, false, HELD>(a, slots, left, h, y);
         __syncthreads();   // the sums of the slots before have been read
       }
@@ -623,7 +644,10 @@ hipError_t launch_any(const CombinePlan& p, CombineArgs& a, const int64_t* eri, 
   a.prep.row_idx_type = p.row_idx_type;
   // a spare workgroup with a bit per row, 16 entries to a thread at most
   const int64_t threads = p.threads(grad);
-  a.bits = p.row_idx_type == 1 && p.M <= std::min<int64_t>(kBitRows, 16 * threads);
+  // Short indexes of positions are searched by every token's workgroup, which saves
+  // the launch that inverts them.
+  a.scan = p.row_idx_type == 0 && p.M <= std::min<int64_t>(kBitRows, 8 * threads) && p.topk <= kScanSlots;
+  a.bits = a.scan || (p.row_idx_type == 1 && p.M <= std::min<int64_t>(kBitRows, 16 * threads));
   a.check = a.bits ? 1 : static_cast<int32_t>(std::min<int64_t>((p.M + 4 * threads - 1) / (4 * threads), 1024));
   hipError_t e = hipSuccess;
   if (!a.bits) {

@@ -192,28 +192,43 @@ __global__ __launch_bounds__(256) void w4_finish_kernel(W4Args a) {
   }
 }
 
-// The layout: a thread makes the 16 bytes of one lane of one block.
+// The layout: a thread makes the 16 bytes of one lane in all four blocks, from 4
+// codes (gated: 2 gate and 2 up) of 32 rows.
 __global__ __launch_bounds__(256) void w4_pack_codes_kernel(const uint8_t* codes, uint8_t* packed, int64_t K, int64_t N,
                                                             int32_t KB, int32_t CB, int32_t gated, int64_t total) {
   const int64_t F = N / 2, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
   for (int64_t id = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; id < total; id += step) {
-    const int lane = static_cast<int>(id & 63), j = static_cast<int>((id >> 6) & 3);
-    const int64_t tile = id >> 8, cb = tile % CB, kb = tile / CB % KB, g = tile / CB / KB;
-    const int64_t n = w4_column(cb, lane & 15, j, gated, F);
-    const bool inside = gated ? cb * 32 + 2 * (lane & 15) + (j & 1) < F : n < N;
-    u32x4_t v;
+    const int lane = static_cast<int>(id & 63), i16 = lane & 15;
+    const int64_t tile = id >> 6, cb = tile % CB, kb = tile / CB % KB, g = tile / CB / KB;
+    const int64_t n0 = w4_column(cb, i16, 0, gated, F), n2 = w4_column(cb, i16, 2, gated, F);
+    const int64_t left = (gated ? F : N) - n0;   // columns from n0 on
+    const int64_t k0 = kb * kW4K + 8 * (lane >> 4);
+    const uint8_t* from = codes + (g * K + k0) * N;
+    u32x4_t v[4];
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      uint32_t w = 0;
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int64_t k = kb * kW4K + 32 * s + 8 * (lane >> 4) + i;
-        const uint32_t c = inside && k < K ? codes[(g * K + k) * N + n] & 15u : 0u;
-        w |= c << (8 * (i & 3) + 4 * (i >> 2));
+        if (k0 + 32 * s + i >= K) continue;
+        const uint8_t* row = from + (32 * s + i) * N;
+        uint8_t c[4] = {0, 0, 0, 0};
+        if (left >= (gated ? 2 : 4)) {
+          __builtin_memcpy(c, row + n0, 2);
+          __builtin_memcpy(c + 2, row + n2, 2);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if ((gated ? j & 1 : j) < left) c[j] = row[w4_column(cb, i16, j, gated, F)];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] |= (c[j] & 15u) << (8 * (i & 3) + 4 * (i >> 2));
       }
-      v[s] = w;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j][s] = w[j];
     }
-    reinterpret_cast<u32x4_t*>(packed)[id] = v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) reinterpret_cast<u32x4_t*>(packed)[tile * 256 + 64 * j + lane] = v[j];
   }
 }
 
@@ -269,7 +284,7 @@ hipError_t launch_typed(const W4Plan& p, const W4Args& a, hipStream_t s) {
 hipError_t launch_w4_pack(const W4Layout& l, const uint8_t* codes, const void* scales, const uint8_t* zeros,
                           void* packed, hipStream_t s) {
   char* base = static_cast<char*>(packed);
-  const int64_t lanes = l.tiles * 256, entries = l.tiles * l.sub * 64;
+  const int64_t lanes = l.tiles * 64, entries = l.tiles * l.sub * 64;
   hipLaunchKernelGGL(w4_pack_codes_kernel, dim3(blocks_for(lanes)), dim3(256), 0, s, codes,
                      reinterpret_cast<uint8_t*>(base), l.K, l.N, l.KB, l.CB, l.gated, lanes);
   hipError_t e = hipGetLastError();
