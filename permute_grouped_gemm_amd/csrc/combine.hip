@@ -25,10 +25,11 @@
 // memory); a second kernel adds the workgroups' parts.
 //
 // The routing index is read as it is where it holds rows (row_idx_type 1);
-// otherwise it is searched where it is short, and inverted by a launch before.  It is checked beside the work: in one
-// spare workgroup with a bit per row where M is small, else by workgroups of the
-// same launch against the tables that the launch before has filled.  Rows
-// outside [0, M) read and write row 0.
+// otherwise it is searched where it is short, and inverted by a launch before
+// where it is long.  It is checked beside the work: in one spare workgroup with a
+// bit per row where M is small, else by workgroups of the same launch against the
+// tables that the launch before has filled.  Rows outside [0, M) read and write
+// row 0.
 #include <algorithm>
 
 #include "pgg_nn.h"

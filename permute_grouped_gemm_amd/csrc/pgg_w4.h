@@ -155,8 +155,8 @@ __device__ __forceinline__ void w4_parts(const u32x4_t (&x)[W4Type<T>::kVec], u3
 template <class T>
 struct W4Scales {
   u32x2_t v;
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t p, uint32_t off) {
-    v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(p, off, 0, 0));
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t p, uint32_t off, uint32_t base = 0) {
+    v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(p, off, base, 0));
   }
   __device__ __forceinline__ float get(int j) const {
     return to_float<T>(static_cast<uint16_t>(v[j >> 1] >> (16 * (j & 1))));
@@ -165,8 +165,8 @@ struct W4Scales {
 template <>
 struct W4Scales<TF32> {
   f32x4_t v;
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t p, uint32_t off) {
-    v = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(p, off, 0, 0));
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t p, uint32_t off, uint32_t base = 0) {
+    v = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(p, off, base, 0));
   }
   __device__ __forceinline__ float get(int j) const { return v[j]; }
 };
@@ -215,6 +215,21 @@ struct W4Weights {
       const uint32_t at = (tile * SUB + u) * 64 + 4 * (lane & 15);
       scale[u].load(p.scales, there ? at * static_cast<uint32_t>(sizeof(typename T::elem)) : kOutside);
       zero[u] = p.have_zeros ? __builtin_amdgcn_raw_buffer_load_b32(p.zeros, there ? at : kOutside, 0, 0) : 0x08080808u;
+    }
+  }
+  // The same for a tile that is there, its number in a scalar register, and that
+  // other workgroups read again.
+  __device__ __forceinline__ void load_there(const W4Planes& p, uint32_t tile, int lane) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      code[j] = __builtin_bit_cast(
+          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(p.codes, lane * 16 + 1024 * j, tile * kW4TileBytes, 0));
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) {
+      constexpr uint32_t kElem = sizeof(typename T::elem);
+      const uint32_t at = 4 * (lane & 15), from = (tile * SUB + u) * 64;
+      scale[u].load(p.scales, at * kElem, from * kElem);
+      zero[u] = p.have_zeros ? __builtin_amdgcn_raw_buffer_load_b32(p.zeros, at, from, 0) : 0x08080808u;
     }
   }
   __device__ __forceinline__ float zero_of(int u, int j) const {

@@ -193,3 +193,19 @@ def test_workspaces_stay_small():
     assert st == pgg.OK and n <= 2 * 4 * M + 17 * 8 + 16 * (M + 16) + 8 * 512 + 4 * 2048 * 7168 // 32
     st, n = _size(pgg.lib().pgg_moe_combine_grad_workspace_size, combine(batch=13824, topk=8, H=7168))
     assert st == pgg.OK and n <= 2 * 4 * 110592 + 2 * 4 * 4096 * 7168
+
+
+def test_sizes_that_fit_a_launch():
+    L = pgg.lib()
+    # 4 rows to a workgroup of 256 lanes at most 1024 experts, a row to a wave above
+    for tokens, status in (((1 << 26) - 4, pgg.ERR_INVALID_ARG), ((1 << 26) - 3, pgg.ERR_UNSUPPORTED)):
+        d = gate(T=tokens, E=1000, groups=1, kept=1)
+        assert L.pgg_moe_gate_grouped(ctypes.byref(d), None, None, FAKE, FAKE, None) == status
+        assert L.pgg_moe_gate_grouped_grad(ctypes.byref(d), None, FAKE, FAKE, FAKE, None) == status
+    # 256 lanes to 16 rows (fp32) and 256 columns
+    for rows, status in ((16 * ((1 << 24) - 2), pgg.OK), (16 * ((1 << 24) - 1), pgg.ERR_UNSUPPORTED)):
+        d = moe_w4(batch=rows, topk=1, idx=0, G=1, K=32, N=64, dtype=F32)
+        assert _size(L.pgg_moe_w4_workspace_size, d)[0] == status
+    # a workgroup of 64 lanes to a token
+    for batch, status in (((1 << 26) - 1025, pgg.OK), ((1 << 26) - 1024, pgg.ERR_UNSUPPORTED)):
+        assert _size(L.pgg_moe_combine_workspace_size, combine(batch=batch, topk=1, H=8))[0] == status
