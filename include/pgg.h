@@ -628,7 +628,9 @@ pgg_status pgg_lora_fwd(const pgg_lora_desc* desc, const void* x, const void* we
  * chosen only after the others of the chosen groups, and has weight 0; a group
  * without any other expert comes after those with one, and in a row of -inf the
  * choice is experts 0..topk-1 with weights 0.  A key that is NaN counts as larger
- * than any number, and a NaN logit makes every weight that it enters NaN.
+ * than any number, and so do a NaN logit's and, for softmax, a logit of +inf's,
+ * which is NaN (among themselves they and keys past 2^1000 are equal).  A NaN
+ * logit makes every weight that it enters NaN.
  * Constraints: groups divides experts, topk_groups <= groups, topk <=
  * topk_groups * (experts / groups).  Limits: experts <= 8192, topk <=
  * PGG_GATE_MAX_TOPK, groups <= PGG_GATE_MAX_GROUPS, tokens <= 2^26 - 4.  No
@@ -684,6 +686,7 @@ pgg_status pgg_moe_gate_grouped_grad(const pgg_moe_gate_grouped_desc* desc, cons
  * With `gated` the columns are gate columns, then as many up columns, for
  * pgg_moe_glu_w4; without, they are for pgg_moe_fwd_w4.
  * group_size is 32, 64 or a multiple of 128; rows need not be a multiple of it.
+ * Limit: rows * cols, each rounded up to 128 and 64, below 2^32 for a group.
  */
 typedef struct {
   int64_t groups, rows, cols;
@@ -712,8 +715,8 @@ pgg_status pgg_w4_pack(const pgg_w4_desc* desc, const uint8_t* codes, const void
  * fp32; the result is rounded once.  (A group's sum of (code - zero) * x has to
  * be finite in fp32.)
  * The workspace holds the tables and, where the reduction is split, fp32
- * partial results; where the rows of x are many and not 16-byte aligned, a copy
- * of them with padded rows, and for many rows the rows' sums over 32 columns.
+ * partial results; where the rows of x are not whole pieces of 16 bytes, a copy of
+ * them with padded rows, and for many rows the rows' sums over the scales' groups.
  * Errors, alignment and workspace rules are pgg_moe_fwd's.
  */
 typedef struct {
@@ -754,8 +757,9 @@ pgg_status pgg_moe_glu_w4(const pgg_moe_w4_desc* desc, const void* x, const void
  * fp32 arithmetic; `normed` comes from the unrounded out; each output is rounded
  * once.  Sums run in a fixed order.  The routing index is checked on the device
  * (out of range / not a permutation: the workspace error word; outputs
- * unspecified).  Limits: hidden <= 16384, M < 2^31 - 1.  Alignment
- * and workspace rules are pgg_moe_unpermute's.
+ * unspecified).  `out` may be `residual`; no other output may alias an input.
+ * Limits: hidden <= 16384, M < 2^31 - 1.  Alignment and workspace rules are
+ * pgg_moe_unpermute's.
  */
 typedef struct {
   int64_t batch, topk;

@@ -199,3 +199,16 @@ def test_x_past_2_31_bytes(M):
         want, bound = ref.w4_fwd(x[pick].cpu(), codes[g:g + 1].cpu(), scales[g:g + 1].cpu(), None, gs,
                                  torch.tensor([len(pick)]))
         ops_ref.assert_within(y[pick], want, bound, f"group {g}")
+
+
+@pytest.mark.parametrize("batch,H", [(16, 7168), (333, 2039), (40, 64), (3, 16384)])
+def test_residual_stream_in_place(batch, H):
+    gen = torch.Generator(device=DEV).manual_seed(0)
+    rand = lambda *s: torch.randn(s, generator=gen, device=DEV).bfloat16()  # noqa: E731
+    permuted, eri = rand(batch * 4, H), torch.randperm(batch * 4, generator=gen, device=DEV)
+    probs, residual, post, nxt = torch.rand((batch, 4), device=DEV), rand(batch, H), rand(H), rand(H)
+    kw = dict(row_idx_type=1, post_weight=post, next_weight=nxt)
+    out, normed = pgg.moe_combine(permuted, eri, probs, residual, **kw)
+    again, normed_again = pgg.moe_combine(permuted, eri, probs, residual, out=residual, **kw)
+    assert again.data_ptr() == residual.data_ptr()
+    assert torch.equal(again, out) and torch.equal(normed_again, normed)
