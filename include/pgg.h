@@ -627,7 +627,8 @@ pgg_status pgg_lora_fwd(const pgg_lora_desc* desc, const void* x, const void* we
  * A logit of -inf excludes an expert: it adds nothing to its group's score, is
  * chosen only after the others of the chosen groups, and has weight 0; a group
  * without any other expert comes after those with one, and in a row of -inf the
- * choice is experts 0..topk-1 with weights 0.  A key that is NaN counts as larger
+ * choice is experts 0..topk-1 with weights 0.  A bias of -inf does the same to the
+ * choice, and an expert chosen all the same has its score's weight.  A key that is NaN counts as larger
  * than any number, and so do a NaN logit's and, for softmax, a logit of +inf's,
  * which is NaN (among themselves they and keys past 2^1000 are equal).  A NaN
  * logit makes every weight that it enters NaN.

@@ -184,3 +184,21 @@ def test_refusals():
             pgg.moe_gate_grouped_grad(l, a, b)
     with pytest.raises(pgg.PggError):
         pgg.moe_gate_grouped_grad(l, ids, gp, out=torch.zeros((4, 15), device=DEV))
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,groups,kept,k", [(16, 4, 2, 5), (60, 4, 3, 8), (256, 8, 4, 8), (1100, 4, 2, 8)])
+def test_biases_without_bounds(E, groups, kept, k, score):
+    each = E // groups
+    for low in (-math.inf, float(torch.finfo(torch.float32).min)):
+        bias = torch.randn((E,), generator=torch.Generator().manual_seed(E)) * 0.1
+        bias[::3] = low                        # experts kept back here and there
+        bias[each:2 * each] = low              # a whole group
+        bias[2 * each:3 * each - 1] = low      # all but one of a group
+        bias[3 * each - 1] = 0.05
+        _check(_logits(9, E, "f32", 3), k, score=score, groups=groups, topk_groups=kept, bias=bias)
+    _check(_logits(3, E, "f32", 4), k, score=score, groups=groups, topk_groups=kept, bias=torch.full((E,), -math.inf))
+    high = torch.zeros(E)
+    high[each + 1] = math.inf
+    ids, _ = _check(_logits(3, E, "f32", 5), k, score=score, groups=groups, topk_groups=kept, bias=high)
+    assert bool((ids[:, 0] == each + 1).all())
