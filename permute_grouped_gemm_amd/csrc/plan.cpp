@@ -854,7 +854,9 @@ pgg_status make_w4_plan(const pgg_moe_w4_desc* d, bool gated, W4Plan* p) {
   q.off_ori = off;      off = align_up(off + (indexed ? sizeof(int32_t) * size_t(M) : 0), kRegionAlign);
   q.table_bytes = q.off_ring = off;
   if (w.ksplit > 1) off = align_up(off + size_t(w.ksplit) * size_t(M) * 64 * size_t(l.CB) * sizeof(float), kRegionAlign);
-  // x is read in chunks of 16 bytes: rows that end inside one are copied to longer ones
+  // x is read in chunks of 16 bytes: rows that end inside one are copied to longer
+  // ones.  (Read where they lie, at odd addresses, rows of 1403 f16 elements made a
+  // call of 36 us with its copy take 57.)
   const int64_t chunk = l.dtype == PGG_F32 ? 4 : 8;
   q.lda = l.K;
   q.off_pad_a = off;

@@ -212,3 +212,37 @@ def test_residual_stream_in_place(batch, H):
     again, normed_again = pgg.moe_combine(permuted, eri, probs, residual, out=residual, **kw)
     assert again.data_ptr() == residual.data_ptr()
     assert torch.equal(again, out) and torch.equal(normed_again, normed)
+
+
+def test_two_graphs_share_a_workspace():
+    # replays in any order on one stream: every call writes what it reads of it
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    rand = lambda *s: torch.randn(s, generator=gen, device=DEV)  # noqa: E731
+    K, N, gs, calls = 512, 128, 64, []
+    w = pgg.w4_pack(torch.randint(0, 16, (300, K, N), generator=gen, device=DEV, dtype=torch.uint8),
+                    (0.02 * torch.rand((300, K // gs, N), generator=gen, device=DEV)).bfloat16(), gs)
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device=DEV)
+    for tokens in (40, 500):
+        ids = torch.randint(0, 300, (tokens, 4), generator=gen, device=DEV)
+        counts, gather, scatter, _ = pgg.moe_routing(ids, 300)
+        x, probs, res = rand(tokens, K).bfloat16(), torch.rand((tokens, 4), device=DEV), rand(tokens, N).bfloat16()
+
+        def call(x=x, counts=counts, gather=gather, scatter=scatter, probs=probs, res=res):
+            y = pgg.moe_fwd_w4(x, w, gather, counts, 4, workspace=ws)
+            out = pgg.moe_combine(y, gather, probs, res, workspace=ws)
+            grads = pgg.moe_combine_grad(res, y, gather, probs, res, post_weight=res[0].contiguous(), workspace=ws)
+            return [y, out, grads[0], grads[1], grads[4]]
+
+        eager = [t.clone() for t in call()]
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            results = call()
+        calls.append((g, results, eager))
+    for order in ((0, 1), (1, 0), (1, 1), (0, 1)):
+        for i in order:
+            calls[i][0].replay()
+        torch.cuda.synchronize()
+        for _, results, eager in calls:
+            for a, b in zip(results, eager):
+                assert torch.equal(a, b)

@@ -81,3 +81,25 @@ def test_a_token_goes_to_one_expert_several_times():
         h = pgg.moe_glu_w4(x.to(DEV), _pack(*w, gs, True), eri.to(DEV), gl.to(DEV), topk, kind)
         want, bound = ref.w4_glu(x, *w, gs, gl, topk=topk, eri=eri, row_idx_type=kind)
         ops_ref.assert_within(h, want, bound, f"index {kind}")
+
+
+# every end of a row inside and beside 8 elements, alone and behind whole tiles
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("counts", [[3, 2], [20, 30], [90, 75]], ids=str)
+def test_every_end_of_a_row(counts, dtype):
+    for K in list(range(1, 20)) + list(range(121, 138)) + [1027, 1030]:
+        _check_fwd(counts, K, 33, 32 if K % 2 else 64, dtype, True, seed=K)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("K", [131, 260])
+def test_nan_in_the_rows_beside(K, dtype):
+    w = _pack(*_weights(1, K, 70, 64, dtype, True, 1), 64, False)
+    for rows in (9, 40, 100):
+        x, gl = _rows(rows, K, dtype, 2).to(DEV), torch.tensor([rows], device=DEV)
+        want = pgg.moe_fwd_w4(x, w, None, gl)
+        x[1::2] = float("nan")
+        y = pgg.moe_fwd_w4(x, w, None, gl)
+        assert bool(y[1::2].isnan().all())
+        # (computed again with code - zero: other roundings of the same sum)
+        assert torch.allclose(y[::2].float(), want[::2].float(), rtol=2.0 ** -7, atol=2.0 ** -9)
