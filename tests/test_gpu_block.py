@@ -238,11 +238,11 @@ def test_two_graphs_share_a_workspace():
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             results = call()
-        calls.append((g, results, eager))
+        calls.append((g, results, eager, call))   # (call holds what the graph reads)
     for order in ((0, 1), (1, 0), (1, 1), (0, 1)):
         for i in order:
             calls[i][0].replay()
         torch.cuda.synchronize()
-        for _, results, eager in calls:
+        for _, results, eager, _ in calls:
             for a, b in zip(results, eager):
                 assert torch.equal(a, b)
