@@ -103,3 +103,18 @@ def test_nan_in_the_rows_beside(K, dtype):
         assert bool(y[1::2].isnan().all())
         # (computed again with code - zero: other roundings of the same sum)
         assert torch.allclose(y[::2].float(), want[::2].float(), rtol=2.0 ** -7, atol=2.0 ** -9)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("K", [256, 200, 131])
+@pytest.mark.parametrize("shift", [1, 4, 8])
+def test_many_rows_at_any_address(shift, K, dtype):
+    # x, and the result, that start 2, 8 and 16 bytes behind a boundary
+    w = _weights(2, K, 96, 64, dtype, True, 7)
+    x, gl = _rows(300, K, dtype, 8), torch.tensor([180, 120])
+    flat = torch.empty(x.numel() + shift, dtype=x.dtype, device=DEV)
+    flat[shift:] = x.to(DEV).reshape(-1)
+    out = torch.empty(300 * 96 + shift, dtype=x.dtype, device=DEV)[shift:].reshape(300, 96)
+    y = pgg.moe_fwd_w4(flat[shift:].reshape(300, K), _pack(*w, 64, False), None, gl.to(DEV), out=out)
+    want, bound = ref.w4_fwd(x, *w, 64, gl)
+    ops_ref.assert_within(y, want, bound)
