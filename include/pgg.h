@@ -755,10 +755,11 @@ pgg_status pgg_moe_glu_w4(const pgg_moe_w4_desc* desc, const void* x, const void
  *   out       [batch, H]  dtype                  output
  *   normed    [batch, H]  dtype                  output, NULL exactly when next_weight is
  *
- * fp32 arithmetic; `normed` comes from the unrounded out; each output is rounded
- * once.  Sums run in a fixed order.  The routing index is checked on the device
- * (out of range / not a permutation: the workspace error word; outputs
- * unspecified).  `out` may be `residual`; no other output may alias an input.
+ * fp32 arithmetic, in which a row's sum of squares has to be finite; `normed` comes
+ * from the unrounded out; each output is rounded once.  Sums run in a fixed order.
+ * The routing index is checked on the device (out of range / not a permutation: the
+ * workspace error word; outputs unspecified).  `out` may be `residual`; no other
+ * output may alias an input.
  * Limits: hidden <= 16384, M < 2^31 - 1.  Alignment and workspace rules are
  * pgg_moe_unpermute's.
  */
@@ -779,7 +780,7 @@ pgg_status pgg_moe_combine(const pgg_moe_combine_desc* desc, const void* permute
 /*
  * Its gradient, from grad_out [batch, H] and, exactly when next_weight is given,
  * grad_normed [batch, H] (dtype); the inputs are the forward's, and what lies
- * between is computed again:
+ * between is computed again (fp32, in which a row's sums of products have to be finite):
  *
  *   grad_permuted    [M, H]         dtype      every row written
  *   grad_probs       [batch, topk]  float32
@@ -788,7 +789,8 @@ pgg_status pgg_moe_combine(const pgg_moe_combine_desc* desc, const void* permute
  *   grad_post_weight [H]            float32    NULL exactly when post_weight is
  *   grad_next_weight [H]            float32    NULL exactly when next_weight is
  *
- * Everything is added in a fixed order: repeated calls give the same bits.
+ * Everything is added in a fixed order: repeated calls give the same bits.  No
+ * output may alias an input.
  */
 typedef struct {
   const void* grad_out;

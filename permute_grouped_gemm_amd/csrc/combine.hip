@@ -7,12 +7,14 @@
 //   normed = out q w_next,  q = 1 / sqrt(mean(out^2) + eps)
 //
 // Gradient, from go = d/d out and gn = d/d normed, u = gn w_next:
-//   go    += q u - out q^3 mean(u out)                          (d/d out in all)
+//   go    += q (u - n mean(u n)),  n = out q                    (d/d out in all)
 //   residual: alpha go        w_next: sum_t gn out q
 //   s      = sum_h go w_post c                                  (w_post 1 without it)
 //   gate:  r s                w_post: sum_t g go c r
 //   gc     = g (r go w_post - c r^3 s / H)                      (or g go)
 //   y_j:   p_j gc             p_j: sum_h gc y_j
+// q stays with the row that it normalises: its cube leaves fp32's range for a
+// stream of 1e13 and more, and for rows near 0 under a small eps.
 //
 // Both are bound by reading and writing the rows once.  A workgroup takes a
 // token, a thread 8 successive elements of each of its rows (16 in the gradient,
@@ -120,6 +122,15 @@ __device__ __forceinline__ Eight<T> load8(const void* base, int64_t row, const P
     for (int k = 0; k < 8; ++k) e[k] = k < c.last ? p[k] : E(0);
     __builtin_memcpy(&r, e, sizeof(r));
   }
+  return r;
+}
+
+template <class T>
+__device__ __forceinline__ Eight<T> ones8() {
+  constexpr uint32_t one = __is_same(T, TF32) ? 0x3F800000u : __is_same(T, TBf16) ? 0x3F803F80u : 0x3C003C00u;
+  Eight<T> r;
+#pragma unroll
+  for (int h = 0; h < 8 / T::kPerChunk; ++h) r.v[h] = u32x4_t{one, one, one, one};
   return r;
 }
 
@@ -390,6 +401,10 @@ __global__ __launch_bounds__(kMaxThreads<NCH>) void combine_grad_kernel(CombineA
   // Long rows leave no registers for the weights' gradients, which then stay in
   // this workgroup's part in memory, nor for inputs that wait for their use.
   constexpr bool kLong = NCH > 2;
+  // A missing post_weight is 1 where registers hold it: with fewer branches the
+  // compiler spills fewer scalar registers (13824 x 8 x 7168, bf16: 821 us, and 872
+  // with branches).  In fp32 it would spill vector registers instead.
+  constexpr bool kOnes = !kLong && !__is_same(T, TF32);
   __shared__ union {
     struct {
       float one[1][kMaxWaves], two[2][kMaxWaves], three[1][kMaxWaves], slots[HELD][kMaxWaves];
@@ -410,6 +425,7 @@ __global__ __launch_bounds__(kMaxThreads<NCH>) void combine_grad_kernel(CombineA
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
       if (a.post) post_reg[i] = load8<T, ROWS>(a.post, 0, piece[i]);
+      else if (kOnes) post_reg[i] = ones8<T>();
       if (a.next) next_reg[i] = load8<T, ROWS>(a.next, 0, piece[i]);
 #pragma unroll
       for (int k = 0; k < 8; ++k) dpost[i][k] = dnext[i][k] = 0.0f;
@@ -485,7 +501,7 @@ __global__ __launch_bounds__(kMaxThreads<NCH>) void combine_grad_kernel(CombineA
       // out, from c
       auto out = [&](int i, float (&v)[8]) {
         const Eight<T> res = input(a.residual, res_reg[i], i);
-        if (a.post) {
+        if (kOnes || a.post) {
           const Eight<T> w = post(i);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
@@ -510,7 +526,7 @@ __global__ __launch_bounds__(kMaxThreads<NCH>) void combine_grad_kernel(CombineA
         }
       block_sum<2>(sum, s.sums.two);
       const float q = 1.0f / sqrtf(sum[0] * a.inv_h + a.eps);
-      const float back = q * q * q * (sum[1] * a.inv_h);
+      const float back = q * (q * (sum[1] * a.inv_h));   // q mean(u n)
 #pragma unroll
       for (int i = 0; i < NCH; ++i)
         if (piece[i].last > 0) {
@@ -519,8 +535,9 @@ __global__ __launch_bounds__(kMaxThreads<NCH>) void combine_grad_kernel(CombineA
           const Eight<T> gn = input(a.grad_normed, gn_reg[i], i), w = next(i);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            d[k] = get<T>(gn, k) * (v[k] * q);
-            go[i][k] += q * (get<T>(gn, k) * get<T>(w, k)) - v[k] * back;
+            const float n = v[k] * q;
+            d[k] = get<T>(gn, k) * n;
+            go[i][k] += q * (get<T>(gn, k) * get<T>(w, k)) - n * back;
           }
           add_weight(a.part_next, dnext, t, i, d);
         }
@@ -532,7 +549,7 @@ __global__ __launch_bounds__(kMaxThreads<NCH>) void combine_grad_kernel(CombineA
         float v[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = a.alpha * go[i][k];
-        if (a.post) {
+        if (kOnes || a.post) {
           const Eight<T> w = post(i);
 #pragma unroll
           for (int k = 0; k < 8; ++k) add<ROWS>(piece[i], k, go[i][k] * get<T>(w, k), c[i][k], dot);
@@ -543,7 +560,7 @@ __global__ __launch_bounds__(kMaxThreads<NCH>) void combine_grad_kernel(CombineA
         store8<T, ROWS, true>(a.grad_residual, t * a.H, piece[i], v);
       }
     float total[1] = {dot};
-    if (a.post || a.gate) block_sum<1>(total, s.sums.three);
+    block_sum<1>(total, s.sums.three);   // (its barrier also parts the sums of successive tokens)
     if (a.gate && threadIdx.x == 0) a.grad_gate[t] = r * total[0];
     const float back = gate * (r * r * r) * (total[0] * a.inv_h);
 #pragma unroll
@@ -600,8 +617,6 @@ __global__ __launch_bounds__(kMaxThreads<NCH>) void combine_grad_kernel(CombineA
       }
       if (ONCE) break;
     }
-    // the next token writes these words after one more barrier, or after this one
-    if (!a.post && !a.gate && !a.next) __syncthreads();
   }
   if constexpr (!kLong) {
 #pragma unroll
