@@ -9,12 +9,12 @@
 // Gradient, from go = d/d out and gn = d/d normed, u = gn w_next:
 //   go    += q (u - n mean(u n)),  n = out q                    (d/d out in all)
 //   residual: alpha go        w_next: sum_t gn out q
-//   s      = sum_h go w_post c                                  (w_post 1 without it)
-//   gate:  r s                w_post: sum_t g go c r
-//   gc     = g (r go w_post - c r^3 s / H)                      (or g go)
+//   m      = c r, s = sum_h go w_post m                         (r and w_post 1 without it)
+//   gate:  s                  w_post: sum_t g go m
+//   gc     = g r (go w_post - m s / H)                          (or g go)
 //   y_j:   p_j gc             p_j: sum_h gc y_j
-// q stays with the row that it normalises: its cube leaves fp32's range for a
-// stream of 1e13 and more, and for rows near 0 under a small eps.
+// q and r stay with the rows that they normalise: their cubes leave fp32's range
+// for rows of 1e13 and more, and for rows near 0 under a small eps.
 //
 // Both are bound by reading and writing the rows once.  A workgroup takes a
 // token, a thread 8 successive elements of each of its rows (16 in the gradient,
@@ -490,6 +490,10 @@ __global__ __launch_bounds__(kMaxThreads<NCH>) void combine_grad_kernel(CombineA
           for (int k = 0; k < 8; ++k) add<ROWS>(piece[i], k, c[i][k], c[i][k], sum[0]);
       block_sum<1>(sum, s.sums.one);
       r = 1.0f / sqrtf(sum[0] * a.inv_h + a.eps);
+#pragma unroll
+      for (int i = 0; i < NCH; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) c[i][k] *= r;   // c is m from here on
     }
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
@@ -498,14 +502,14 @@ __global__ __launch_bounds__(kMaxThreads<NCH>) void combine_grad_kernel(CombineA
       for (int k = 0; k < 8; ++k) go[i][k] = get<T>(raw, k);
     }
     if (a.next) {
-      // out, from c
+      // out, from m
       auto out = [&](int i, float (&v)[8]) {
         const Eight<T> res = input(a.residual, res_reg[i], i);
         if (kOnes || a.post) {
           const Eight<T> w = post(i);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            v[k] = __builtin_fmaf(a.alpha, get<T>(res, k), gate * (c[i][k] * r * get<T>(w, k)));
+            v[k] = __builtin_fmaf(a.alpha, get<T>(res, k), gate * (c[i][k] * get<T>(w, k)));
         } else {
 #pragma unroll
           for (int k = 0; k < 8; ++k) v[k] = __builtin_fmaf(a.alpha, get<T>(res, k), gate * c[i][k]);
@@ -542,7 +546,7 @@ __global__ __launch_bounds__(kMaxThreads<NCH>) void combine_grad_kernel(CombineA
           add_weight(a.part_next, dnext, t, i, d);
         }
     }
-    float dot = 0.0f;   // sum go w_post c
+    float dot = 0.0f;   // sum go w_post m
 #pragma unroll
     for (int i = 0; i < NCH; ++i)
       if (piece[i].last > 0) {
@@ -561,8 +565,8 @@ __global__ __launch_bounds__(kMaxThreads<NCH>) void combine_grad_kernel(CombineA
       }
     float total[1] = {dot};
     block_sum<1>(total, s.sums.three);   // (its barrier also parts the sums of successive tokens)
-    if (a.gate && threadIdx.x == 0) a.grad_gate[t] = r * total[0];
-    const float back = gate * (r * r * r) * (total[0] * a.inv_h);
+    if (a.gate && threadIdx.x == 0) a.grad_gate[t] = total[0];
+    const float back = gate * (r * (total[0] * a.inv_h));
 #pragma unroll
     for (int i = 0; i < NCH; ++i)
       if (piece[i].last > 0) {
@@ -571,7 +575,7 @@ __global__ __launch_bounds__(kMaxThreads<NCH>) void combine_grad_kernel(CombineA
           float d[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            d[k] = gate * go[i][k] * (c[i][k] * r);
+            d[k] = gate * go[i][k] * c[i][k];
             go[i][k] = (gate * r) * (go[i][k] * get<T>(w, k)) - c[i][k] * back;
           }
           add_weight(a.part_post, dpost, t, i, d);

@@ -1,4 +1,4 @@
-"""The combination and its gradient at the ends of fp32's range: streams
+"""The combination and its gradient at the ends of fp32's range: sums and streams
 whose norms' factors cubed are no fp32 numbers, and rows of zeros under a small eps
 (needs an MI355X)."""
 import pytest
@@ -42,6 +42,14 @@ def _sized(shape, dtype, post, gate, nxt, rms):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
 @pytest.mark.parametrize("rms,eps", [(1e10, 1e-6), (1e15, 1e-6), (1e17, 1e-5), (1e-14, 0.0), (1e-12, 1e-30)])
+def test_size_of_the_sum(rms, eps, shape, dtype):
+    _compare(_sized(shape, dtype, True, True, False, rms), eps)
+    _compare(_sized(shape, dtype, True, False, False, rms), eps, rit=0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("rms,eps", [(1e10, 1e-6), (1e15, 1e-6), (1e17, 1e-5), (1e-14, 0.0), (1e-12, 1e-30)])
 def test_size_of_the_stream(rms, eps, shape, dtype):
     _compare(_sized(shape, dtype, False, False, True, rms), eps)
     _compare(_sized(shape, dtype, False, True, True, rms), eps, rit=0)
@@ -49,9 +57,18 @@ def test_size_of_the_stream(rms, eps, shape, dtype):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
-@pytest.mark.parametrize("eps", [1e-30, 1e-36])
-def test_rows_of_zeros_under_a_small_eps(eps, shape, dtype):
-    s = _inputs(*shape, dtype, False, True, True, seed=1)
+@pytest.mark.parametrize("rms,eps", [(1e15, 1e-6), (1e-14, 0.0)])
+def test_size_of_both(rms, eps, shape, dtype):
+    _compare(_sized(shape, dtype, True, True, True, rms), eps)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("post,nxt,eps", [(True, False, 1e-30), (True, False, 1e-36), (False, True, 1e-30),
+                                          (False, True, 1e-36), (True, True, 1e-30)])
+def test_rows_of_zeros_under_a_small_eps(post, nxt, eps, shape, dtype):
+    # (1 / sqrt(eps) twice, with both norms, is 1e30)
+    s = _inputs(*shape, dtype, post, True, nxt, seed=1)
     at = ref.slots(s["eri"], shape[0], shape[1], 1)
     s["permuted"][at[0]] = 0
     s["residual"][0] = 0
