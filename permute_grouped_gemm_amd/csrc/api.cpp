@@ -715,12 +715,10 @@ pgg_status pgg_w4_pack(const pgg_w4_desc* desc, const uint8_t* codes, const void
 
 pgg_status pgg_moe_w4_workspace_size(const pgg_moe_w4_desc* desc, size_t* bytes) {
   if (!desc || !bytes) return PGG_ERR_INVALID_ARG;
-  W4Plan p, other;   // enough for x at any address
-  const pgg_status st = make_w4_plan(desc, desc->weight.gated != 0, true, &p);
+  W4Plan p;
+  const pgg_status st = make_w4_plan(desc, desc->weight.gated != 0, &p);
   if (st != PGG_OK) return st;
   *bytes = p.base.total;
-  if (make_w4_plan(desc, desc->weight.gated != 0, false, &other) == PGG_OK && other.base.total > *bytes)
-    *bytes = other.base.total;
   return PGG_OK;
 }
 
@@ -728,7 +726,7 @@ static pgg_status run_w4(const pgg_moe_w4_desc* desc, bool gated, const void* x,
                          const int64_t* eri, const int64_t* group_list, void* out, void* workspace,
                          size_t workspace_bytes, hipStream_t stream) {
   W4Plan p;
-  const pgg_status st = make_w4_plan(desc, gated, is_aligned(x, 16), &p);
+  const pgg_status st = make_w4_plan(desc, gated, &p);
   if (st != PGG_OK) return st;
   if (!x || !packed || !group_list || !out || !workspace || (eri != nullptr) != (desc->idx_len != 0))
     return PGG_ERR_INVALID_ARG;

@@ -255,8 +255,7 @@ struct W4Plan {
   bool tiles;              // many rows per expert: tiles of 64 rows x 256 columns
   size_t off_sums;         // and the sums of x over the scale groups for them
 };
-// aligned: x starts on a 16-byte boundary
-pgg_status make_w4_plan(const pgg_moe_w4_desc* desc, bool gated, bool aligned, W4Plan* plan);
+pgg_status make_w4_plan(const pgg_moe_w4_desc* desc, bool gated, W4Plan* plan);
 hipError_t launch_w4(const W4Plan& p, int32_t act, const void* x, const void* packed, const int64_t* eri,
                      const int64_t* group_list, void* out, void* ws, hipStream_t s);
 

@@ -778,7 +778,7 @@ pgg_status make_w4_layout(const pgg_w4_desc* d, W4Layout* l) {
   return PGG_OK;
 }
 
-pgg_status make_w4_plan(const pgg_moe_w4_desc* d, bool gated, bool aligned, W4Plan* p) {
+pgg_status make_w4_plan(const pgg_moe_w4_desc* d, bool gated, W4Plan* p) {
   if (!d || !p) return PGG_ERR_INVALID_ARG;
   W4Plan w{};
   const pgg_status st = make_w4_layout(&d->weight, &w.layout);
@@ -807,9 +807,8 @@ pgg_status make_w4_plan(const pgg_moe_w4_desc* d, bool gated, bool aligned, W4Pl
   //   bf16, 7168 x 4096: 8 rows per expert 53, 60, 70; 16 62, 66, 69; 24 106, 73, 70;
   //     32 110, 82, 84; 48 161, 142, 85; 64 202, 150, 87; 1024 3258, 2268, 945
   //   f16, 1403 x 2039, groups of 64: 8 15, 23, 33; 32 28, 23, 35; 64 48, 39, 40; 128 86, 66, 41
-  // (They address x with 32-bit byte offsets, padded rows included, and read whole
-  // pieces of 16 bytes on such boundaries.)
-  w.tiles = l.dtype != PGG_F32 && M > 32 * l.G && !(indexed && d->batch <= 32) && (aligned || l.K % 8 != 0) &&
+  // (They address x with 32-bit byte offsets, padded rows included.)
+  w.tiles = l.dtype != PGG_F32 && M > 32 * l.G && !(indexed && d->batch <= 32) &&
             d->batch < ((int64_t(1) << 31) - 64) / 2 / (l.K + 64);
   q.bm = w.tiles ? 64 : l.dtype == PGG_F32 || M <= 12 * l.G || (indexed && d->batch <= 16) ? 16 : 32;
   const int64_t max_tiles = std::min<int64_t>(M, (M + q.bm - 1) / q.bm + l.G);   // each holds a row at least

@@ -10,10 +10,14 @@
 // one stage ahead.  The sums of x over the scale groups, by which the zero points
 // are multiplied, are computed once per row of x by a kernel before; a group's
 // product starts from -zero times that sum as the instruction's third operand.
+// x on no 16-byte boundary, which the direct loads need, goes through registers: loaded
+// a stage ahead, and stored when the stage before has been multiplied.
 //
 // Measured: 2048 tokens to 8 of 16 experts each (16384 rows), 7168 x 4096 with gate,
-// groups of 128, zero points, bf16: 1.0 ms, 0.96 PFLOP/s (a library product of 8192^3
-// on this card: 1.19).  The matrix instructions are busy 45 % of the time; copies of the kernel without
+// groups of 128, zero points, bf16: 0.98 to 1.05 ms on several cards, 0.92 to 0.98
+// PFLOP/s (a library product of 8192^3: 1.19).  1024 rows to each of 16 experts,
+// 7168 x 4096 without gate: 0.99 ms, 1.16 with x at an odd address (6.67 in the tiles
+// of few rows).  The matrix instructions are busy 45 % of the time; copies of the kernel without
 // its loads took 0.81 ms, without the scales' multiply-adds 0.85.  Not faster: codes
 // with the non-temporal hint (1.06, the tiles of an expert share them), reading the
 // operands of the next 32 k ahead, tiles of 2 x 16, 4 x 8 or 16 x 4 for the order of
@@ -28,7 +32,7 @@ namespace {
 
 constexpr int kTileRows = 64, kTileStage = kTileRows * 256;
 
-template <class T, int SUB, bool ZEROS>
+template <class T, int SUB, bool ZEROS, bool ALIGNED>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void w4_tile_kernel(W4Args a) {
   using E = typename T::elem;
@@ -65,16 +69,20 @@ void w4_tile_kernel(W4Args a) {
   const float* psum = a.sums + static_cast<int64_t>(s_rows[lane]) * (a.KB * SUB);
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(lds));
   const uint32_t sum0 = __builtin_amdgcn_readfirstlane(lds_offset(s_sum));
+  u32x4_t held[4];   // x on no 16-byte boundary: the same pieces through registers
   auto load_x = [&](int kb) {
     const uint32_t m0 = lds0 + (kb & 1) * kTileStage + wave * 4096;
     const char* p = static_cast<const char*>(a.x) + static_cast<int64_t>(kb) * (2 * kW4K);
     const int64_t left = a.K - static_cast<int64_t>(kb) * kW4K;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      if (left >= kW4K) {
+      if constexpr (!ALIGNED) {
+        const int chunk = lr ^ (4 * q + lg);   // 16 wave is a multiple of 16
+        held[q] = load16(8 * chunk < left ? p + ox[q] : reinterpret_cast<const char*>(&kZero16));
+      } else if (left >= kW4K) {
         dma16_off(p, ox[q], m0 + q * 1024);
       } else {
-        const int chunk = lr ^ (4 * q + lg);   // 16 wave is a multiple of 16
+        const int chunk = lr ^ (4 * q + lg);
         dma16(8 * chunk < left ? static_cast<const void*>(p + ox[q]) : static_cast<const void*>(&kZero16),
               m0 + q * 1024);
       }
@@ -84,6 +92,13 @@ void w4_tile_kernel(W4Args a) {
       for (int u = 0; u < SUB; ++u)
         dma4(psum + kb * SUB + u, sum0 + ((kb & 1) * SUB + u) * kTileRows * 4);
     }
+  };
+
+  // these into their stage, which all waves have read before the last barrier
+  auto store_x = [&](int kb) {
+    if constexpr (!ALIGNED)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) lds[(kb & 1) * (kTileStage / 16) + wave * 256 + q * 64 + lane] = held[q];
   };
 
   f32x4_t acc[RB][4];
@@ -135,6 +150,7 @@ void w4_tile_kernel(W4Args a) {
 
   W4Weights<T, SUB> w[2];
   load_x(kb0);
+  store_x(kb0);
   w[0].load_there(planes, static_cast<uint32_t>(kb0) * a.CB, lane);
   for (int kb = kb0; kb < kb1; kb += 2) {
 #pragma unroll
@@ -145,6 +161,7 @@ void w4_tile_kernel(W4Args a) {
         if (kb + h + 1 < kb1) load_x(kb + h + 1);
         w[1 - h].load_there(planes, static_cast<uint32_t>(min(kb + h + 1, kb1 - 1)) * a.CB, lane);   // past the end: unused
         multiply(w[h], (kb + h) & 1);
+        if (kb + h + 1 < kb1) store_x(kb + h + 1);
       }
   }
   fetched_barrier<0>();
@@ -200,8 +217,11 @@ __global__ __launch_bounds__(256) void w4_sums_kernel(const void* x, float* sums
 template <class T, int SUB>
 hipError_t launch_sub(const W4Args& a, hipStream_t s) {
   const dim3 grid(tile_blocks(a), static_cast<unsigned>(a.ksplit));
-  if (a.zeros) hipLaunchKernelGGL((w4_tile_kernel<T, SUB, true>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((w4_tile_kernel<T, SUB, false>), grid, dim3(256), 0, s, a);
+  const bool aligned = reinterpret_cast<uintptr_t>(a.x) % 16 == 0;
+  if (a.zeros && aligned) hipLaunchKernelGGL((w4_tile_kernel<T, SUB, true, true>), grid, dim3(256), 0, s, a);
+  else if (a.zeros) hipLaunchKernelGGL((w4_tile_kernel<T, SUB, true, false>), grid, dim3(256), 0, s, a);
+  else if (aligned) hipLaunchKernelGGL((w4_tile_kernel<T, SUB, false, true>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((w4_tile_kernel<T, SUB, false, false>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
