@@ -807,8 +807,18 @@ pgg_status make_w4_plan(const pgg_moe_w4_desc* d, bool gated, W4Plan* p) {
   //   bf16, 7168 x 4096: 8 rows per expert 53, 60, 70; 16 62, 66, 69; 24 106, 73, 70;
   //     32 110, 82, 84; 48 161, 142, 85; 64 202, 150, 87; 1024 3258, 2268, 945
   //   f16, 1403 x 2039, groups of 64: 8 15, 23, 33; 32 28, 23, 35; 64 48, 39, 40; 128 86, 66, 41
+  // How the rows are spread the host does not know, so the rule goes by their average
+  // over all experts.  From 24 the 64 x 256 tiles lose little where experts are alike
+  // and win where few have the rows, if the call is large: tiles of 32 rows would be
+  // two workgroups to a compute unit (with an index, whose tables the large tiles
+  // need, three).  Tiles of 32 and of 64 rows at 24 on average: experts drawn alike,
+  // by a popularity of 1 / rank^1.1, and all rows on 2 experts:
+  //   16, bf16, 7168 x 4096: 73 67, 92 101, 73 68;  64, 2048 x 2816: 75 59, 79 69, 67 42
+  //   64, f16, 1403 x 2039: 64 41, 63 57, 43 38
+  //   and of small matrices, 8, bf16, 1408 x 2048: 14 24, 14 25;  16, 512 x 512: 11 17, 11 18
   // (They address x with 32-bit byte offsets, padded rows included.)
-  w.tiles = l.dtype != PGG_F32 && M > 32 * l.G && !(indexed && d->batch <= 32) &&
+  const bool large = (M + 31) / 32 * l.CB >= (indexed ? 768 : 512);
+  w.tiles = l.dtype != PGG_F32 && (M > 32 * l.G || (large && M >= 24 * l.G)) && !(indexed && d->batch <= 32) &&
             d->batch < ((int64_t(1) << 31) - 64) / 2 / (l.K + 64);
   q.bm = w.tiles ? 64 : l.dtype == PGG_F32 || M <= 12 * l.G || (indexed && d->batch <= 16) ? 16 : 32;
   const int64_t max_tiles = std::min<int64_t>(M, (M + q.bm - 1) / q.bm + l.G);   // each holds a row at least

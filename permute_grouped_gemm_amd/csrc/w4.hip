@@ -14,7 +14,9 @@
 // of that size 152 us, 6.4 TB/s of codes and scales.  The codes carry the
 // non-temporal hint: with 8 layers' weights in turn the 12 experts take 38.9 us with
 // it and 41.7 without (one layer again and again, which a model does not do, 38.7 and
-// 34.1: it fits the last cache).
+// 34.1: it fits the last cache).  Where few experts have all rows, whose codes several
+// tiles read, it costs instead: 4 layers in turn, 16 experts, rows on all of them 46.4
+// and 50.2, on 2 26.6 and 24.1; 64 experts of 2048 x 2816, 37.4 and 41.3, 30.6 and 26.7.
 #include <algorithm>
 
 #include "pgg_w4.h"
