@@ -1303,7 +1303,7 @@ def moe_combine(permuted: torch.Tensor, expanded_row_idx: torch.Tensor, probs: t
     permuted [batch*topk, H], residual [batch, H], post_weight and next_weight [H]
     share one of float32 / float16 / bfloat16; probs [batch, topk] and gate
     [batch] are float32; expanded_row_idx [batch*topk] int64 as for
-    moe_unpermute (row_idx_type 1 needs one launch less).  Returns out, with
+    moe_unpermute (a long one takes a second launch).  Returns out, with
     next_weight (out, normed).  H <= 16384."""
     d = _combine_desc(permuted, probs, row_idx_type, residual_scale, eps)
     _check_combine(d, permuted, expanded_row_idx, residual, post_weight, gate, next_weight)

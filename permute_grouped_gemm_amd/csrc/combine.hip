@@ -706,8 +706,15 @@ hipError_t launch_any(const CombinePlan& p, CombineArgs& a, const int64_t* eri, 
   // a spare workgroup with a bit per row, 16 entries to a thread at most
   const int64_t threads = p.threads(grad);
   // Short indexes of positions are searched by every token's workgroup, which saves
-  // the launch that inverts them.
-  a.scan = p.row_idx_type == 0 && p.M <= std::min<int64_t>(kBitRows, 8 * threads) && p.topk <= kScanSlots;
+  // the launch that inverts them: up to 8 entries to a thread, and batch * M entries
+  // in all, 16 MB from the caches (gradient, which reads more beside them, 8).
+  // Searched and inverted in us, in a graph, bf16, topk x M, forward and gradient:
+  //   H 7168: 1 x 512 10.2 11.8, 26.6 28.0; 1 x 1024 24.7 25.5, 39.4 39.2; 1 x 2048 47.1 45.2, 67.9 62.8;
+  //     1 x 7168 170 141, -; 8 x 2048 9.2 10.7, 25.9 26.5; 8 x 4096 16.3 18.5, 43.7 40.4; 8 x 7168 35.6 32.1, -
+  //   H 2048: 1 x 512 5.8 7.1, 15.2 16.6; 1 x 1024 7.8 8.8, 22.3 22.7; 2 x 2048 9.5 10.5, 24.9 23.4
+  //   H 64: 1 x 512 5.2 5.9, 9.9 10.6; 1 x 1024 6.6 6.1, 12.1 11.7 (8 entries to a thread are 512)
+  a.scan = p.row_idx_type == 0 && p.M <= std::min<int64_t>(kBitRows, 8 * threads) && p.topk <= kScanSlots &&
+           p.batch * p.M <= (grad ? 1 << 20 : 1 << 21);
   a.bits = a.scan || (p.row_idx_type == 1 && p.M <= std::min<int64_t>(kBitRows, 16 * threads));
   a.check = a.bits ? 1 : static_cast<int32_t>(std::min<int64_t>((p.M + 4 * threads - 1) / (4 * threads), 1024));
   hipError_t e = hipSuccess;
