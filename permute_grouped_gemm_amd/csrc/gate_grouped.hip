@@ -170,9 +170,10 @@ __device__ __forceinline__ double reciprocal(double v) {
   return __builtin_fma(__builtin_fma(-v, r, 1.0), r, r);
 }
 
-// exp(v) for v <= 0, to 2^-46 of itself, more than a key keeps: v = n ln 2 + r with
-// |r| <= ln 2 / 2, the Taylor polynomial of degree 11 at r (the first term left out
-// is 2^-47), times 2^n.  Below -800 as at -800, which is 0; NaN likewise.
+// exp(v) for v <= 0, to 2^-44 of itself, more than a key keeps (2^-46 down to v = -100):
+// v = n ln 2 + r with |r| <= ln 2 / 2, the Taylor polynomial of degree 11 at r (the
+// first term left out is 2^-47), times 2^n; ln 2 as one double is off by 2^-55, n
+// times.  Below -800 as at -800, which is 0; NaN likewise.
 __device__ __forceinline__ double exp_negative(double v) {
   v = max64(v, -800.0);
   const double n = __builtin_rint(v * 1.4426950408889634);
