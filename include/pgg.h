@@ -714,7 +714,7 @@ pgg_status pgg_w4_pack(const pgg_w4_desc* desc, const uint8_t* codes, const void
  * matrix.  x and the result are the weights' dtype.  Codes and zero points are
  * multiplied exactly, as integers, and a group's sum is scaled and added in
  * fp32; the result is rounded once.  (A group's sum of (code - zero) * x has to
- * be finite in fp32.)
+ * be finite in fp32; of fp32 x, bits below 2^-133 do not count.)
  * The workspace holds the tables and, where the reduction is split, fp32
  * partial results; where the rows of x are not whole pieces of 16 bytes, a copy of
  * them with padded rows, and for many rows the rows' sums over the scales' groups.

@@ -22,7 +22,7 @@
 // and stay in registers from the first use to the last; only the sums over h go
 // through LDS.  The forward's loads and stores carry the non-temporal hint
 // (110592 x 7168, f16: 374 us, 5.8 TB/s, and 427 without it; the gradient, bf16,
-// takes 845 us without, 4.7 TB/s, and 915 with it).  In the gradient a workgroup goes
+// takes 822 us without, 4.8 TB/s, and 887 with it).  In the gradient a workgroup goes
 // through tokens in steps of the grid and keeps its part of the weights' gradients
 // in registers (of long rows in memory); a second kernel adds the workgroups' parts.
 //

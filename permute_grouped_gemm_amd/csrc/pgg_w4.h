@@ -16,7 +16,8 @@
 // A result that is not finite (an infinity or NaN in x or in a scale, or an
 // overflow) is computed again with code - zero multiplied directly, so that an
 // infinity times a weight of one sign stays an infinity.
-// x in fp32 is cut into three bf16 parts, 8 bits of the 24 each, which are exact.
+// x in fp32 is cut into three bf16 parts, 8 bits of the 24 each, which are exact but
+// for bits below 2^-133, bf16's smallest number (|x| below 2^-110 has such).
 //
 // Layout.  Tiles of 128 k x 64 columns, [G][KB][CB][4 blocks][64 lanes][16 bytes]:
 // lane l of block j holds column column_of(l % 16, j) of the tile, and its word s

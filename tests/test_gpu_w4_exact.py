@@ -67,6 +67,20 @@ def test_one_weight_to_a_column(counts, K, dtype):
         assert torch.equal(y, want.to(T)), gs
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [3, 40])
+def test_small_fp32_x(rows):
+    # all 24 bits down to 2^-90; under that what lies below 2^-133 is cut off
+    K, scale = 128, 2.0 ** 60
+    w = _pack(torch.eye(K, dtype=torch.uint8)[None], torch.full((1, 1, K), scale),
+              torch.zeros((1, 1, K), dtype=torch.uint8), 128, False)
+    for e in (90, 112, 124, 132):
+        x = (torch.randn((rows, K), generator=torch.Generator().manual_seed(e), dtype=torch.float64) * 2.0 ** -e).float()
+        y = pgg.moe_fwd_w4(x.to(DEV), w, None, torch.tensor([rows], device=DEV)).cpu().double()
+        cut = torch.where(x.abs() < 2.0 ** -110, 2.0 ** -133, 0.0).double() * scale
+        assert bool(((y - x.double() * scale).abs() <= cut).all()), e
+
+
 def _chained(x, codes, scales, z, gs, gl):
     """w4_fwd with the bound of the chain that the kernels add in: a group's products
     (fp32 x in three parts), the groups of a wave, and 16 for waves, splits and the
